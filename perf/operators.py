@@ -180,8 +180,9 @@ def _pow2(e):
 
 def _save(x):
     """E4M3 values of x / 2^e and the biased exponents e + 127 for each 32 columns of a row:
-    2^e is the smallest power of two, not below 2^-124, with max|x| / 2^e <= 448. A block with a
-    value that is not finite has exponent 255 and NaN values."""
+    2^e is the smallest power of two, not below 2^-124, with max|x| / 2^e <= 448 (at e = 120 the
+    values stop at 240, or 256 2^120 would leave bf16). A block with a value that is not finite
+    has exponent 255 and NaN values."""
     M, K = x.shape
     xb = x.float().reshape(M, K // 32, 32)
     amax = xb.abs().amax(-1)
@@ -191,6 +192,7 @@ def _save(x):
     bad = ~torch.isfinite(amax)
     e = torch.where(bad, torch.zeros_like(e), e)
     v = xb * _pow2(-e).unsqueeze(-1)
+    v = torch.where(e.unsqueeze(-1) == 120, v.clamp(-240, 240), v)
     v = torch.where(bad.unsqueeze(-1), torch.full_like(v, math.nan), v)
     scale = torch.where(bad, torch.full_like(e, 255), e + 127).to(torch.uint8)
     return v.to(torch.float8_e4m3fn).reshape(M, K), scale
@@ -336,7 +338,8 @@ def _checkpoint64(x):
     low = torch.where((v.abs() < _two_to(low)) & (low > -6), low - 1, low)
     step = _two_to(low - 3)
     v = torch.round(v / step) * step
-    return v, e
+    top = torch.where(e == 120, 240.0, 448.0).repeat_interleave(32, dim=1)
+    return torch.minimum(torch.maximum(v, -top), top), e
 
 
 def exact(case, seed):
