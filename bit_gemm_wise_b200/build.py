@@ -30,6 +30,8 @@ SOURCES = {
     "w4a8_gemm.cu": [],
     "w4_moe.cu": [],
     "w4_nf4.cu": [],
+    "w4_gated.cu": [],
+    "fp8_ckpt.cu": [],
 }
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

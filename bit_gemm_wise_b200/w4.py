@@ -18,6 +18,7 @@ W4_OK = 0
 W4_SYM, W4_ASYM = 0, 1
 W4_LAYOUT_GEMV, W4_LAYOUT_GEMM, W4_LAYOUT_TC = 0, 1, 2
 W4_OUT_FP32, W4_OVERLAP_PREVIOUS = 1, 2  # flags of w4a16_gemv
+W4_ACT_SILU, W4_ACT_GELU_TANH = 0, 1
 
 STATUS = {
     0: "W4_OK", 1: "W4_ERR_NULL", 2: "W4_ERR_SHAPE", 3: "W4_ERR_GROUP", 4: "W4_ERR_ALIGN",
@@ -64,6 +65,17 @@ SIGNATURES = [
     ("w4a8_gemm_rowquant_layout", _I, [_I64, _I64, _I64, _I, _P]),
     ("w4a8_gemm_rowquant", _I, [_P, _I64, _P, _I64, _I64, _I, _I, _P, _I, _P, _SZ, _P]),
     ("w4a8_grouped_gemm", _I, [_P, _P, _P, _P, _P, _I, _I64, _P, _I64, _I64, _I, _I, _P, _P]),
+    ("w4a16_gated_workspace_bytes", _SZ, [_I64, _I64, _I64, _I]),
+    ("w4a16_gated", _I, [_P, _I64, _P, _P, _P, _P, _P, _P, _I64, _I64, _I, _I, _I, _P, _P, _SZ, _P]),
+    ("w4a16_gated_bwd_workspace_bytes", _SZ, [_I64, _I64, _I64, _I, _I]),
+    ("w4a16_gated_bwd", _I, [_P, _P, _P, _P, _I64, _P, _P, _P, _P, _P, _P, _I64, _I64, _I, _I, _I, _P, _P, _P,
+                             _P, _SZ, _P]),
+    ("w4a16_dgrad_workspace_bytes", _SZ, [_I64, _I64, _I64, _I]),
+    ("w4a16_dgrad", _I, [_P, _I64, _P, _P, _P, _I64, _I64, _I, _I, _P, _P, _SZ, _P]),
+    ("fp8_ckpt_save", _I, [_P, _I64, _I64, _P, _P, _P]),
+    ("fp8_ckpt_load", _I, [_P, _P, _I64, _I64, _P, _P]),
+    ("fp8_ckpt_wgrad_workspace_bytes", _SZ, [_I64, _I64, _I64]),
+    ("fp8_ckpt_wgrad", _I, [_P, _P, _P, _I64, _I64, _I64, _P, _I, _P, _SZ, _P]),
     ("w4_device_status", _I, [_P, ctypes.POINTER(ctypes.c_int)]),
     ("w4_selftest_bounded_wait", _I, [_I64, _P]),
 ]
@@ -357,6 +369,138 @@ def w4a8_grouped_gemm(X8, row_scale, gsum_op, expert_row_offsets, E, M_total, pa
     _check("w4a8_grouped_gemm", rc)
 
 
+def _act(act) -> int:
+    if act in ("silu", W4_ACT_SILU):
+        return W4_ACT_SILU
+    if act in ("gelu_tanh", W4_ACT_GELU_TANH):
+        return W4_ACT_GELU_TANH
+    return int(act)
+
+
+def _buf(name, t, need):
+    """Pointer of a contiguous CUDA tensor that must hold `need` bytes; None stays None. The C
+    entry points take bare pointers, so a tensor of the wrong size is caught here."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.numel() * t.element_size() < need:
+        raise ValueError(f"{name} holds {t.numel() * t.element_size()} bytes, {need} are needed")
+    return t.data_ptr()
+
+
+def _weight4(name, w, N, K, group):
+    """Pointers of a canonical weight (codes, scales, zeros or None) of W[N, K]."""
+    codes, scales, zeros = w
+    if group not in (32, 64, 128, 256) or N < 1 or K < 1:
+        J = 0  # refused by the C entry point
+    else:
+        J = N * (K // group) * 2
+    return (_buf(name + " codes", codes, N * K // 2), _buf(name + " scales", scales, J),
+            _buf(name + " zeros", zeros, J))
+
+
+def _ws(workspace):
+    if workspace is None:
+        return None, 0
+    return _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
+def _check_device(first, *rest):
+    for t in rest:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}: one device is wanted")
+
+
+def w4a16_gated_workspace_bytes(M, H, K, group) -> int:
+    return int(lib().w4a16_gated_workspace_bytes(M, H, K, group))
+
+
+def w4a16_gated(X, M, gate, up, H, K, group, mode, act, Y, workspace=None, stream=None):
+    """Y = act(X Wg^T) * (X Wu^T). gate, up: (codes, scales, zeros) as w4_quantize writes them
+    (zeros None for symmetric weights); act: "silu" or "gelu_tanh"; workspace:
+    alloc_gated_workspace(M, H, K, group). Runs on X's device."""
+    x, y = _buf("X", X, 2 * M * K), _buf("Y", Y, 2 * M * H)
+    g, u = _weight4("gate", gate, H, K, group), _weight4("up", up, H, K, group)
+    _check_device(X, Y, workspace, *gate, *up)
+    ws, n = _ws(workspace)
+    with torch.cuda.device(X.device):
+        rc = lib().w4a16_gated(x, M, *g, *u, H, K, group, _mode(mode), _act(act), y, ws, n, _stream(stream))
+    _check("w4a16_gated", rc)
+
+
+def w4a16_gated_bwd_workspace_bytes(M, H, K, group, from_ckpt) -> int:
+    return int(lib().w4a16_gated_bwd_workspace_bytes(M, H, K, group, 1 if from_ckpt else 0))
+
+
+def w4a16_gated_bwd(dH, M, gate, up, H, K, group, mode, act, dG, dU, dX, workspace=None, stream=None, *,
+                    X=None, X8=None, x_scale=None):
+    """dG, dU (the gradients of X Wg^T and X Wu^T) and dX from dH, with X as bf16 or as the 8-bit
+    checkpoint X8, x_scale (fp8_ckpt_save). dX may be None. workspace:
+    alloc_gated_bwd_workspace(M, H, K, group, from_ckpt=X8 is not None)."""
+    p = [_buf("dH", dH, 2 * M * H), _buf("X", X, 2 * M * K), _buf("X8", X8, M * K),
+         _buf("x_scale", x_scale, M * (K // 32))]
+    o = [_buf("dG", dG, 2 * M * H), _buf("dU", dU, 2 * M * H), _buf("dX", dX, 2 * M * K)]
+    g, u = _weight4("gate", gate, H, K, group), _weight4("up", up, H, K, group)
+    _check_device(dH, X, X8, x_scale, dG, dU, dX, workspace, *gate, *up)
+    ws, n = _ws(workspace)
+    with torch.cuda.device(dH.device):
+        rc = lib().w4a16_gated_bwd(*p, M, *g, *u, H, K, group, _mode(mode), _act(act), *o, ws, n, _stream(stream))
+    _check("w4a16_gated_bwd", rc)
+
+
+def w4a16_dgrad_workspace_bytes(M, N, K, group) -> int:
+    return int(lib().w4a16_dgrad_workspace_bytes(M, N, K, group))
+
+
+def w4a16_dgrad(dY, M, weight, N, K, group, mode, dX, workspace=None, stream=None):
+    """dX = dY W of a 4-bit linear layer; weight: (codes, scales, zeros) of W[N, K]; workspace:
+    alloc_dgrad_workspace(M, N, K, group)."""
+    dy, dx = _buf("dY", dY, 2 * M * N), _buf("dX", dX, 2 * M * K)
+    w = _weight4("weight", weight, N, K, group)
+    _check_device(dY, dX, workspace, *weight)
+    ws, n = _ws(workspace)
+    with torch.cuda.device(dY.device):
+        rc = lib().w4a16_dgrad(dy, M, *w, N, K, group, _mode(mode), dx, ws, n, _stream(stream))
+    _check("w4a16_dgrad", rc)
+
+
+def fp8_ckpt_save(X, M, K, X8, x_scale, stream=None):
+    """The 8-bit checkpoint of X [M, K]: X8 uint8 (or float8_e4m3fn) [M, K], x_scale uint8 [M, K/32]."""
+    p = _buf("X", X, 2 * M * K), M, K, _buf("X8", X8, M * K), _buf("x_scale", x_scale, M * (K // 32))
+    _check_device(X, X8, x_scale)
+    with torch.cuda.device(X.device):
+        rc = lib().fp8_ckpt_save(*p, _stream(stream))
+    _check("fp8_ckpt_save", rc)
+
+
+def fp8_ckpt_load(X8, x_scale, M, K, X, stream=None):
+    """X [M, K] bf16 from its 8-bit checkpoint, exactly."""
+    p = _buf("X8", X8, M * K), _buf("x_scale", x_scale, M * (K // 32)), M, K, _buf("X", X, 2 * M * K)
+    _check_device(X8, X, x_scale)
+    with torch.cuda.device(X8.device):
+        rc = lib().fp8_ckpt_load(*p, _stream(stream))
+    _check("fp8_ckpt_load", rc)
+
+
+def fp8_ckpt_wgrad_workspace_bytes(M, N, K) -> int:
+    return int(lib().fp8_ckpt_wgrad_workspace_bytes(M, N, K))
+
+
+def fp8_ckpt_wgrad(dY, X8, x_scale, M, N, K, dW, flags=0, workspace=None, stream=None):
+    """dW [N, K] = dY^T X from the 8-bit checkpoint of X; bf16, or fp32 with W4_OUT_FP32 in flags;
+    workspace: alloc_ckpt_wgrad_workspace(M, N, K)."""
+    p = (_buf("dY", dY, 2 * M * N), _buf("X8", X8, M * K), _buf("x_scale", x_scale, M * (K // 32)), M, N, K,
+         _buf("dW", dW, (4 if int(flags) & W4_OUT_FP32 else 2) * N * K))
+    _check_device(dY, X8, x_scale, dW, workspace)
+    ws, n = _ws(workspace)
+    with torch.cuda.device(dY.device):
+        rc = lib().fp8_ckpt_wgrad(*p, int(flags), ws, n, _stream(stream))
+    _check("fp8_ckpt_wgrad", rc)
+
+
 def w4_device_status(stream=None) -> int:
     code = ctypes.c_int(-1)
     rc = lib().w4_device_status(_stream(stream), ctypes.byref(code))
@@ -409,6 +553,36 @@ def alloc_gemm_rowquant_workspace(M, N, K, group, device="cuda"):
     if nbytes == 0:
         raise W4Error("w4a8_gemm_rowquant_workspace_bytes", 6)
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _zeros_or_none(nbytes, device):
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def alloc_gated_workspace(M, H, K, group, device="cuda"):
+    """Zero-filled workspace for w4a16_gated (calls leave its counters zero), or None."""
+    return _zeros_or_none(w4a16_gated_workspace_bytes(M, H, K, group), device)
+
+
+def alloc_gated_bwd_workspace(M, H, K, group, from_ckpt=False, device="cuda"):
+    """Zero-filled workspace for w4a16_gated_bwd, or None."""
+    return _zeros_or_none(w4a16_gated_bwd_workspace_bytes(M, H, K, group, from_ckpt), device)
+
+
+def alloc_dgrad_workspace(M, N, K, group, device="cuda"):
+    """Zero-filled workspace for w4a16_dgrad, or None."""
+    return _zeros_or_none(w4a16_dgrad_workspace_bytes(M, N, K, group), device)
+
+
+def alloc_ckpt_wgrad_workspace(M, N, K, device="cuda"):
+    """Zero-filled workspace for fp8_ckpt_wgrad, or None."""
+    return _zeros_or_none(fp8_ckpt_wgrad_workspace_bytes(M, N, K), device)
+
+
+def alloc_ckpt(M, K, device="cuda"):
+    """Empty outputs of fp8_ckpt_save: X8 uint8 [M, K] and the scale bytes uint8 [M, K/32]."""
+    return (torch.empty(M, K, dtype=torch.uint8, device=device),
+            torch.empty(M, K // 32, dtype=torch.uint8, device=device))
 
 
 def alloc_packed(N, K, group, layout, device="cuda", copies: int = 1):

@@ -69,6 +69,9 @@ enum {
 /* Kernel layouts produced by w4_prepack. */
 typedef enum { W4_LAYOUT_GEMV = 0, W4_LAYOUT_GEMM = 1, W4_LAYOUT_TC = 2 } w4_layout;
 
+/* Activations of w4a16_gated and w4a16_gated_bwd. */
+typedef enum { W4_ACT_SILU = 0, W4_ACT_GELU_TANH = 1 } w4_act;
+
 /* Human-readable name of a status code (static storage). */
 const char *w4_status_str(int status);
 
@@ -532,6 +535,104 @@ w4_status w4_nf4_quantize(const void *W_bf16, int64_t N, int64_t K, uint8_t *cod
                           cudaStream_t stream);
 w4_status w4_nf4_gemv(const void *x_bf16, int64_t M, const uint8_t *codes, const float *absmax,
                       int64_t N, int64_t K, void *y, int flags, cudaStream_t stream);
+
+/*
+ * w4a16_gated -- the gated feed-forward block over 4-bit weights in one kernel: both projections,
+ *   the activation and the product. No [gate | up] tensor goes through memory.
+ *     G = X Wg^T,  U = X Wu^T,  Y[m, h] = act(G[m, h]) * U[m, h]
+ *   W4_ACT_SILU: act(g) = g / (1 + exp(-g)); W4_ACT_GELU_TANH: act(g) = 0.5 g (1 + tanh(sqrt(2/pi)
+ *   (g + 0.044715 g^3))). The weights are the CANONICAL ones that w4_quantize writes (no prepack),
+ *   so that the forward pass, the backward pass and the portable form are the same bytes.
+ *   X_bf16       device, bf16 [M, K]; M >= 1 (one decoded token up to a prefill batch)
+ *   codes, scales, zeros (gate and up)   device, w4_quantize's outputs for Wg[H, K] and Wu[H, K],
+ *                the same group and mode for both; zeros NULL for W4_SYM, required for W4_ASYM
+ *   Y_bf16       device, bf16 [M, H]
+ *   workspace    NULL where w4a16_gated_workspace_bytes(M, H, K, group) is 0, else device scratch of
+ *                at least that many bytes (partial sums of outputs whose K range is shared by several
+ *                SMs, and their arrival counters). Zero-fill it before its first use; every call that
+ *                completes leaves its counters zero again, so one workspace serves any sequence of
+ *                calls of that shape or of one that needs no more, on one stream. Calls that may run
+ *                concurrently need separate workspaces. After a call whose kernel recorded an error
+ *                in the device status, zero-fill it again.
+ *   M <= 16: the weights enter as exact integers and group scales and zero points are applied in
+ *   fp32 (about 1e-6 relative before the one rounding to bf16). M > 16: tcgen05 MMAs on weights
+ *   dequantized to bf16 with one rounding (relative 2^-9 per weight) and fp32 accumulation.
+ *   Outputs must not overlap inputs. Results are bit-identical run to run on a given GPU.
+ *   M, H <= 2^24; 32 <= K <= 2^24, K % 32 == 0. Errors: NULL / SHAPE / GROUP / ALIGN / ARG (mode,
+ *   act, zeros given for W4_SYM) / WORKSPACE / CUDA.
+ */
+size_t w4a16_gated_workspace_bytes(int64_t M, int64_t H, int64_t K, int group);
+w4_status w4a16_gated(const void *X_bf16, int64_t M, const uint8_t *codes_gate, const uint16_t *scales_gate,
+                      const int16_t *zeros_gate, const uint8_t *codes_up, const uint16_t *scales_up,
+                      const int16_t *zeros_up, int64_t H, int64_t K, int group, int mode, int act,
+                      void *Y_bf16, void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * w4a16_gated_bwd -- the backward pass of w4a16_gated for frozen 4-bit weights (4-bit codes have no
+ *   gradient; what a model trains beside them takes dG, dU and dX). The forward keeps X only; G and U
+ *   are computed again here, in the kernel that forms their gradients:
+ *     dG = dH * U * act'(G),  dU = dH * act(G),  dX = dG Wg + dU Wu
+ *   dH_bf16      device, bf16 [M, H], the gradient of w4a16_gated's output
+ *   X_bf16       device, bf16 [M, K], the forward's input; or NULL with the 8-bit checkpoint of it:
+ *   X_e4m3, X_scale   device, fp8_ckpt_save's outputs for X; both NULL when X_bf16 is given
+ *   dG_bf16, dU_bf16  device, bf16 [M, H], outputs (rounded once; dX is formed from the rounded ones)
+ *   dX_bf16      device, bf16 [M, K], output, or NULL where it is not wanted (a first layer)
+ *   workspace    as w4a16_gated's, of w4a16_gated_bwd_workspace_bytes(M, H, K, group, from_ckpt) bytes
+ *                (0 is possible without a checkpoint); from_ckpt 1 adds the restored X.
+ *   Weights are dequantized to bf16 with one rounding, accumulation is fp32. Outputs must not overlap
+ *   inputs or each other. H % 8 == 0; other limits and errors as w4a16_gated.
+ */
+size_t w4a16_gated_bwd_workspace_bytes(int64_t M, int64_t H, int64_t K, int group, int from_ckpt);
+w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const uint8_t *X_e4m3, const uint8_t *X_scale,
+                          int64_t M, const uint8_t *codes_gate, const uint16_t *scales_gate,
+                          const int16_t *zeros_gate, const uint8_t *codes_up, const uint16_t *scales_up,
+                          const int16_t *zeros_up, int64_t H, int64_t K, int group, int mode, int act,
+                          void *dG_bf16, void *dU_bf16, void *dX_bf16, void *workspace, size_t workspace_bytes,
+                          cudaStream_t stream);
+
+/*
+ * w4a16_dgrad -- the gradient of a 4-bit linear layer y = x W^T by its input, dX = dY W, from the
+ *   canonical weight (the transposed product reads the same codes; there is no second copy):
+ *     dX[m, k] = sum_n dY[m, n] (q[n, k] - z[n, j(k)]) s[n, j(k)]
+ *   dY_bf16 [M, N], dX_bf16 [M, K] bf16; codes, scales, zeros as w4_quantize writes them for W[N, K].
+ *   workspace as w4a16_gated's, of w4a16_dgrad_workspace_bytes(M, N, K, group) bytes. Weights are
+ *   dequantized to bf16 with one rounding, accumulation is fp32.
+ *   M <= 2^24; N <= 2^24, N % 8 == 0; K as w4a16_gated. Errors as w4a16_gated.
+ */
+size_t w4a16_dgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int group);
+w4_status w4a16_dgrad(const void *dY_bf16, int64_t M, const uint8_t *codes, const uint16_t *scales,
+                      const int16_t *zeros, int64_t N, int64_t K, int group, int mode, void *dX_bf16,
+                      void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * fp8_ckpt_save, fp8_ckpt_load -- an activation kept for the backward pass in 8.25 bits a value:
+ *   E4M3 values with one power-of-two scale for each 32 consecutive columns of a row. The scale is
+ *   the smallest 2^e, e >= -124, with max|x| / 2^e <= 448; the value is e4m3(x / 2^e), round to
+ *   nearest even (no value saturates but those that would leave bf16's range when restored, from
+ *   3.3e38: at e = 120 the values stop at 240). A power of two makes value x scale exact in bf16, so that
+ *   what the backward pass multiplies is the checkpoint itself, rounded nowhere again.
+ *   X_bf16 [M, K] bf16; X_e4m3 uint8 [M, K]; X_scale uint8 [M, K/32], the byte e + 127. A block of 32
+ *   with an infinity or a NaN gets scale byte 255 and values 0x7F, and restores as NaN.
+ *   fp8_ckpt_load writes value * 2^e to bf16, exactly; a scale byte of 255 makes its block NaN.
+ *   M >= 1; K >= 32, K % 32 == 0. Errors: NULL / SHAPE / ALIGN / CUDA.
+ */
+w4_status fp8_ckpt_save(const void *X_bf16, int64_t M, int64_t K, uint8_t *X_e4m3, uint8_t *X_scale,
+                        cudaStream_t stream);
+w4_status fp8_ckpt_load(const uint8_t *X_e4m3, const uint8_t *X_scale, int64_t M, int64_t K, void *X_bf16,
+                        cudaStream_t stream);
+
+/*
+ * fp8_ckpt_wgrad -- the gradient of a linear layer y = x W^T by its weight (an adapter's, or a full
+ *   one's) from the 8-bit checkpoint of x: dW[n, k] = sum_m dY[m, n] x8[m, k] 2^e[m, k/32].
+ *   dY_bf16 [M, N] bf16; X_e4m3, X_scale as fp8_ckpt_save writes them for x [M, K]; dW [N, K] bf16, or
+ *   fp32 with W4_OUT_FP32 in flags. The products are exact, accumulation is fp32.
+ *   workspace as w4a16_gated's, of fp8_ckpt_wgrad_workspace_bytes(M, N, K) bytes.
+ *   M, N <= 2^24, N % 8 == 0; 32 <= K <= 2^24, K % 32 == 0. Errors: NULL / SHAPE / ALIGN / ARG / WORKSPACE / CUDA.
+ */
+size_t fp8_ckpt_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K);
+w4_status fp8_ckpt_wgrad(const void *dY_bf16, const uint8_t *X_e4m3, const uint8_t *X_scale, int64_t M, int64_t N,
+                         int64_t K, void *dW, int flags, void *workspace, size_t workspace_bytes,
+                         cudaStream_t stream);
 
 /*
  * w4_device_status -- synchronizes `stream`, then reads and clears the device status word

@@ -1,0 +1,254 @@
+"""GPU w4a16_gated, w4a16_gated_bwd and w4a16_dgrad against their 64-bit forms.
+
+Tolerances. A value rounded to bf16 is off by at most 2^-8 of it (HALF), a weight dequantized to
+bf16 too. Element by element, with A = |X| |W|^T the sum of magnitudes of a projection:
+  - the projections are off by at most D = (HALF + 2^-12) A (2^-12: fp32 accumulation, far above
+    it); for M <= 16 the weights are exact integers and D = 2^-12 A;
+  - an activation's slope is at most 1.13 in magnitude, its second derivative at most 1.2, so
+    |dY| <= 1.13 Dg (|u| + Du) + |act(g)| Du + HALF |Y|, and the gradients likewise.
+Over all elements the roundings are independent, so the relative Frobenius error is about
+HALF / sqrt(3) for each rounding that enters: output, u, g (times the ratio of slopes, taken as
+1.5) for Y, dG and dU: sqrt(1 + 1 + 2.25) HALF / sqrt(3) = 4.7e-3 -> 5e-3. dX adds the rounding of
+dG and dU and of the weights: 6e-3. For M <= 16 only the output's rounding: 2.6e-3. dgrad has two
+(weights, output): sqrt(2 / 3) HALF = 3.2e-3 -> 4e-3. These are means over many roundings: with
+fewer than 4096 outputs a few large ones carry the norm (a single one may be off by HALF = 3.9e-3
+from its own rounding alone), so only the element bounds hold there."""
+import pytest
+import torch
+
+import gated_ref as R
+from bit_gemm_wise_b200 import w4
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0") if torch.cuda.is_available() else None
+
+
+def nan_like(*shape):
+    return torch.full(shape, float("nan"), dtype=R.BF16, device=DEV)
+
+
+def status_ok():
+    torch.cuda.synchronize()
+    assert w4.w4_device_status() == 0
+
+
+def run_gated(x, wg, wu, group, mode, act, ws="new"):
+    M, K, H = x.shape[0], x.shape[1], wg[0].shape[0]
+    y = nan_like(M, H)
+    if ws == "new":
+        ws = w4.alloc_gated_workspace(M, H, K, group)
+    w4.w4a16_gated(x, M, wg, wu, H, K, group, mode, act, y, ws)
+    return y
+
+
+def run_bwd(dh, wg, wu, group, mode, act, X=None, ckpt=None, want_dx=True):
+    M, H, K = dh.shape[0], wg[0].shape[0], wg[0].shape[1] * 2
+    dg, du, dx = nan_like(M, H), nan_like(M, H), nan_like(M, K) if want_dx else None
+    x8, xs = ckpt if ckpt is not None else (None, None)
+    ws = w4.alloc_gated_bwd_workspace(M, H, K, group, from_ckpt=ckpt is not None)
+    w4.w4a16_gated_bwd(dh, M, wg, wu, H, K, group, mode, act, dg, du, dx, ws, X=X, X8=x8, x_scale=xs)
+    return dg, du, dx
+
+
+def run_dgrad(dy, w, group, mode):
+    M, N, K = dy.shape[0], w[0].shape[0], w[0].shape[1] * 2
+    dx = nan_like(M, K)
+    w4.w4a16_dgrad(dy, M, w, N, K, group, mode, dx, w4.alloc_dgrad_workspace(M, N, K, group))
+    return dx
+
+
+def magnitudes(x, w, group):
+    return x.double().abs() @ R.dequant(w, group).abs().t()
+
+
+def near(got, ref, bound, frob):
+    got, ref = got.double(), ref.double()
+    assert bool(torch.isfinite(got).all()), "unwritten outputs"
+    over = (got - ref).abs() > bound
+    assert not bool(over.any()), (int(over.sum()), torch.nonzero(over)[:8].tolist())
+    if ref.numel() >= 4096:
+        assert R.rel(got, ref) <= frob, R.rel(got, ref)
+
+
+def weights(H, K, group, mode, seed, shift=0.0):
+    return (R.weight(H, K, group, mode, seed, DEV, shift), R.weight(H, K, group, mode, seed + 1, DEV, shift))
+
+
+def check_gated(x, wg, wu, group, mode, act):
+    y = run_gated(x, wg, wu, group, mode, act)
+    status_ok()
+    g, u = x.double() @ R.dequant(wg, group).t(), x.double() @ R.dequant(wu, group).t()
+    few = x.shape[0] <= 16
+    e = 2.0 ** -12 + (0 if few else R.HALF)
+    dg, du = e * magnitudes(x, wg, group), e * magnitudes(x, wu, group)
+    ref = R.act(g, act) * u
+    bound = 1.13 * dg * (u.abs() + du) + R.act(g, act).abs() * du + R.HALF * ref.abs() + 1e-30
+    near(y, ref, bound, 2.6e-3 if few else 5e-3)
+
+
+# rows from one token up, over and beside the kernels' tile sizes; odd H; K of whole and half
+# blocks of 64, shorter than a block, and long
+SHAPES = [
+    (1, 64, 128, 128, "asym"), (1, 1, 32, 32, "sym"), (2, 7, 96, 32, "asym"), (5, 333, 320, 64, "sym"),
+    (8, 65, 512, 256, "asym"), (9, 200, 576, 32, "sym"), (16, 129, 1056, 32, "asym"), (16, 40, 4096, 128, "sym"),
+    (17, 64, 128, 128, "asym"), (17, 3, 32, 32, "asym"), (33, 100, 96, 32, "sym"), (64, 65, 256, 64, "asym"),
+    (100, 333, 576, 64, "sym"), (129, 127, 1024, 256, "asym"), (255, 64, 160, 32, "asym"), (257, 193, 1088, 64, "asym"),
+    (300, 1000, 2048, 128, "asym"), (520, 96, 8192, 256, "sym"), (1, 2049, 2048, 128, "asym"), (3, 515, 14336, 128, "asym"),
+]
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("M,H,K,group,mode", SHAPES)
+def test_gated(M, H, K, group, mode, act):
+    wg, wu = weights(H, K, group, mode, M + H)
+    check_gated(R.rows(M, K, K + M, DEV, outliers=4), wg, wu, group, mode, act)
+
+
+@pytest.mark.parametrize("M", [4, 40])
+@pytest.mark.parametrize("shift", [0.5, -3.0])
+def test_gated_zero_points_outside_the_codes(M, shift):
+    """Weights all of one sign have zero points far from 0..15 (here about -90 and 600)."""
+    wg, wu = weights(72, 256, 64, "asym", 5, shift)
+    assert int(wg[2].abs().max()) > 60
+    check_gated(R.rows(M, 256, 7, DEV), wg, wu, 64, "asym", "silu")
+
+
+@pytest.mark.parametrize("M", [6, 50])
+def test_gated_rows_are_independent(M):
+    """A NaN or an infinity in one row, or a row of zeros, leaves the other rows as they were."""
+    wg, wu = weights(96, 256, 128, "asym", 9)
+    x = R.rows(M, 256, 11, DEV)
+    base = run_gated(x, wg, wu, 128, "asym", "silu")
+    bad = x.clone()
+    bad[1, 3], bad[3, 200], bad[4] = float("nan"), float("inf"), 0.0
+    y = run_gated(bad, wg, wu, 128, "asym", "silu")
+    status_ok()
+    keep = [m for m in range(M) if m not in (1, 3, 4)]
+    assert torch.equal(y[keep], base[keep])
+    assert bool(torch.isnan(y[1]).all()) and not bool(torch.isfinite(y[3]).any()) and bool((y[4] == 0).all())
+
+
+BWD = [(1, 8, 32, 32, "sym"), (3, 64, 128, 128, "asym"), (16, 72, 96, 32, "asym"), (65, 136, 320, 64, "sym"),
+       (130, 64, 512, 256, "asym"), (257, 200, 1088, 64, "asym"), (300, 1000, 768, 128, "sym")]
+
+
+def check_bwd(got, x, dh, wg, wu, group, act):
+    a, b = R.dequant(wg, group), R.dequant(wu, group)
+    g, u, d = x.double() @ a.t(), x.double() @ b.t(), dh.double()
+    e = R.HALF + 2.0 ** -12
+    eg, eu = e * magnitudes(x, wg, group), e * magnitudes(x, wu, group)
+    rg, ru, rx = R.gated_grads(x, dh, wg, wu, group, act)
+    bg = d.abs() * (1.13 * eu + 1.2 * eg * (u.abs() + eu)) + R.HALF * rg.abs() + 1e-30
+    bu = d.abs() * 1.13 * eg + R.HALF * ru.abs() + 1e-30
+    near(got[0], rg, bg, 5e-3)
+    near(got[1], ru, bu, 5e-3)
+    if got[2] is not None:
+        bx = (1 + e) * (bg @ a.abs() + bu @ b.abs()) + e * (rg.abs() @ a.abs() + ru.abs() @ b.abs()) + R.HALF * rx.abs()
+        near(got[2], rx, bx + 1e-30, 6e-3)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("M,H,K,group,mode", BWD)
+def test_gated_bwd(M, H, K, group, mode, act):
+    wg, wu = weights(H, K, group, mode, M + H)
+    x, dh = R.rows(M, K, 1, DEV, outliers=4), R.rows(M, H, 2, DEV, std=0.01)
+    got = run_bwd(dh, wg, wu, group, mode, act, X=x)
+    status_ok()
+    check_bwd(got, x, dh, wg, wu, group, act)
+
+
+@pytest.mark.parametrize("M,H,K,group,mode", BWD)
+def test_gated_bwd_from_the_checkpoint(M, H, K, group, mode):
+    """The gradients at the checkpoint's value of x, which is exact in bf16: bit for bit those
+    from the bf16 tensor of that value."""
+    wg, wu = weights(H, K, group, mode, M + H)
+    x, dh = R.rows(M, K, 1, DEV, outliers=4), R.rows(M, H, 2, DEV, std=0.01)
+    x8, xs = w4.alloc_ckpt(M, K)
+    w4.fp8_ckpt_save(x, M, K, x8, xs)
+    got = run_bwd(dh, wg, wu, group, mode, "silu", ckpt=(x8, xs))
+    status_ok()
+    xr = R.restored(x8, xs).to(R.BF16)
+    check_bwd(got, xr, dh, wg, wu, group, "silu")
+    for p, q in zip(got, run_bwd(dh, wg, wu, group, mode, "silu", X=xr)):
+        assert torch.equal(p, q)
+
+
+def test_gated_bwd_without_dx():
+    wg, wu = weights(64, 128, 64, "asym", 3)
+    x, dh = R.rows(20, 128, 1, DEV), R.rows(20, 64, 2, DEV)
+    full, part = run_bwd(dh, wg, wu, 64, "asym", "silu", X=x), run_bwd(dh, wg, wu, 64, "asym", "silu", X=x, want_dx=False)
+    status_ok()
+    assert torch.equal(full[0], part[0]) and torch.equal(full[1], part[1])
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_gated_bwd_against_differences(act):
+    """<dX, V> against the central difference of the 64-bit forward along V. The difference is
+    exact to 1e-8; the kernel's dX is off by the roundings of bf16, 6e-3 of |dX| |V| at most by
+    Cauchy's inequality."""
+    M, H, K, g = 48, 136, 256, 64
+    wg, wu = weights(H, K, g, "asym", 21)
+    x, dh = R.rows(M, K, 1, DEV), R.rows(M, H, 2, DEV)
+    _, _, dx = run_bwd(dh, wg, wu, g, "asym", act, X=x)
+    status_ok()
+    for seed in range(4):
+        v = R.rows(M, K, 30 + seed, DEV).double()
+        h = 1e-5
+        num = ((R.gated(x.double() + h * v, wg, wu, g, act) - R.gated(x.double() - h * v, wg, wu, g, act)) * dh.double()).sum() / (2 * h)
+        assert abs(float((dx.double() * v).sum() - num)) <= 6e-3 * float(dx.double().norm() * v.norm())
+
+
+DGRAD = [(1, 8, 32, 32, "sym"), (2, 24, 96, 32, "asym"), (16, 200, 128, 128, "asym"), (17, 64, 320, 64, "sym"),
+         (64, 1000, 512, 256, "asym"), (130, 328, 1088, 64, "asym"), (300, 2048, 384, 128, "sym"), (257, 72, 4096, 128, "asym")]
+
+
+@pytest.mark.parametrize("M,N,K,group,mode", DGRAD)
+def test_dgrad(M, N, K, group, mode):
+    w = R.weight(N, K, group, mode, N + K, DEV)
+    dy = R.rows(M, N, 5, DEV, std=0.01)
+    dx = run_dgrad(dy, w, group, mode)
+    status_ok()
+    a = R.dequant(w, group)
+    ref = dy.double() @ a
+    bound = (R.HALF + 2.0 ** -12) * (dy.double().abs() @ a.abs()) + R.HALF * ref.abs() + 1e-30
+    near(dx, ref, bound, 4e-3)
+
+
+def test_results_do_not_change_from_run_to_run_and_workspaces_serve_again():
+    """One workspace of the largest need over several shapes, each twice: the same bits."""
+    shapes = [(40, 64, 4096, 128), (300, 64, 2048, 128), (17, 200, 8192, 128)]
+    n = max(w4.w4a16_gated_workspace_bytes(*s) for s in shapes)
+    ws = torch.zeros(max(n, 16), dtype=torch.uint8, device=DEV)
+    for M, H, K, g in shapes + shapes[::-1]:
+        wg, wu = weights(H, K, g, "asym", H)
+        x = R.rows(M, K, M, DEV)
+        first = run_gated(x, wg, wu, g, "asym", "silu", ws)
+        assert torch.equal(first, run_gated(x, wg, wu, g, "asym", "silu", ws))
+        assert torch.equal(first, run_gated(x, wg, wu, g, "asym", "silu"))
+    status_ok()
+
+
+def test_another_stream_and_a_replayed_graph():
+    """Calls on a side stream and in a captured graph, replayed on new inputs."""
+    g, act = 64, "silu"
+    for M, H, K in [(4, 200, 512), (70, 72, 4096)]:
+        wg, wu = weights(H, K, g, "asym", 2)
+        x = [R.rows(M, K, s, DEV) for s in (1, 2, 3)]
+        want = [run_gated(v, wg, wu, g, "asym", act) for v in x]
+        ws = w4.alloc_gated_workspace(M, H, K, g)
+        buf, y = x[0].clone(), nan_like(M, H)
+        torch.cuda.synchronize()
+        s = torch.cuda.Stream()
+        w4.w4a16_gated(buf, M, wg, wu, H, K, g, "asym", act, y, ws, stream=s)
+        s.synchronize()
+        assert torch.equal(y, want[0])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            w4.w4a16_gated(buf, M, wg, wu, H, K, g, "asym", act, y, ws)
+        for i in (1, 2, 0):
+            buf.copy_(x[i])
+            y.fill_(float("nan"))
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, want[i])
+    status_ok()
