@@ -1,17 +1,16 @@
 // The gated feed-forward block over canonical 4-bit weights (w4a16_gated), its backward pass
 // (w4a16_gated_bwd) and the input gradient of a 4-bit layer (w4a16_dgrad).
 //
-// First form: one thread per output, the weight dequantized to fp32 as it is read.
+// The products of many rows are those of w4_expand_gemm.cuh; for up to 16 rows w4a16_gated has one
+// thread per output, the weight dequantized to fp32 as it is read.
 #include "w4_common.cuh"
+#include "w4_expand_gemm.cuh"
 
 namespace w4 {
 namespace gated {
 
-struct Weight {
-    const uint8_t *codes;     // [N, K/2]
-    const uint16_t *scales;   // [N, K/g] fp16 bits
-    const int16_t *zeros;     // [N, K/g], NULL for symmetric weights (z = 8)
-};
+using xg::Weight;
+using xg::act_of;
 
 __device__ __forceinline__ float weight_at(const Weight &w, int64_t n, int64_t k, int64_t K, int gshift) {
     const int q = (w.codes[n * (K / 2) + (k >> 1)] >> (4 * (k & 1))) & 15;
@@ -20,24 +19,8 @@ __device__ __forceinline__ float weight_at(const Weight &w, int64_t n, int64_t k
     return (float)(q - z) * __half2float(__ushort_as_half(w.scales[j]));
 }
 
-__device__ __forceinline__ float act_of(float g, int act) {
-    if (act == W4_ACT_SILU) return g / (1.0f + expf(-g));
-    const float t = tanhf(0.7978845608028654f * (g + 0.044715f * g * g * g));
-    return 0.5f * g * (1.0f + t);
-}
-
-__device__ __forceinline__ float slope_of(float g, int act) {
-    if (act == W4_ACT_SILU) {
-        const float s = 1.0f / (1.0f + expf(-g));
-        return s * (1.0f + g * (1.0f - s));
-    }
-    const float t = tanhf(0.7978845608028654f * (g + 0.044715f * g * g * g));
-    return 0.5f * (1.0f + t) + 0.5f * g * (1.0f - t * t) * 0.7978845608028654f * (1.0f + 3.0f * 0.044715f * g * g);
-}
-
-// act(g) u, or with dh the gradients dG and dU
 __global__ void gated_kernel(const __nv_bfloat16 *x, int64_t M, Weight wg, Weight wu, int64_t H, int64_t K, int gshift,
-                             int act, const __nv_bfloat16 *dh, __nv_bfloat16 *y, __nv_bfloat16 *dg, __nv_bfloat16 *du) {
+                             int act, __nv_bfloat16 *y) {
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < M * H; i += (int64_t)gridDim.x * blockDim.x) {
         const int64_t m = i / H, h = i % H;
         float g = 0.0f, u = 0.0f;
@@ -46,26 +29,7 @@ __global__ void gated_kernel(const __nv_bfloat16 *x, int64_t M, Weight wg, Weigh
             g = fmaf(xv, weight_at(wg, h, k, K, gshift), g);
             u = fmaf(xv, weight_at(wu, h, k, K, gshift), u);
         }
-        if (!dh) {
-            y[i] = __float2bfloat16_rn(act_of(g, act) * u);
-        } else {
-            const float d = __bfloat162float(dh[i]);
-            dg[i] = __float2bfloat16_rn(d * u * slope_of(g, act));
-            du[i] = __float2bfloat16_rn(d * act_of(g, act));
-        }
-    }
-}
-
-// dX = dA Wa (+ dB Wb)
-__global__ void dgrad_kernel(const __nv_bfloat16 *da, Weight wa, const __nv_bfloat16 *db, Weight wb, int64_t M, int64_t N,
-                             int64_t K, int gshift, __nv_bfloat16 *dx) {
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < M * K; i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t m = i / K, k = i % K;
-        float s = 0.0f;
-        for (int64_t n = 0; n < N; ++n) s = fmaf(__bfloat162float(da[m * N + n]), weight_at(wa, n, k, K, gshift), s);
-        if (db)
-            for (int64_t n = 0; n < N; ++n) s = fmaf(__bfloat162float(db[m * N + n]), weight_at(wb, n, k, K, gshift), s);
-        dx[i] = __float2bfloat16_rn(s);
+        y[i] = __float2bfloat16_rn(act_of(g, act) * u);
     }
 }
 
@@ -76,6 +40,7 @@ using namespace w4;
 
 namespace {
 
+constexpr int64_t kFewRows = 16;  // up to here w4a16_gated reads the weights as a decode step does
 constexpr int64_t kMaxRows = (int64_t)1 << 24;
 
 bool gated_shape_ok(int64_t M, int64_t N, int64_t K) {
@@ -100,7 +65,10 @@ unsigned blocks_for(int64_t n) {
 
 }  // namespace
 
-W4_API size_t w4a16_gated_workspace_bytes(int64_t M, int64_t H, int64_t K, int group) { return 0; }
+W4_API size_t w4a16_gated_workspace_bytes(int64_t M, int64_t H, int64_t K, int group) {
+    if (!gated_shape_ok(M, H, K) || !valid_group(group) || K % group != 0 || M <= kFewRows) return 0;
+    return xg::make_plan(xg::FWD, H, M, K, 1, 0, num_sms()).bytes;
+}
 
 W4_API w4_status w4a16_gated(const void *X_bf16, int64_t M, const uint8_t *codes_gate, const uint16_t *scales_gate,
                              const int16_t *zeros_gate, const uint8_t *codes_up, const uint16_t *scales_up,
@@ -114,16 +82,51 @@ W4_API w4_status w4a16_gated(const void *X_bf16, int64_t M, const uint8_t *codes
     if (st == W4_OK) st = weight_ok(codes_up, scales_up, zeros_up, mode);
     if (st != W4_OK) return st;
     if (!aligned16(X_bf16) || !aligned16(Y_bf16) || (workspace && !aligned16(workspace))) return W4_ERR_ALIGN;
-    if (workspace_bytes < w4a16_gated_workspace_bytes(M, H, K, group)) return W4_ERR_WORKSPACE;
-    gated::gated_kernel<<<blocks_for(M * H), 256, 0, stream>>>(
-        (const __nv_bfloat16 *)X_bf16, M, {codes_gate, scales_gate, zeros_gate}, {codes_up, scales_up, zeros_up}, H, K,
-        group_shift(group), act, nullptr, (__nv_bfloat16 *)Y_bf16, nullptr, nullptr);
-    return launch_status();
+    if (M <= kFewRows) {
+        gated::gated_kernel<<<blocks_for(M * H), 256, 0, stream>>>(
+            (const __nv_bfloat16 *)X_bf16, M, {codes_gate, scales_gate, zeros_gate}, {codes_up, scales_up, zeros_up}, H,
+            K, group_shift(group), act, (__nv_bfloat16 *)Y_bf16);
+        return launch_status();
+    }
+    const int sms = num_sms();
+    const xg::Plan p = xg::make_plan(xg::FWD, H, M, K, 1, 0, sms);
+    if (p.bytes && (!workspace || workspace_bytes < p.bytes)) return W4_ERR_WORKSPACE;
+    CUtensorMap tm;
+    if (!xg::make_map(&tm, X_bf16, M, K, p.NT)) return W4_ERR_CUDA;
+    xg::Args a = {};
+    a.w[0] = {codes_gate, scales_gate, zeros_gate};
+    a.w[1] = {codes_up, scales_up, zeros_up};
+    a.out = Y_bf16;
+    a.rows = H;
+    a.K = K;
+    a.cols = M;
+    a.gshift = group_shift(group);
+    a.act = act;
+    return xg::launch<xg::FWD, false>(p, tm, tm, a, workspace, sms, stream);
 }
+
+namespace {
+
+// Workspace of the backward pass: counters and partial sums of its two products (one after the
+// other in the same place), then the restored X.
+struct BwdLayout {
+    xg::Plan grads, dx;
+    size_t restored, bytes;
+};
+BwdLayout bwd_layout(int64_t M, int64_t H, int64_t K, bool ckpt, int sms) {
+    BwdLayout l;
+    l.grads = xg::make_plan(xg::FWD, H, M, K, 1, 0, sms);
+    l.dx = xg::make_plan(xg::DGRAD, K, M, H, 2, 0, sms);
+    l.restored = ((l.grads.bytes > l.dx.bytes ? l.grads.bytes : l.dx.bytes) + 255) / 256 * 256;
+    l.bytes = l.restored + (ckpt ? (size_t)M * K * 2 : 0);
+    return l;
+}
+
+}  // namespace
 
 W4_API size_t w4a16_gated_bwd_workspace_bytes(int64_t M, int64_t H, int64_t K, int group, int from_ckpt) {
     if (!gated_shape_ok(M, H, K) || H % 8 != 0 || !valid_group(group) || K % group != 0) return 0;
-    return from_ckpt ? (size_t)M * K * 2 : 0;
+    return bwd_layout(M, H, K, from_ckpt != 0, num_sms()).bytes;
 }
 
 W4_API w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const uint8_t *X_e4m3, const uint8_t *X_scale,
@@ -144,25 +147,41 @@ W4_API w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const 
     for (const void *p : {dH_bf16, X_bf16, (const void *)X_e4m3, (const void *)X_scale, (const void *)dG_bf16,
                           (const void *)dU_bf16, (const void *)dX_bf16, (const void *)workspace})
         if (p && !aligned16(p)) return W4_ERR_ALIGN;
-    const size_t need = w4a16_gated_bwd_workspace_bytes(M, H, K, group, ckpt ? 1 : 0);
-    if (need && (!workspace || workspace_bytes < need)) return W4_ERR_WORKSPACE;
+    const int sms = num_sms();
+    const BwdLayout l = bwd_layout(M, H, K, ckpt, sms);
+    if (l.bytes && (!workspace || workspace_bytes < l.bytes)) return W4_ERR_WORKSPACE;
     if (ckpt) {
-        st = fp8_ckpt_load(X_e4m3, X_scale, M, K, workspace, stream);
+        void *x = static_cast<uint8_t *>(workspace) + l.restored;
+        st = fp8_ckpt_load(X_e4m3, X_scale, M, K, x, stream);
         if (st != W4_OK) return st;
-        X_bf16 = workspace;
+        X_bf16 = x;
     }
-    const gated::Weight wg = {codes_gate, scales_gate, zeros_gate}, wu = {codes_up, scales_up, zeros_up};
-    gated::gated_kernel<<<blocks_for(M * H), 256, 0, stream>>>(
-        (const __nv_bfloat16 *)X_bf16, M, wg, wu, H, K, group_shift(group), act, (const __nv_bfloat16 *)dH_bf16, nullptr,
-        (__nv_bfloat16 *)dG_bf16, (__nv_bfloat16 *)dU_bf16);
-    if (dX_bf16)
-        gated::dgrad_kernel<<<blocks_for(M * K), 256, 0, stream>>>((const __nv_bfloat16 *)dG_bf16, wg,
-                                                                   (const __nv_bfloat16 *)dU_bf16, wu, M, H, K,
-                                                                   group_shift(group), (__nv_bfloat16 *)dX_bf16);
-    return launch_status();
+    CUtensorMap tm0, tm1;
+    xg::Args a = {};
+    a.w[0] = {codes_gate, scales_gate, zeros_gate};
+    a.w[1] = {codes_up, scales_up, zeros_up};
+    a.rows = H;
+    a.K = K;
+    a.cols = M;
+    a.gshift = group_shift(group);
+    a.act = act;
+    a.dh = static_cast<const __nv_bfloat16 *>(dH_bf16);
+    a.out = dG_bf16;
+    a.out2 = static_cast<__nv_bfloat16 *>(dU_bf16);
+    if (!xg::make_map(&tm0, X_bf16, M, K, l.grads.NT)) return W4_ERR_CUDA;
+    st = xg::launch<xg::FWD, true>(l.grads, tm0, tm0, a, workspace, sms, stream);
+    if (st != W4_OK || !dX_bf16) return st;
+    if (!xg::make_map(&tm0, dG_bf16, M, H, l.dx.NT) || !xg::make_map(&tm1, dU_bf16, M, H, l.dx.NT)) return W4_ERR_CUDA;
+    a.dh = nullptr;
+    a.out = dX_bf16;
+    a.out2 = nullptr;
+    return xg::launch<xg::DGRAD, false>(l.dx, tm0, tm1, a, workspace, sms, stream);
 }
 
-W4_API size_t w4a16_dgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int group) { return 0; }
+W4_API size_t w4a16_dgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int group) {
+    if (!gated_shape_ok(M, N, K) || N % 8 != 0 || !valid_group(group) || K % group != 0) return 0;
+    return xg::make_plan(xg::DGRAD, K, M, N, 1, 0, num_sms()).bytes;
+}
 
 W4_API w4_status w4a16_dgrad(const void *dY_bf16, int64_t M, const uint8_t *codes, const uint16_t *scales,
                              const int16_t *zeros, int64_t N, int64_t K, int group, int mode, void *dX_bf16,
@@ -174,9 +193,17 @@ W4_API w4_status w4a16_dgrad(const void *dY_bf16, int64_t M, const uint8_t *code
     w4_status st = weight_ok(codes, scales, zeros, mode);
     if (st != W4_OK) return st;
     if (!aligned16(dY_bf16) || !aligned16(dX_bf16) || (workspace && !aligned16(workspace))) return W4_ERR_ALIGN;
-    if (workspace_bytes < w4a16_dgrad_workspace_bytes(M, N, K, group)) return W4_ERR_WORKSPACE;
-    gated::dgrad_kernel<<<blocks_for(M * K), 256, 0, stream>>>((const __nv_bfloat16 *)dY_bf16, {codes, scales, zeros},
-                                                               nullptr, {}, M, N, K, group_shift(group),
-                                                               (__nv_bfloat16 *)dX_bf16);
-    return launch_status();
+    const int sms = num_sms();
+    const xg::Plan p = xg::make_plan(xg::DGRAD, K, M, N, 1, 0, sms);
+    if (p.bytes && (!workspace || workspace_bytes < p.bytes)) return W4_ERR_WORKSPACE;
+    CUtensorMap tm;
+    if (!xg::make_map(&tm, dY_bf16, M, N, p.NT)) return W4_ERR_CUDA;
+    xg::Args a = {};
+    a.w[0] = a.w[1] = {codes, scales, zeros};
+    a.out = dX_bf16;
+    a.rows = N;
+    a.K = K;
+    a.cols = M;
+    a.gshift = group_shift(group);
+    return xg::launch<xg::DGRAD, false>(p, tm, tm, a, workspace, sms, stream);
 }
