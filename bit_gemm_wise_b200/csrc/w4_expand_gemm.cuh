@@ -2,10 +2,14 @@
 // the gated feed-forward block over 4-bit weights, its backward pass, the input gradient of a
 // 4-bit layer and the weight gradient from an 8-bit checkpoint are all
 //     D[i, c] = sum_r A[i, r] B[c, r],     i: 128 lanes of a tile, c: up to 256 columns
-// with A expanded to bf16 by the kernel's own warps and B bf16 in memory:
+// with A expanded to 16 bits by the kernel's own warps and B 16-bit in memory:
 //   FWD    A = 64 gate rows and 64 up rows of the weights, r = their K columns; B = X [token, K]
 //   DGRAD  A = 128 columns k of the weight(s), r = weight rows n;               B = dY [token, N]
 //   WGRAD  A = 128 columns k of the checkpoint, r = tokens;                      B = dY^T (c = n)
+// FWD and DGRAD multiply in fp16: a weight (q - z) s then takes one rounding of 2^-11, an eighth of
+// bf16's, and bf16 activations are exact in fp16 once each token's row is divided by a power of
+// two (row_prep_kernel writes that copy; the epilogue multiplies the power back). WGRAD multiplies
+// in bf16, in which both operands are exact.
 // In FWD a row of A is contiguous along r (K-major); in DGRAD and WGRAD it is contiguous along i
 // (MN-major, which the MMA reads as it stands), so the expansion writes the same bytes either way:
 // 16-byte chunks of eight k, at the place that the 128-byte swizzle gives them.
@@ -66,6 +70,7 @@ struct Args {
     const __nv_bfloat16 *dh;  // FWD: NULL, or [cols, rows]: write the gradients of both projections
     void *out;                // FWD: Y or dG [cols, rows]; DGRAD: dX [cols, K]; WGRAD: dW [cols, K]
     __nv_bfloat16 *out2;      // FWD with dh: dU
+    const float *row_pow;     // FWD, DGRAD: the power of two that each token's row was divided by
     float *part;              // partial sums [tile][part][column][lane]
     uint32_t *cnt;            // arrival counters [tile][4], zero between calls
     int *status;
@@ -122,14 +127,24 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-__device__ __forceinline__ uint32_t bsub(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t hsub(uint32_t a, uint32_t b) {
     uint32_t d;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
-__device__ __forceinline__ uint32_t badd(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t hadd(uint32_t a, uint32_t b) {
     uint32_t d;
-    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t hmul(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t hfma(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
 __device__ __forceinline__ uint32_t bmul(uint32_t a, uint32_t b) {
@@ -137,62 +152,46 @@ __device__ __forceinline__ uint32_t bmul(uint32_t a, uint32_t b) {
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
-__device__ __forceinline__ uint32_t bfma(uint32_t a, uint32_t b, uint32_t c) {
-    uint32_t d;
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-    return d;
-}
-__device__ __forceinline__ uint32_t bpair(float v) {  // v, rounded to bf16, in both halves
-    const uint32_t b = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+__device__ __forceinline__ uint32_t hpair(float v) {  // v, rounded to fp16, in both halves
+    const uint32_t b = __half_as_ushort(__float2half_rn(v));
     return b | (b << 16);
 }
-__device__ __forceinline__ float bvalue(uint32_t pair) { return __uint_as_float(pair << 16); }
 
 // The scale and zero point of 32 values, as the constants of their expansion. A weight is
-// (q - z) s rounded once to bf16: q enters the mantissa of 16.0 (16 + q, exact), less 16 + z is
-// q - z (exact for |z| <= 240), times s = s_hi + s_lo by one multiplication and one fused
-// multiply-add, of which only the last one rounds at the weight's size. Zero points beyond 240
-// (groups of one sign far from zero) take (q - 8) s + (8 - z) s with the constant split in two.
+// (q - z) s rounded once to fp16: q enters the mantissa of 1024.0 (1024 + q, exact), less 1024 + z
+// is q - z (exact for |z| <= 1024), times the fp16 scale as it is. Zero points beyond that
+// (groups of one sign far from zero) take ((q - 8) s + c_lo) + c_hi with (8 - z) s = c_hi + c_lo,
+// of which again only the last operation rounds at the weight's size.
 struct Scale {
-    uint32_t hi, lo, zc;   // s_hi, s_lo, 16 + z
+    uint32_t s, zc;        // s, 1024 + z
     uint32_t ch, cl;       // (8 - z) s, split
     bool far;
 };
 __device__ __forceinline__ Scale scale_of(uint32_t sz) {
     Scale c;
-    const float s = __half2float(__ushort_as_half((unsigned short)(sz & 0xFFFFu)));
+    c.s = __byte_perm(sz, 0, 0x1010);
     const int z = (int)(int16_t)(sz >> 16);
-    c.hi = bpair(s);
-    const float rest = s - bvalue(c.hi);
-    c.lo = bpair(rest == rest ? rest : 0.0f);  // an infinite scale stays infinite
-    c.far = z > 240 || z < -240;
-    c.zc = bpair((float)(16 + z));
-    const float k = (float)(8 - z) * s;
-    c.ch = bpair(k);
-    const float kr = k - bvalue(c.ch);
-    c.cl = bpair(kr == kr ? kr : 0.0f);
+    c.far = z > 1024 || z < -1024;
+    c.zc = hpair((float)(1024 + z));
+    c.ch = c.cl = 0u;
+    if (c.far) {
+        const float k = (float)(8 - z) * __half2float(__ushort_as_half((unsigned short)(sz & 0xFFFFu)));
+        c.ch = hpair(k);
+        c.cl = hpair(k - __half2float(__ushort_as_half((unsigned short)(c.ch & 0xFFFFu))));
+    }
     return c;
 }
-// eight codes (nibble i is value i) as bf16, in order
+// eight codes (nibble i is value i) as fp16, in order
 __device__ __forceinline__ void expand8(uint32_t w, const Scale &c, uint32_t (&o)[4]) {
     uint32_t p[4];  // pairs (i, i + 4)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t sh = i == 0 ? w << 3 : w >> (4 * i - 3);
-        p[i] = (sh & 0x00780078u) | 0x41804180u;
-    }
+    for (int i = 0; i < 4; ++i) p[i] = ((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u;
     if (!c.far) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t d = bsub(p[i], c.zc);
-            p[i] = bfma(d, c.hi, bmul(d, c.lo));
-        }
+        for (int i = 0; i < 4; ++i) p[i] = hmul(hsub(p[i], c.zc), c.s);
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t d = bsub(p[i], 0x41C041C0u);  // q - 8
-            p[i] = badd(bfma(d, c.hi, bfma(d, c.lo, c.cl)), c.ch);
-        }
+        for (int i = 0; i < 4; ++i) p[i] = hadd(hfma(hsub(p[i], 0x64086408u), c.s, c.cl), c.ch);
     }
     o[0] = __byte_perm(p[0], p[1], 0x5410);
     o[1] = __byte_perm(p[2], p[3], 0x5410);
@@ -412,7 +411,8 @@ __device__ __forceinline__ void emit(const Args &a, const Unit &un, int q4, int 
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float got = __shfl_xor_sync(FULL, up ? v[2 * i] : v[2 * i + 1], 16);
-            const float g = up ? got : v[2 * i], u = up ? v[2 * i + 1] : got;
+            const float f = a.row_pow[tok0 + 2 * i];
+            const float g = f * (up ? got : v[2 * i]), u = f * (up ? v[2 * i + 1] : got);
             if (h < a.rows && c + 2 * i + (up ? 1 : 0) < ncols) {
                 const int64_t at = (tok0 + 2 * i) * a.rows + h;
                 if (GRADS) {
@@ -436,7 +436,8 @@ __device__ __forceinline__ void emit(const Args &a, const Unit &un, int q4, int 
             __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.out) + at;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                if (c + i < ncols) o[i * a.K] = __float2bfloat16_rn(v[i]);
+                if (c + i < ncols)
+                    o[i * a.K] = __float2bfloat16_rn(KIND == DGRAD ? v[i] * a.row_pow[un.tn * a.NT + c + i] : v[i]);
         }
     }
 }
@@ -508,6 +509,7 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
     } else if (warp == 12) {
         // ------------------------------------------------ B by TMA
         if (lane == 0) {
+            if (KIND != WGRAD) asm volatile("griddepcontrol.wait;" ::: "memory");  // B is row_prep_kernel's
             int slot = 0, issued = 0;
             uint32_t phase = 0;
             bool ok = true;
@@ -539,8 +541,9 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
     } else if (warp == 13) {
         // ------------------------------------------------ MMA issue
         if (lane == 0) {
-            // D fp32, A and B bf16, M = 128, N = NT; A (and B in WGRAD) contiguous along M (N)
-            const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (KIND != FWD ? 1u << 15 : 0u) |
+            // D fp32, A and B fp16 (0) or bf16 (1), M = 128, N = NT; A (and B in WGRAD) contiguous
+            // along M (N)
+            const uint32_t idesc = (1u << 4) | (KIND == WGRAD ? (1u << 7) | (1u << 10) : 0u) | (KIND != FWD ? 1u << 15 : 0u) |
                                    (KIND == WGRAD ? 1u << 16 : 0u) | ((uint32_t)(a.NT >> 3) << 17) | (8u << 24);
             // low word: address / 16 | leading offset / 16 (K-major: unused; MN-major: 8192 bytes
             // between the 64-element atoms); a K step of 16 is 32 bytes, or 16 rows of 128
@@ -581,6 +584,7 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
         // ------------------------------------------------ results (lane 32 q4 + lane of the tile)
         const int q4 = warp & 3, r = q4 * 32 + lane;
         const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
+        if (KIND != WGRAD) asm volatile("griddepcontrol.wait;" ::: "memory");  // row_pow too
         int n = 0;
         bool ok = true;
         for (int64_t u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
@@ -643,6 +647,112 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
     tc_fence_after();
     if (warp == 13)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+}
+
+// ------------------------------------------------------------------ activations as fp16 rows
+
+// The fp16 copy of bf16 rows that the products above multiply: row m divided by the power of two
+// that brings its largest finite value into [2^14, 2^15). A bf16 value within 2^-31 of the
+// largest is exact in it; what is smaller is off by 2^-40 of the largest at most. One or two
+// tensors of the same rows (the two gradients, which one accumulator sums) share a power; the 8-bit
+// checkpoint is restored on the way. One block per row, which it reads twice (the second time from
+// L1 or L2); bound by the memory traffic of reading 2 (1) and writing 2 bytes a value.
+struct Prep {
+    const __nv_bfloat16 *x[2];    // [M, K] each; NULL for the checkpoint
+    const uint8_t *x8, *xs;       // checkpoint values [M, K] and scale bytes [M, K/32]
+    __half *y[2];                 // [M, K] each
+    float *row_pow;               // [M]
+    int64_t M, K;
+    int tensors;
+};
+
+// a non-finite value takes no part in the maximum
+__device__ __forceinline__ float finite_abs(float v) {
+    const float f = fabsf(v);
+    return f <= 3.4e38f ? f : 0.0f;
+}
+
+template <bool CKPT> __device__ __forceinline__ void prep_read(const Prep &p, int t, int64_t m, int64_t i, float (&v)[8]) {
+    if (CKPT) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p.x8 + m * p.K) + i);
+        const Pow2 f = pow2_of(__ldg(p.xs + m * (p.K >> 5) + (i >> 2)));
+        uint32_t o[4];
+        expand4(w.x, f, o[0], o[1]);
+        expand4(w.y, f, o[2], o[3]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = bf16_lo(o[j]);
+            v[2 * j + 1] = bf16_hi(o[j]);
+        }
+    } else {
+        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p.x[t] + m * p.K) + i);
+        const uint32_t o[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = bf16_lo(o[j]);
+            v[2 * j + 1] = bf16_hi(o[j]);
+        }
+    }
+}
+
+template <bool CKPT> __global__ void __launch_bounds__(256) row_prep_kernel(const Prep p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ float top[8];
+    const int64_t chunks = p.K >> 3;
+    for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
+        float mx = 0.0f;
+        for (int t = 0; t < p.tensors; ++t)
+            for (int64_t i = threadIdx.x; i < chunks; i += 256) {
+                float v[8];
+                prep_read<CKPT>(p, t, m, i, v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) mx = fmaxf(mx, finite_abs(v[j]));
+            }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
+        __syncthreads();  // the previous row's readers of top
+        if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = mx;
+        __syncthreads();
+        mx = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), fmaxf(fmaxf(top[4], top[5]), fmaxf(top[6], top[7])));
+        int e = (int)(__float_as_uint(mx) >> 23);  // the exponent, biased by 127
+        if (e < 15) e = mx == 0.0f ? 141 : 15;      // factors stay finite; a row of zeros has factor 1
+        const float f = __uint_as_float((uint32_t)(268 - e) << 23);  // 2^(14 - (e - 127))
+        if (threadIdx.x == 0) p.row_pow[m] = __uint_as_float((uint32_t)(e - 14) << 23);
+        for (int t = 0; t < p.tensors; ++t)
+            for (int64_t i = threadIdx.x; i < chunks; i += 256) {
+                float v[8];
+                prep_read<CKPT>(p, t, m, i, v);
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const __half2 h = __floats2half2_rn(v[2 * j] * f, v[2 * j + 1] * f);
+                    o[j] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+                reinterpret_cast<uint4 *>(p.y[t] + m * p.K)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+    }
+}
+
+// Place of the fp16 copy (of `values` in all) and of its powers (M of them, and room for the rest
+// of a column group, which the epilogue may read beside them) behind the first `at` bytes.
+struct PrepPlace {
+    size_t y, row_pow, end;
+};
+inline PrepPlace place_prep(size_t at, int64_t values, int64_t M) {
+    PrepPlace q;
+    q.y = (at + 255) / 256 * 256;
+    q.row_pow = (q.y + (size_t)values * 2 + 255) / 256 * 256;
+    q.end = (q.row_pow + ((size_t)M + 16) * sizeof(float) + 255) / 256 * 256;
+    return q;
+}
+
+inline w4_status launch_prep(const Prep &p, cudaStream_t stream) {
+    const unsigned grid = (unsigned)(p.M < (1 << 20) ? p.M : (1 << 20));
+    if (p.x8)
+        row_prep_kernel<true><<<grid, 256, 0, stream>>>(p);
+    else
+        row_prep_kernel<false><<<grid, 256, 0, stream>>>(p);
+    return launch_status();
 }
 
 // ------------------------------------------------------------------ host side
@@ -710,7 +820,7 @@ inline EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// bf16 [rows, width], boxes of 64 columns x box_rows with the 128-byte swizzle; what lies outside
+// 16-bit [rows, width], boxes of 64 columns x box_rows with the 128-byte swizzle; what lies outside
 // reads as zero
 inline bool make_map(CUtensorMap *tm, const void *p, int64_t rows, int64_t width, int box_rows) {
     EncodeTiledFn enc = encode_fn();
@@ -751,7 +861,19 @@ w4_status launch(const Plan &p, const CUtensorMap &tm0, const CUtensorMap &tm1, 
         attr_done.fetch_or(bit, std::memory_order_relaxed);
     }
     const unsigned grid = (unsigned)(p.units < sms ? p.units : sms);
-    expand_gemm_kernel<KIND, GRADS><<<grid, THREADS, smem, stream>>>(tm0, tm1, a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    // FWD and DGRAD follow row_prep_kernel: they may start, and read weights, while it finishes.
+    // Whatever came before on the stream was complete when it began.
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = KIND == WGRAD ? 0 : 1;
+    if (cudaLaunchKernelEx(&cfg, expand_gemm_kernel<KIND, GRADS>, tm0, tm1, a) != cudaSuccess) return W4_ERR_CUDA;
     return launch_status();
 }
 

@@ -67,7 +67,7 @@ unsigned blocks_for(int64_t n) {
 
 W4_API size_t w4a16_gated_workspace_bytes(int64_t M, int64_t H, int64_t K, int group) {
     if (!gated_shape_ok(M, H, K) || !valid_group(group) || K % group != 0 || M <= kFewRows) return 0;
-    return xg::make_plan(xg::FWD, H, M, K, 1, 0, num_sms()).bytes;
+    return xg::place_prep(xg::make_plan(xg::FWD, H, M, K, 1, 0, num_sms()).bytes, M * K, M).end;
 }
 
 W4_API w4_status w4a16_gated(const void *X_bf16, int64_t M, const uint8_t *codes_gate, const uint16_t *scales_gate,
@@ -90,10 +90,22 @@ W4_API w4_status w4a16_gated(const void *X_bf16, int64_t M, const uint8_t *codes
     }
     const int sms = num_sms();
     const xg::Plan p = xg::make_plan(xg::FWD, H, M, K, 1, 0, sms);
-    if (p.bytes && (!workspace || workspace_bytes < p.bytes)) return W4_ERR_WORKSPACE;
+    const xg::PrepPlace q = xg::place_prep(p.bytes, M * K, M);
+    if (!workspace || workspace_bytes < q.end) return W4_ERR_WORKSPACE;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
     CUtensorMap tm;
-    if (!xg::make_map(&tm, X_bf16, M, K, p.NT)) return W4_ERR_CUDA;
+    if (!xg::make_map(&tm, ws + q.y, M, K, p.NT)) return W4_ERR_CUDA;
+    xg::Prep prep = {};
+    prep.x[0] = static_cast<const __nv_bfloat16 *>(X_bf16);
+    prep.y[0] = reinterpret_cast<__half *>(ws + q.y);
+    prep.row_pow = reinterpret_cast<float *>(ws + q.row_pow);
+    prep.M = M;
+    prep.K = K;
+    prep.tensors = 1;
+    st = xg::launch_prep(prep, stream);
+    if (st != W4_OK) return st;
     xg::Args a = {};
+    a.row_pow = prep.row_pow;
     a.w[0] = {codes_gate, scales_gate, zeros_gate};
     a.w[1] = {codes_up, scales_up, zeros_up};
     a.out = Y_bf16;
@@ -107,18 +119,17 @@ W4_API w4_status w4a16_gated(const void *X_bf16, int64_t M, const uint8_t *codes
 
 namespace {
 
-// Workspace of the backward pass: counters and partial sums of its two products (one after the
-// other in the same place), then the restored X.
+// Workspace of the backward pass: counters and partial sums of its two products, then the fp16 rows
+// that each multiplies (X, and after it dG and dU), each time in the same place.
 struct BwdLayout {
     xg::Plan grads, dx;
-    size_t restored, bytes;
+    xg::PrepPlace q;
 };
-BwdLayout bwd_layout(int64_t M, int64_t H, int64_t K, bool ckpt, int sms) {
+BwdLayout bwd_layout(int64_t M, int64_t H, int64_t K, int sms) {
     BwdLayout l;
     l.grads = xg::make_plan(xg::FWD, H, M, K, 1, 0, sms);
     l.dx = xg::make_plan(xg::DGRAD, K, M, H, 2, 0, sms);
-    l.restored = ((l.grads.bytes > l.dx.bytes ? l.grads.bytes : l.dx.bytes) + 255) / 256 * 256;
-    l.bytes = l.restored + (ckpt ? (size_t)M * K * 2 : 0);
+    l.q = xg::place_prep(l.grads.bytes > l.dx.bytes ? l.grads.bytes : l.dx.bytes, M * (K > 2 * H ? K : 2 * H), M);
     return l;
 }
 
@@ -126,7 +137,8 @@ BwdLayout bwd_layout(int64_t M, int64_t H, int64_t K, bool ckpt, int sms) {
 
 W4_API size_t w4a16_gated_bwd_workspace_bytes(int64_t M, int64_t H, int64_t K, int group, int from_ckpt) {
     if (!gated_shape_ok(M, H, K) || H % 8 != 0 || !valid_group(group) || K % group != 0) return 0;
-    return bwd_layout(M, H, K, from_ckpt != 0, num_sms()).bytes;
+    (void)from_ckpt;  // both sources become the same fp16 rows
+    return bwd_layout(M, H, K, num_sms()).q.end;
 }
 
 W4_API w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const uint8_t *X_e4m3, const uint8_t *X_scale,
@@ -148,14 +160,20 @@ W4_API w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const 
                           (const void *)dU_bf16, (const void *)dX_bf16, (const void *)workspace})
         if (p && !aligned16(p)) return W4_ERR_ALIGN;
     const int sms = num_sms();
-    const BwdLayout l = bwd_layout(M, H, K, ckpt, sms);
-    if (l.bytes && (!workspace || workspace_bytes < l.bytes)) return W4_ERR_WORKSPACE;
-    if (ckpt) {
-        void *x = static_cast<uint8_t *>(workspace) + l.restored;
-        st = fp8_ckpt_load(X_e4m3, X_scale, M, K, x, stream);
-        if (st != W4_OK) return st;
-        X_bf16 = x;
-    }
+    const BwdLayout l = bwd_layout(M, H, K, sms);
+    if (!workspace || workspace_bytes < l.q.end) return W4_ERR_WORKSPACE;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    xg::Prep prep = {};
+    prep.x[0] = static_cast<const __nv_bfloat16 *>(X_bf16);
+    prep.x8 = X_e4m3;
+    prep.xs = X_scale;
+    prep.y[0] = reinterpret_cast<__half *>(ws + l.q.y);
+    prep.row_pow = reinterpret_cast<float *>(ws + l.q.row_pow);
+    prep.M = M;
+    prep.K = K;
+    prep.tensors = 1;
+    st = xg::launch_prep(prep, stream);
+    if (st != W4_OK) return st;
     CUtensorMap tm0, tm1;
     xg::Args a = {};
     a.w[0] = {codes_gate, scales_gate, zeros_gate};
@@ -168,10 +186,20 @@ W4_API w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const 
     a.dh = static_cast<const __nv_bfloat16 *>(dH_bf16);
     a.out = dG_bf16;
     a.out2 = static_cast<__nv_bfloat16 *>(dU_bf16);
-    if (!xg::make_map(&tm0, X_bf16, M, K, l.grads.NT)) return W4_ERR_CUDA;
+    a.row_pow = prep.row_pow;
+    if (!xg::make_map(&tm0, prep.y[0], M, K, l.grads.NT)) return W4_ERR_CUDA;
     st = xg::launch<xg::FWD, true>(l.grads, tm0, tm0, a, workspace, sms, stream);
     if (st != W4_OK || !dX_bf16) return st;
-    if (!xg::make_map(&tm0, dG_bf16, M, H, l.dx.NT) || !xg::make_map(&tm1, dU_bf16, M, H, l.dx.NT)) return W4_ERR_CUDA;
+    prep.x[0] = static_cast<const __nv_bfloat16 *>(dG_bf16);
+    prep.x[1] = static_cast<const __nv_bfloat16 *>(dU_bf16);
+    prep.x8 = prep.xs = nullptr;
+    prep.y[1] = prep.y[0] + M * H;
+    prep.K = H;
+    prep.tensors = 2;
+    st = xg::launch_prep(prep, stream);
+    if (st != W4_OK) return st;
+    if (!xg::make_map(&tm0, prep.y[0], M, H, l.dx.NT) || !xg::make_map(&tm1, prep.y[1], M, H, l.dx.NT))
+        return W4_ERR_CUDA;
     a.dh = nullptr;
     a.out = dX_bf16;
     a.out2 = nullptr;
@@ -180,7 +208,7 @@ W4_API w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const 
 
 W4_API size_t w4a16_dgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int group) {
     if (!gated_shape_ok(M, N, K) || N % 8 != 0 || !valid_group(group) || K % group != 0) return 0;
-    return xg::make_plan(xg::DGRAD, K, M, N, 1, 0, num_sms()).bytes;
+    return xg::place_prep(xg::make_plan(xg::DGRAD, K, M, N, 1, 0, num_sms()).bytes, M * N, M).end;
 }
 
 W4_API w4_status w4a16_dgrad(const void *dY_bf16, int64_t M, const uint8_t *codes, const uint16_t *scales,
@@ -195,10 +223,22 @@ W4_API w4_status w4a16_dgrad(const void *dY_bf16, int64_t M, const uint8_t *code
     if (!aligned16(dY_bf16) || !aligned16(dX_bf16) || (workspace && !aligned16(workspace))) return W4_ERR_ALIGN;
     const int sms = num_sms();
     const xg::Plan p = xg::make_plan(xg::DGRAD, K, M, N, 1, 0, sms);
-    if (p.bytes && (!workspace || workspace_bytes < p.bytes)) return W4_ERR_WORKSPACE;
+    const xg::PrepPlace q = xg::place_prep(p.bytes, M * N, M);
+    if (!workspace || workspace_bytes < q.end) return W4_ERR_WORKSPACE;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
     CUtensorMap tm;
-    if (!xg::make_map(&tm, dY_bf16, M, N, p.NT)) return W4_ERR_CUDA;
+    if (!xg::make_map(&tm, ws + q.y, M, N, p.NT)) return W4_ERR_CUDA;
+    xg::Prep prep = {};
+    prep.x[0] = static_cast<const __nv_bfloat16 *>(dY_bf16);
+    prep.y[0] = reinterpret_cast<__half *>(ws + q.y);
+    prep.row_pow = reinterpret_cast<float *>(ws + q.row_pow);
+    prep.M = M;
+    prep.K = N;
+    prep.tensors = 1;
+    st = xg::launch_prep(prep, stream);
+    if (st != W4_OK) return st;
     xg::Args a = {};
+    a.row_pow = prep.row_pow;
     a.w[0] = a.w[1] = {codes, scales, zeros};
     a.out = dX_bf16;
     a.rows = N;

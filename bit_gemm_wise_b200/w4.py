@@ -565,12 +565,12 @@ def alloc_gated_workspace(M, H, K, group, device="cuda"):
 
 
 def alloc_gated_bwd_workspace(M, H, K, group, from_ckpt=False, device="cuda"):
-    """Zero-filled workspace for w4a16_gated_bwd, or None."""
+    """Zero-filled workspace for w4a16_gated_bwd (from_ckpt: X as its 8-bit checkpoint)."""
     return _zeros_or_none(w4a16_gated_bwd_workspace_bytes(M, H, K, group, from_ckpt), device)
 
 
 def alloc_dgrad_workspace(M, N, K, group, device="cuda"):
-    """Zero-filled workspace for w4a16_dgrad, or None."""
+    """Zero-filled workspace for w4a16_dgrad."""
     return _zeros_or_none(w4a16_dgrad_workspace_bytes(M, N, K, group), device)
 
 

@@ -547,16 +547,19 @@ w4_status w4_nf4_gemv(const void *x_bf16, int64_t M, const uint8_t *codes, const
  *   codes, scales, zeros (gate and up)   device, w4_quantize's outputs for Wg[H, K] and Wu[H, K],
  *                the same group and mode for both; zeros NULL for W4_SYM, required for W4_ASYM
  *   Y_bf16       device, bf16 [M, H]
- *   workspace    NULL where w4a16_gated_workspace_bytes(M, H, K, group) is 0, else device scratch of
- *                at least that many bytes (partial sums of outputs whose K range is shared by several
- *                SMs, and their arrival counters). Zero-fill it before its first use; every call that
- *                completes leaves its counters zero again, so one workspace serves any sequence of
- *                calls of that shape or of one that needs no more, on one stream. Calls that may run
+ *   workspace    NULL where w4a16_gated_workspace_bytes(M, H, K, group) is 0 (M <= 16), else device
+ *                scratch of at least that many bytes (an fp16 copy of X; partial sums of outputs whose
+ *                K range is shared by several SMs, and their arrival counters). Zero-fill it before its
+ *                first use; every call that completes leaves its counters zero again, so one workspace
+ *                serves any sequence of calls, of this and of the three entry points below, whose
+ *                queries ask for no more, on one stream. Calls that may run
  *                concurrently need separate workspaces. After a call whose kernel recorded an error
  *                in the device status, zero-fill it again.
  *   M <= 16: the weights enter as exact integers and group scales and zero points are applied in
  *   fp32 (about 1e-6 relative before the one rounding to bf16). M > 16: tcgen05 MMAs on weights
- *   dequantized to bf16 with one rounding (relative 2^-9 per weight) and fp32 accumulation.
+ *   dequantized to fp16 with one rounding (relative 2^-11 per weight; |w| up to 65504) and fp32
+ *   accumulation; X enters as fp16 after each row is divided by a power of two, exact for values
+ *   within 2^-31 of the row's largest.
  *   Outputs must not overlap inputs. Results are bit-identical run to run on a given GPU.
  *   M, H <= 2^24; 32 <= K <= 2^24, K % 32 == 0. Errors: NULL / SHAPE / GROUP / ALIGN / ARG (mode,
  *   act, zeros given for W4_SYM) / WORKSPACE / CUDA.
@@ -578,9 +581,9 @@ w4_status w4a16_gated(const void *X_bf16, int64_t M, const uint8_t *codes_gate, 
  *   dG_bf16, dU_bf16  device, bf16 [M, H], outputs (rounded once; dX is formed from the rounded ones)
  *   dX_bf16      device, bf16 [M, K], output, or NULL where it is not wanted (a first layer)
  *   workspace    as w4a16_gated's, of w4a16_gated_bwd_workspace_bytes(M, H, K, group, from_ckpt) bytes
- *                (0 is possible without a checkpoint); from_ckpt 1 adds the restored X.
- *   Weights are dequantized to bf16 with one rounding, accumulation is fp32. Outputs must not overlap
- *   inputs or each other. H % 8 == 0; other limits and errors as w4a16_gated.
+ *                (from_ckpt 1: X comes as the checkpoint). Always needed.
+ *   Weights, X and the gradients enter the products as w4a16_gated's at M > 16. Outputs must not
+ *   overlap inputs or each other. H % 8 == 0; other limits and errors as w4a16_gated.
  */
 size_t w4a16_gated_bwd_workspace_bytes(int64_t M, int64_t H, int64_t K, int group, int from_ckpt);
 w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const uint8_t *X_e4m3, const uint8_t *X_scale,
@@ -595,8 +598,8 @@ w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const uint8_t
  *   canonical weight (the transposed product reads the same codes; there is no second copy):
  *     dX[m, k] = sum_n dY[m, n] (q[n, k] - z[n, j(k)]) s[n, j(k)]
  *   dY_bf16 [M, N], dX_bf16 [M, K] bf16; codes, scales, zeros as w4_quantize writes them for W[N, K].
- *   workspace as w4a16_gated's, of w4a16_dgrad_workspace_bytes(M, N, K, group) bytes. Weights are
- *   dequantized to bf16 with one rounding, accumulation is fp32.
+ *   workspace as w4a16_gated's, of w4a16_dgrad_workspace_bytes(M, N, K, group) bytes, always needed.
+ *   Weights and dY enter the product as w4a16_gated's do at M > 16.
  *   M <= 2^24; N <= 2^24, N % 8 == 0; K as w4a16_gated. Errors as w4a16_gated.
  */
 size_t w4a16_dgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int group);

@@ -46,6 +46,7 @@ def test_shapes_groups_and_modes(fn, kw, code):
     (dict(wu=(FAKE, FAKE, None)), NULL), (dict(mode=0), ARG), (dict(mode=0, wg=(FAKE, FAKE, None)), ARG),
     (dict(act=2), ARG), (dict(act=-1), ARG), (dict(H=0), SHAPE), (dict(X=FAKE + 2), ALIGN), (dict(Y=FAKE + 8), ALIGN),
     (dict(wg=(FAKE + 4, FAKE, FAKE)), ALIGN), (dict(wu=(FAKE, FAKE, FAKE + 2)), ALIGN), (dict(ws=FAKE + 4, n=1 << 20), ALIGN),
+    (dict(M=17), WORKSPACE), (dict(M=17, ws=FAKE, n=64), WORKSPACE),
 ])
 def test_gated_refuses(kw, code):
     assert gated(**kw) == code
@@ -55,7 +56,7 @@ def test_gated_refuses(kw, code):
     (dict(dH=None), NULL), (dict(dG=None), NULL), (dict(dU=None), NULL), (dict(X=None), NULL),
     (dict(X=None, X8=FAKE), NULL), (dict(X8=FAKE, xs=FAKE), ARG), (dict(xs=FAKE), ARG), (dict(H=12), SHAPE),
     (dict(act=7), ARG), (dict(dX=FAKE + 4), ALIGN), (dict(dH=FAKE + 2), ALIGN),
-    (dict(X=None, X8=FAKE, xs=FAKE), WORKSPACE), (dict(X=None, X8=FAKE, xs=FAKE, ws=FAKE, n=16), WORKSPACE),
+    (dict(), WORKSPACE), (dict(X=None, X8=FAKE, xs=FAKE), WORKSPACE), (dict(X=None, X8=FAKE, xs=FAKE, ws=FAKE, n=16), WORKSPACE),
 ])
 def test_gated_bwd_refuses(kw, code):
     assert bwd(**kw) == code
@@ -64,6 +65,7 @@ def test_gated_bwd_refuses(kw, code):
 @pytest.mark.parametrize("kw,code", [
     (dict(dY=None), NULL), (dict(dX=None), NULL), (dict(w=(FAKE, FAKE, None)), NULL), (dict(mode=0), ARG),
     (dict(N=20), SHAPE), (dict(N=0), SHAPE), (dict(dY=FAKE + 2), ALIGN), (dict(dX=FAKE + 2), ALIGN),
+    (dict(), WORKSPACE), (dict(ws=FAKE, n=100), WORKSPACE),
 ])
 def test_dgrad_refuses(kw, code):
     assert dgrad(**kw) == code

@@ -140,8 +140,9 @@ def test_training_step_of_an_adapter():
     w4.fp8_ckpt_wgrad(t, x8, xs, M, r, K, da, w4.W4_OUT_FP32, w4.alloc_ckpt_wgrad_workspace(M, r, K))
     status_ok()
     xr = R.restored(x8, xs)
-    assert R.rel(y, R.gated(x, wg, wu, g, "silu")) <= 5e-3
-    assert R.rel(dh256, dout.double() @ R.dequant(wd, g)) <= 4e-3
+    # the tolerances of test_gpu_gated.py
+    assert R.rel(y, R.gated(x, wg, wu, g, "silu")) <= 2.6e-3
+    assert R.rel(dh256, dout.double() @ R.dequant(wd, g)) <= 2.6e-3
     rg, ru, rx = R.gated_grads(xr, dh, wg, wu, g, "silu")
-    assert R.rel(dg, rg) <= 5e-3 and R.rel(du, ru) <= 5e-3 and R.rel(dx, rx) <= 6e-3
+    assert R.rel(dg, rg) <= 2.6e-3 and R.rel(du, ru) <= 2.6e-3 and R.rel(dx, rx) <= 3.5e-3
     assert R.rel(da, t.double().t() @ xr) <= 1e-5
