@@ -116,8 +116,9 @@ W4_API w4_status fp8_ckpt_wgrad(const void *dY_bf16, const uint8_t *X_e4m3, cons
     const bool fp32 = (flags & W4_OUT_FP32) != 0;
     const xg::Plan p = wgrad_plan(M, N, K, fp32, sms);
     if (p.bytes && (!workspace || workspace_bytes < p.bytes)) return W4_ERR_WORKSPACE;
-    CUtensorMap tm;
-    if (!xg::make_map(&tm, dY_bf16, M, N, xg::BK)) return W4_ERR_CUDA;
+    xg::Maps tm;
+    if (!xg::make_map(&tm.b[0], dY_bf16, M, N, xg::BK)) return W4_ERR_CUDA;
+    tm.b[1] = tm.b[0];
     xg::Args a = {};
     a.x8 = X_e4m3;
     a.xs = X_scale;
@@ -126,5 +127,5 @@ W4_API w4_status fp8_ckpt_wgrad(const void *dY_bf16, const uint8_t *X_e4m3, cons
     a.K = K;
     a.cols = N;
     a.out_fp32 = fp32 ? 1 : 0;
-    return xg::launch<xg::WGRAD, false>(p, tm, tm, a, workspace, sms, stream);
+    return xg::launch<xg::WGRAD, false>(p, tm, a, workspace, sms, stream);
 }

@@ -14,14 +14,20 @@
 // (MN-major, which the MMA reads as it stands), so the expansion writes the same bytes either way:
 // 16-byte chunks of eight k, at the place that the 128-byte swizzle gives them.
 //
-// One persistent CTA per SM takes units (tile, part of the reduction). Warps 0-7 expand A: thread
-// t takes 32 consecutive values a stage (a row's half block of 64 columns, or a quarter of a row
-// of 128), loaded straight into registers LOOKAHEAD stages ahead, so that every value's group
-// scale is a single one. Warp 12 loads B by TMA, warp 13 issues the MMAs (M = 128, N = the token
-// tile, K = 16), warps 8-11 read the fp32 accumulators (two buffers in TMEM, so that a tile's
-// results leave while the next one is multiplied). Lanes are weights and columns are tokens: a
-// small batch takes a small N and the MMAs shrink with it, while the expansion is shared by all
-// tokens of a tile.
+// One persistent CTA per SM takes units (tile, part of the reduction), stages of 64 along it:
+//   warps 0-7    expand A, in two groups that take the stages in turn. A thread takes two chunks of
+//                32 consecutive values (half of a row's 64 columns, or a quarter of a row of 128), so
+//                that a chunk has a single group scale, and touches shared memory only;
+//   warps 8-15   read the fp32 accumulators (two buffers in TMEM, so that a tile's results leave while
+//                the next one is multiplied) and finish them;
+//   warp 16      loads B by TMA; warp 17 issues the MMAs (M = 128, N = the token tile, K = 16);
+//   warps 18-19  load the codes by TMA, into a ring of their own, fetch the scales and hand the
+//                expansion the constants of each chunk.
+// Lanes are weights and columns are tokens: a small batch takes a small N and the MMAs shrink with
+// it, while the expansion is shared by all tokens of a tile. What bounds a stage is the instructions
+// that the SM issues for it (about 1900 at first: 1.0 us a stage, twice its MMAs): the codes' pairs
+// (i, i + 4) of eight stay in that order, and B's rows (FWD) or the results' lanes (DGRAD, WGRAD)
+// are permuted instead; the constants come ready; a waiting warp sleeps.
 //
 // Where the tiles are too few for the SMs, the reduction is cut into S parts: each part's fp32 sums
 // go to the workspace and the last part to finish adds them in order, so results do not depend on
@@ -39,24 +45,44 @@ namespace xg {
 
 enum Kind { FWD = 0, DGRAD = 1, WGRAD = 2 };
 
-constexpr int THREADS = 448;
 constexpr int EXPAND_WARPS = 8;
+constexpr int GROUPS = 2;                     // of expansion warps; stage i is group i % GROUPS's
+constexpr int WPG = EXPAND_WARPS / GROUPS;    // warps per group
+constexpr int TPG = WPG * 32;                 // threads per group: two chunks of 32 values each
+constexpr int OUT_WARPS = 8;                  // two for each quarter of the lanes, 16 columns in turn
+constexpr int W_OUT = EXPAND_WARPS, W_B = W_OUT + OUT_WARPS, W_MMA = W_B + 1, W_S = W_B + 2;
+constexpr int THREADS = (W_S + GROUPS) * 32;
 constexpr int BK = 64;                        // reduction per stage
 constexpr uint32_t A_BYTES = 128 * BK * 2;    // an expanded stage
 constexpr int MAX_STAGES = 8;
-constexpr uint32_t SMEM_RING = 200 * 1024;
-constexpr int LOOKAHEAD = 4;                  // stages whose codes are on their way to registers
-constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int MIN_STAGES = 4;
+constexpr int MAX_RAW = 16;                   // stages of codes
+constexpr uint32_t SMEM_MAX = 224 * 1024;     // rings and control
+constexpr long long kWaitCycles = 4000000000ll;
 
 struct Smem {
     uint64_t full[MAX_STAGES];    // B landed (TMA bytes) and A expanded (one arrival per warp)
     uint64_t empty[MAX_STAGES];   // the stage's MMAs completed (commit)
+    uint64_t rawf[MAX_RAW];       // codes landed (TMA bytes) and scales stored (the arrival)
+    uint64_t rawe[MAX_RAW];       // the group's warps read them (one arrival per warp)
     uint64_t accf[2];             // an accumulator is complete (commit)
     uint64_t acce[2];             // its columns were read (one arrival per warp)
     uint32_t tmem_base;
     int abort;
 };
 static_assert(sizeof(Smem) <= 1024, "control block");
+
+// one stage of codes (128 x 64 values of 4 or 8 bits), of two words for each of its 256 chunks, and
+// whether the words are constants or what the general expansion starts from
+template <int KIND> struct Raw {
+    static constexpr uint32_t CODES = KIND == WGRAD ? 8192 : 4096;
+    static constexpr uint32_t FLAG = CODES + 2048;
+    static constexpr uint32_t BYTES = FLAG + 128;
+};
+static_assert(TPG == 128 && MIN_STAGES >= GROUPS, "warp roles");
+static_assert(MIN_STAGES * (A_BYTES + 256 * 128 + Raw<FWD>::BYTES) <= SMEM_MAX - 2048 &&
+                  MIN_STAGES * (A_BYTES + 192 * 128 + Raw<WGRAD>::BYTES) <= SMEM_MAX - 2048,
+              "four stages of each ring");
 
 struct Weight {
     const uint8_t *codes;     // [N, K/2]
@@ -72,7 +98,7 @@ struct Args {
     __nv_bfloat16 *out2;      // FWD with dh: dU
     const float *row_pow;     // FWD, DGRAD: the power of two that each token's row was divided by
     float *part;              // partial sums [tile][part][column][lane]
-    uint32_t *cnt;            // arrival counters [tile][4], zero between calls
+    uint32_t *cnt;            // arrival counters [tile][8], zero between calls
     int *status;
     int64_t rows;             // weight rows (FWD, DGRAD: of one source) or tokens (WGRAD)
     int64_t K;                // columns of the expanded matrix
@@ -82,9 +108,14 @@ struct Args {
     int KB, KB0;              // stages of the whole reduction, and of the first source
     int seg;                  // stages that one fp32 accumulator sums at most
     int NT;                   // columns per tile, a multiple of 16
-    int stages;
+    int stages, raws;         // of the expanded operands and of the codes
     uint32_t stage_bytes;
-    int gshift, act, out_fp32;
+    int gshift, asym, act, out_fp32;
+};
+
+// tensor maps: B (DGRAD: of one or two sources) and the codes of A (FWD: gate, up)
+struct Maps {
+    CUtensorMap b[2], q[2];
 };
 
 __device__ __forceinline__ void mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
@@ -123,6 +154,21 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, i
         "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
         : "memory");
 }
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -157,99 +203,95 @@ __device__ __forceinline__ uint32_t hpair(float v) {  // v, rounded to fp16, in 
     return b | (b << 16);
 }
 
-// The scale and zero point of 32 values, as the constants of their expansion. A weight is
-// (q - z) s rounded once to fp16: q enters the mantissa of 1024.0 (1024 + q, exact), less 1024 + z
-// is q - z (exact for |z| <= 1024), times the fp16 scale as it is. Zero points beyond that
-// (groups of one sign far from zero) take ((q - 8) s + c_lo) + c_hi with (8 - z) s = c_hi + c_lo,
-// of which again only the last operation rounds at the weight's size.
-struct Scale {
-    uint32_t s, zc;        // s, 1024 + z
-    uint32_t ch, cl;       // (8 - z) s, split
-    bool far;
-};
-__device__ __forceinline__ Scale scale_of(uint32_t sz) {
-    Scale c;
-    c.s = __byte_perm(sz, 0, 0x1010);
+// A weight is (q - z) s rounded once to fp16: q enters the mantissa of 1024.0 (1024 + q, exact), less
+// 1024 + z is q - z (exact for |z| <= 1024), times the fp16 scale as it is. Zero points from 0 to
+// 1023 have their two constants formed from bits. Any other (groups of one sign far from zero): beyond
+// 1024, ((q - 8) s + c_lo) + c_hi with (8 - z) s = c_hi + c_lo, of which again only the last operation
+// rounds at the weight's size.
+__device__ __forceinline__ bool is_near(uint32_t sz) { return (sz >> 16) < 1024u; }
+__device__ __forceinline__ uint2 near_words(uint32_t sz) {
+    return make_uint2(__byte_perm(sz, 0, 0x1010), __byte_perm(sz + 0x64000000u, 0, 0x3232));
+}
+// Eight codes (nibble i is value i) as fp16 pairs (0, 4), (1, 5), (2, 6), (3, 7).
+__device__ __forceinline__ void expand8(uint32_t w, uint32_t s, uint32_t zc, uint32_t (&o)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = hmul(hsub(((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u, zc), s);
+}
+__device__ __forceinline__ void expand8_any(uint32_t w, uint32_t sz, uint32_t (&o)[4]) {
     const int z = (int)(int16_t)(sz >> 16);
-    c.far = z > 1024 || z < -1024;
-    c.zc = hpair((float)(1024 + z));
-    c.ch = c.cl = 0u;
-    if (c.far) {
-        const float k = (float)(8 - z) * __half2float(__ushort_as_half((unsigned short)(sz & 0xFFFFu)));
-        c.ch = hpair(k);
-        c.cl = hpair(k - __half2float(__ushort_as_half((unsigned short)(c.ch & 0xFFFFu))));
+    const uint32_t s = __byte_perm(sz, 0, 0x1010);
+    if (z <= 1024 && z >= -1024) {
+        expand8(w, s, hpair((float)(1024 + z)), o);
+        return;
     }
-    return c;
-}
-// eight codes (nibble i is value i) as fp16, in order
-__device__ __forceinline__ void expand8(uint32_t w, const Scale &c, uint32_t (&o)[4]) {
-    uint32_t p[4];  // pairs (i, i + 4)
+    const float k = (float)(8 - z) * __half2float(__ushort_as_half((unsigned short)(sz & 0xFFFFu)));
+    const uint32_t ch = hpair(k), cl = hpair(k - __half2float(__ushort_as_half((unsigned short)(ch & 0xFFFFu))));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = ((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u;
-    if (!c.far) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = hmul(hsub(p[i], c.zc), c.s);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = hadd(hfma(hsub(p[i], 0x64086408u), c.s, c.cl), c.ch);
-    }
-    o[0] = __byte_perm(p[0], p[1], 0x5410);
-    o[1] = __byte_perm(p[2], p[3], 0x5410);
-    o[2] = __byte_perm(p[0], p[1], 0x7632);
-    o[3] = __byte_perm(p[2], p[3], 0x7632);
+    for (int i = 0; i < 4; ++i)
+        o[i] = hadd(hfma(hsub(((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u, 0x64086408u), s, cl), ch);
 }
-// four E4M3 bytes as bf16 pairs, times 2^e: the value's seven exponent and mantissa bits under
-// bf16's exponent read as the value times 2^-120 (subnormals too), so one multiplication by
-// 2^(120 + e) restores it exactly; two where that power is past bf16's range.
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t t) {  // bytes in the high halves' places
-    return ((t >> 4) & 0x07F007F0u) | (t & 0x80008000u);
+// Four E4M3 bytes as bf16 pairs (0, 2), (1, 3), times 2^e: the value's seven exponent and mantissa
+// bits under bf16's exponent read as the value times 2^-120 (subnormals too), so one multiplication
+// by 2^(120 + e) restores it exactly; two where that power is past bf16's range.
+__device__ __forceinline__ void expand4(uint32_t w, uint32_t f, uint32_t &o0, uint32_t &o1) {
+    o0 = bmul(((w << 4) & 0x07F007F0u) | ((w << 8) & 0x80008000u), f);
+    o1 = bmul(((w >> 4) & 0x07F007F0u) | (w & 0x80008000u), f);
 }
-struct Pow2 {
-    uint32_t f1, f2;
-    bool two;
-};
-__device__ __forceinline__ Pow2 pow2_of(uint32_t b) {  // scale byte e + 127; 255 is NaN
-    Pow2 p;
-    p.two = b > 134u;
-    const uint32_t one = p.two ? 0x7B80u : (120u + b) << 7;        // 2^120, or 2^(120 + e)
-    const uint32_t two = b == 255u ? 0x7FC0u : b << 7;
-    p.f1 = b == 0u ? 0u : one | (one << 16);
-    p.f2 = two | (two << 16);
-    return p;
+// factors of scale byte b = e + 127 (255 is NaN, 0 is 0): one up to b = 134, else 2^120 and 2^e
+__device__ __forceinline__ uint32_t pow2_one(uint32_t b) {
+    const uint32_t f = b == 0u ? 0u : (120u + b) << 7;
+    return f | (f << 16);
 }
-__device__ __forceinline__ void expand4(uint32_t w, const Pow2 &p, uint32_t &o0, uint32_t &o1) {
-    o0 = bmul(e4m3_pair(__byte_perm(w, 0, 0x1404)), p.f1);
-    o1 = bmul(e4m3_pair(__byte_perm(w, 0, 0x3424)), p.f1);
-    if (p.two) {
-        o0 = bmul(o0, p.f2);
-        o1 = bmul(o1, p.f2);
-    }
+__device__ __forceinline__ uint32_t pow2_two(uint32_t b) {
+    const uint32_t f = b == 255u ? 0x7FC0u : b << 7;
+    return f | (f << 16);
+}
+__device__ __forceinline__ void expand4_any(uint32_t w, uint32_t b, uint32_t &o0, uint32_t &o1) {
+    expand4(w, 0x7B807B80u, o0, o1);
+    o0 = bmul(o0, pow2_two(b));
+    o1 = bmul(o1, pow2_two(b));
 }
 
+// A wait for the whole warp, polled by one lane: every lane's try_wait is an operation of its own
+// on shared memory. Bounded by the SM's clock (4e9 cycles, about 2 s).
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, Smem *sm, int *status) {
     bool r = true;
-    if ((threadIdx.x & 31) == 0) r = mbar_wait_abortable(bar, parity, &sm->abort, status, kWaitNs);
-    r = __shfl_sync(FULL, r ? 1 : 0, 0) != 0;
-    __syncwarp();
-    return r;
-}
-__device__ __forceinline__ bool wait1(uint64_t *bar, uint32_t parity, Smem *sm, int *status) {
-    return mbar_wait_abortable<true>(bar, parity, &sm->abort, status, kWaitNs);
-}
-
-// act(g) and act'(g)
-__device__ __forceinline__ float act_of(float g, int act) {
-    if (act == W4_ACT_SILU) return g / (1.0f + __expf(-g));
-    const float t = tanhf(0.7978845608028654f * (g + 0.044715f * g * g * g));
-    return 0.5f * g * (1.0f + t);
-}
-__device__ __forceinline__ float slope_of(float g, int act) {
-    if (act == W4_ACT_SILU) {
-        const float s = 1.0f / (1.0f + __expf(-g));
-        return s * (1.0f + g * (1.0f - s));
+    if ((threadIdx.x & 31) == 0) {
+        r = mbar_try_wait(bar, parity);
+        if (!r) {
+            const long long t0 = clock64();
+            while (!(r = mbar_try_wait(bar, parity))) {
+                if (*(volatile int *)&sm->abort) break;
+                if (clock64() - t0 > kWaitCycles) {
+                    *(volatile int *)&sm->abort = 1;
+                    record_status(status, W4_ERR_TIMEOUT);
+                    break;
+                }
+            }
+        }
     }
-    const float t = tanhf(0.7978845608028654f * (g + 0.044715f * g * g * g));
-    return 0.5f * (1.0f + t) + 0.5f * g * (1.0f - t * t) * 0.7978845608028654f * (1.0f + 3.0f * 0.044715f * g * g);
+    return __all_sync(FULL, r);
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+// Both activations are g times a logistic function: silu of g itself, the tanh form of gelu of
+// p(g) = 2 sqrt(2/pi) (g + 0.044715 g^3), since (1 + tanh(y)) / 2 = 1 / (1 + exp(-2 y)).
+struct Act {
+    float value, slope;
+};
+__device__ __forceinline__ Act act_of(float g, int act) {
+    const bool gelu = act == W4_ACT_GELU_TANH;
+    const float g2 = 0.07135481282f * g * g;                     // 2 sqrt(2/pi) 0.044715 g^2
+    const float p = gelu ? g * (1.5957691216f + g2) : g;
+    const float dp = gelu ? 1.5957691216f + 3.0f * g2 : 1.0f;     // p'
+    const float s = __fdividef(1.0f, 1.0f + __expf(-p));
+    Act r;
+    r.value = g * s;
+    r.slope = s + r.value * (1.0f - s) * dp;
+    return r;
 }
 
 // A unit: its tile, its part of the reduction (stages [b0, b1)) and its place in the partial sums.
@@ -269,202 +311,262 @@ __device__ __forceinline__ Unit unit_of(const Args &a, int64_t u) {
     return t;
 }
 
-// The values that one thread expands in one stage, and where they come from.
-template <int KIND> struct Chunk {
-    uint4 q[KIND == WGRAD ? 2 : 1];
-    uint32_t s;               // scale and zero point, or the scale byte
-};
-
-template <int KIND> struct Loader {
+// The stages of this CTA's units, one after the other.
+struct Walk {
     int64_t u;
-    int kb, b1;
-    bool ok;                  // this thread's row or columns exist
-    const uint8_t *q;         // its values in stage kb
-    const uint16_t *sc;
-    const int16_t *zp;
-    int64_t k, row;           // its column (in stage 0 for FWD) and row
-
-    __device__ __forceinline__ void begin(const Args &a, int t) {
-        const Unit un = unit_of(a, u);
+    Unit un;
+    int kb;
+    __device__ __forceinline__ bool start(const Args &a) {
+        u = blockIdx.x;
+        if (u >= a.units) return false;
+        un = unit_of(a, u);
         kb = un.b0;
-        b1 = un.b1;
-        if (KIND == FWD) {
-            const int r = t >> 1;
-            const int i = r & 31;
-            row = un.tw * 64 + 16 * (r >> 5) + (i & 15);
-            const Weight &w = a.w[i >> 4];
-            ok = row < a.rows;
-            k = 32 * (t & 1);
-            q = w.codes + row * (a.K >> 1) + (k >> 1);
-            sc = w.scales + row * (a.K >> a.gshift);
-            zp = w.zeros ? w.zeros + row * (a.K >> a.gshift) : nullptr;
-        } else {
-            k = un.tw * 128 + 32 * (t & 3);
-            ok = k < a.K;
-        }
+        return true;
     }
-    __device__ __forceinline__ void load(const Args &a, int t, Chunk<KIND> &c) {
-        if (KIND == FWD) {
-            const int64_t kk = (int64_t)kb * BK + k;
-            if (ok && kk < a.K) {
-                c.q[0] = ldg_stream(q + (int64_t)kb * (BK / 2));
-                const int64_t j = kk >> a.gshift;
-                c.s = (uint32_t)__ldg(sc + j) | ((zp ? (uint32_t)(uint16_t)__ldg(zp + j) : 8u) << 16);
-            } else {
-                c.q[0] = make_uint4(0, 0, 0, 0);
-                c.s = 8u << 16;
-            }
-        } else if (KIND == DGRAD) {
-            const int src = kb >= a.KB0 ? 1 : 0;
-            const int64_t n = (int64_t)(kb - (src ? a.KB0 : 0)) * BK + (t >> 2);
-            if (ok && n < a.rows) {
-                const Weight &w = a.w[src];
-                c.q[0] = ldg_stream(w.codes + n * (a.K >> 1) + (k >> 1));
-                const int64_t j = n * (a.K >> a.gshift) + (k >> a.gshift);
-                c.s = (uint32_t)__ldg(w.scales + j) | ((w.zeros ? (uint32_t)(uint16_t)__ldg(w.zeros + j) : 8u) << 16);
-            } else {
-                c.q[0] = make_uint4(0, 0, 0, 0);
-                c.s = 8u << 16;
-            }
-        } else {
-            const int64_t m = (int64_t)kb * BK + (t >> 2);
-            if (ok && m < a.rows) {
-                const uint8_t *p = a.x8 + m * a.K + k;
-                c.q[0] = ldg_stream(p);
-                c.q[KIND == WGRAD ? 1 : 0] = ldg_stream(p + 16);
-                c.s = __ldg(a.xs + m * (a.K >> 5) + (k >> 5));
-            } else {
-                c.q[0] = c.q[KIND == WGRAD ? 1 : 0] = make_uint4(0, 0, 0, 0);
-                c.s = 127u;
-            }
-        }
-        if (++kb == b1) {
+    __device__ __forceinline__ void skip(const Args &a, int n) {
+        kb += n;
+        while (kb >= un.b1) {
+            const int over = kb - un.b1;
             u += gridDim.x;
-            if (u < a.units) begin(a, t);
+            if (u >= a.units) return;
+            un = unit_of(a, u);
+            kb = un.b0 + over;
         }
     }
 };
 
-// thread t's chunk into the A tile at `base`
-template <int KIND> __device__ __forceinline__ void expand_store(const Chunk<KIND> &c, uint32_t base, int t) {
-    if (KIND == WGRAD) {
-        const int row = t >> 2, x = row & 7, c0 = 4 * (t & 1);
-        const uint32_t at = base + (uint32_t)((t >> 1) & 1) * 8192u + (uint32_t)row * 128u;
-        const Pow2 p = pow2_of(c.s);
-        const bool f = (t & 2) != 0;  // chunk order as for DGRAD below
-        const uint4 q0 = c.q[0], q1 = c.q[KIND == WGRAD ? 1 : 0];
-        const uint4 v[2] = {f ? q1 : q0, f ? q0 : q1};
+// The scales of a stage's 256 chunks, eight a lane of the warp that fetches them: FWD rows lane + 32 i
+// (64 of the gate, then 64 of up), both halves; else rows lane and lane + 32, columns 32 i. fetch()
+// only issues loads, from addresses that always exist, and nothing waits for them before store(): no
+// branch and no arithmetic on a loaded value may stand between the two, or each stage costs a memory
+// latency.
+template <int KIND> struct Scales {
+    uint16_t s[8], z[8];      // fp16 scales and zero points; WGRAD: scale bytes in s
+    uint32_t there;           // bit i: chunk i exists
+
+    __device__ __forceinline__ void fetch(const Args &a, const Walk &w, int lane) {
+        const int64_t J = KIND == WGRAD ? a.K >> 5 : a.K >> a.gshift;
+        const int gmask = (1 << a.gshift) - 1;
+        const int src = KIND == DGRAD && w.kb >= a.KB0 ? 1 : 0;
+        const int64_t kb = w.kb - (src ? a.KB0 : 0);
+        there = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t o[4];
-            expand4(i & 1 ? v[i >> 1].z : v[i >> 1].x, p, o[0], o[1]);
-            expand4(i & 1 ? v[i >> 1].w : v[i >> 1].y, p, o[2], o[3]);
-            sts128(at + (uint32_t)(((c0 + (f ? i ^ 2 : i)) ^ x) << 4), o[0], o[1], o[2], o[3]);
+        for (int i = 0; i < 8; ++i) {
+            // row of the matrix and column of the chunk
+            const int part = KIND == FWD ? i >> 1 : i >> 2, in = KIND == FWD ? i & 1 : i & 3;
+            const int64_t row = KIND == FWD ? w.un.tw * 64 + lane + 32 * (part & 1) : kb * BK + lane + 32 * part;
+            const int64_t k = KIND == FWD ? (int64_t)w.kb * BK + 32 * in : w.un.tw * 128 + 32 * in;
+            const bool ok = row < a.rows && k < a.K;
+            there |= ok ? 1u << i : 0u;
+            if (KIND == WGRAD) {
+                s[i] = __ldg(a.xs + (ok ? row * J + (k >> 5) : 0));
+            } else if (in > 0 && ((32 * in) & gmask) != 0) {
+                s[i] = s[i > 0 ? i - 1 : 0];  // the group of the chunk before
+                z[i] = z[i > 0 ? i - 1 : 0];
+            } else {
+                const Weight &m = a.w[KIND == FWD ? part >> 1 : src];
+                const int64_t j = ok ? row * J + (k >> a.gshift) : 0;
+                s[i] = __ldg(m.scales + j);
+                if (a.asym) z[i] = __ldg(reinterpret_cast<const uint16_t *>(m.zeros) + j);
+            }
         }
-        return;
     }
-    const Scale s = scale_of(c.s);
-    const uint4 v = c.q[0];
-    if (KIND == FWD) {
-        const int row = t >> 1, x = row & 7, c0 = 4 * (t & 1);
-        const uint32_t at = base + (uint32_t)row * 128u;
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    // fp16 scale with the zero point above it, or the scale byte; a chunk that does not exist has
+    // scale 0 (its codes read as zero)
+    __device__ __forceinline__ uint32_t word(const Args &a, int i) const {
+        if (KIND == WGRAD) return (there >> i) & 1u ? (uint32_t)s[i] : 127u;
+        return (there >> i) & 1u ? (uint32_t)s[i] | ((a.asym ? (uint32_t)z[i] : 8u) << 16) : 8u << 16;
+    }
+    // the words that the expansion reads, and the stage's flag
+    __device__ __forceinline__ void store(const Args &a, uint8_t *raw, int lane) const {
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) odd = odd || (KIND == WGRAD ? word(a, i) > 134u : !is_near(word(a, i)));
+        odd = __any_sync(FULL, odd);
+        uint4 *sc = reinterpret_cast<uint4 *>(raw + Raw<KIND>::CODES);  // two chunks each
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            uint32_t o[4];
-            expand8(w[i], s, o);
-            sts128(at + (uint32_t)(((c0 + i) ^ x) << 4), o[0], o[1], o[2], o[3]);
+            uint2 x = make_uint2(word(a, 2 * i), 0u), y = make_uint2(word(a, 2 * i + 1), 0u);
+            if (!odd) {
+                x = KIND == WGRAD ? make_uint2(pow2_one(x.x), 0u) : near_words(x.x);
+                y = KIND == WGRAD ? make_uint2(pow2_one(y.x), 0u) : near_words(y.x);
+            }
+            const int at = KIND == FWD ? lane + 32 * i : 2 * (lane + 32 * (i >> 1)) + (i & 1);
+            sc[at] = make_uint4(x.x, x.y, y.x, y.y);
         }
+        if (lane == 0) *reinterpret_cast<uint32_t *>(raw + Raw<KIND>::FLAG) = odd ? 1u : 0u;
+    }
+};
+
+// Chunk c of a stage is 32 values of a row: FWD row c / 2 (64 of the gate, then 64 of up), half
+// c % 2; else row c / 4, columns 32 (c % 4). In FWD the rows go to the lanes 16 of the gate, 16 of
+// up, 16 of the gate, ..., so that a warp of the results has both of a feature. Its codes are at
+// c * 16 (WGRAD: c * 32) of the stage's codes, its words at c * 8 behind them.
+// A thread's place in that: chunks tt and tt + 128, whose rows in the A tile are 16 (FWD) or 32 apart.
+template <int KIND> struct Place {
+    static constexpr uint32_t NEXT = KIND == FWD ? 16 * 128 : 32 * 128;
+    uint32_t codes, words;    // of the first chunk, from the start of the stage's codes
+    uint32_t swap;            // DGRAD, WGRAD: which half of the codes comes first
+    uint32_t out[4];          // of its four 16-byte pieces, from the start of the A tile
+    __device__ __forceinline__ explicit Place(int tt) {
+        const int r = tt >> 1;
+        const int row = KIND == FWD ? 32 * (r >> 4) + (r & 15) : tt >> 2;
+        // DGRAD, WGRAD: the threads of the second 64 columns write their pieces in the order
+        // 2, 3, 0, 1: the eight threads of a quarter warp then write eight different 16-byte banks
+        const uint32_t flip = KIND != FWD && (tt & 2) ? 32u : 0u;
+        const uint32_t at = (KIND == FWD ? 0u : (uint32_t)((tt >> 1) & 1) * 8192u) + (uint32_t)row * 128u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[i] = at + ((((uint32_t)(tt & 1) << 6) + 16u * i) ^ flip ^ ((uint32_t)(row & 7) << 4));
+        codes = (uint32_t)tt * (KIND == WGRAD ? 32u : 16u);
+        words = Raw<KIND>::CODES + (uint32_t)tt * 8u;
+        swap = flip ? (KIND == WGRAD ? 16u : 8u) : 0u;
+    }
+};
+
+template <int KIND> __device__ __forceinline__ void expand_store(uint32_t raw, uint32_t base, const Place<KIND> &p) {
+    const bool any = lds32(raw + Raw<KIND>::FLAG) != 0u;
+    uint32_t q[2][KIND == WGRAD ? 8 : 4];
+    uint2 k[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t at = raw + p.codes + (KIND == WGRAD ? 128u * 32u : 128u * 16u) * j;
+        if (KIND == FWD) {
+            const uint4 v = lds128(at);
+            q[j][0] = v.x; q[j][1] = v.y; q[j][2] = v.z; q[j][3] = v.w;
+        } else if (KIND == DGRAD) {
+            const uint2 v = lds64(at + p.swap), u = lds64(at + (p.swap ^ 8u));
+            q[j][0] = v.x; q[j][1] = v.y; q[j][2] = u.x; q[j][3] = u.y;
+        } else {
+            const uint4 v = lds128(at + p.swap), u = lds128(at + (p.swap ^ 16u));
+            q[j][0] = v.x; q[j][1] = v.y; q[j][2] = v.z; q[j][3] = v.w;
+            q[j][KIND == WGRAD ? 4 : 0] = u.x; q[j][KIND == WGRAD ? 5 : 1] = u.y;
+            q[j][KIND == WGRAD ? 6 : 2] = u.z; q[j][KIND == WGRAD ? 7 : 3] = u.w;
+        }
+        k[j] = lds64(raw + p.words + 128u * 8u * j);
+    }
+    if (!any) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t o[4];
+                if (KIND == WGRAD) {
+                    expand4(q[j][KIND == WGRAD ? 2 * i : 0], k[j].x, o[0], o[1]);
+                    expand4(q[j][KIND == WGRAD ? 2 * i + 1 : 0], k[j].x, o[2], o[3]);
+                } else {
+                    expand8(q[j][i], k[j].x, k[j].y, o);
+                }
+                sts128(base + p.out[i] + Place<KIND>::NEXT * j, o[0], o[1], o[2], o[3]);
+            }
     } else {
-        const int row = t >> 2, x = row & 7, c0 = 4 * (t & 1);
-        const uint32_t at = base + (uint32_t)((t >> 1) & 1) * 8192u + (uint32_t)row * 128u;
-        // the threads of the second 64 columns write their chunks in the order 2, 3, 0, 1: the
-        // eight threads of a quarter warp then write eight different 16-byte bank groups
-        const bool f = (t & 2) != 0;
-        const uint32_t w[4] = {f ? v.z : v.x, f ? v.w : v.y, f ? v.x : v.z, f ? v.y : v.w};
+        // rare, and kept small
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t o[4];
-            expand8(w[i], s, o);
-            sts128(at + (uint32_t)(((c0 + (f ? i ^ 2 : i)) ^ x) << 4), o[0], o[1], o[2], o[3]);
-        }
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t o[4];
+                if (KIND == WGRAD) {
+                    expand4_any(q[j][KIND == WGRAD ? 2 * i : 0], k[j].x, o[0], o[1]);
+                    expand4_any(q[j][KIND == WGRAD ? 2 * i + 1 : 0], k[j].x, o[2], o[3]);
+                } else {
+                    expand8_any(q[j][i], k[j].x, o);
+                }
+                sts128(base + p.out[i] + Place<KIND>::NEXT * j, o[0], o[1], o[2], o[3]);
+            }
     }
 }
+// The place of value i of eight (FWD, DGRAD) or of four (WGRAD) in what expand8 and expand4 write
+__host__ __device__ __forceinline__ constexpr int value_at8(int place) { return (place >> 1) | ((place & 1) << 2); }
+__host__ __device__ __forceinline__ constexpr int value_at4(int place) { return (place >> 1) | ((place & 1) << 1); }
 
-// Results of columns [c, c + 16) of a tile for this thread's lane.
+// Results of columns [c, c + 16) of a tile, of which n exist, for this thread's lane.
 template <int KIND, bool GRADS>
-__device__ __forceinline__ void emit(const Args &a, const Unit &un, int q4, int lane, int c, int ncols,
-                                     const float (&v)[16], bool add) {
+__device__ __forceinline__ void emit(const Args &a, const Unit &un, int q4, int lane, int c, int n, const float (&v)[16],
+                                     bool add) {
+    const int64_t col = un.tn * a.NT + c;
+    float4 pw[KIND == WGRAD ? 1 : 4];
+    if (KIND != WGRAD) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pw[KIND == WGRAD ? 0 : i] = reinterpret_cast<const float4 *>(a.row_pow + col)[i];
+    }
     if (KIND == FWD) {
         // lanes 0-15 of a warp hold gate rows, lanes 16-31 the same features' up rows: of each pair
         // of tokens the lower half takes the even one and the upper half the odd one
-        const bool up = lane >= 16;
+        const int up = lane >> 4;
         const int64_t h = un.tw * 64 + 16 * q4 + (lane & 15);
-        const int64_t tok0 = un.tn * a.NT + c + (up ? 1 : 0);
+        const int64_t at = (col + up) * a.rows + h, step = 2 * a.rows;
+        const int m = h < a.rows ? n - up : 0;  // this lane's tokens are those with 2 i < m
         float d[8];
         if (GRADS) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                d[i] = (h < a.rows && c + 2 * i + (up ? 1 : 0) < ncols) ? __bfloat162float(a.dh[(tok0 + 2 * i) * a.rows + h])
-                                                                        : 0.0f;
+            for (int i = 0; i < 8; ++i) d[i] = 2 * i < m ? __bfloat162float(a.dh[at + i * step]) : 0.0f;
         }
+        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.out) + at;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float got = __shfl_xor_sync(FULL, up ? v[2 * i] : v[2 * i + 1], 16);
-            const float f = a.row_pow[tok0 + 2 * i];
+            const float4 p4 = pw[KIND == WGRAD ? 0 : i >> 1];
+            const float f = i & 1 ? (up ? p4.w : p4.z) : (up ? p4.y : p4.x);
             const float g = f * (up ? got : v[2 * i]), u = f * (up ? v[2 * i + 1] : got);
-            if (h < a.rows && c + 2 * i + (up ? 1 : 0) < ncols) {
-                const int64_t at = (tok0 + 2 * i) * a.rows + h;
+            const Act t = act_of(g, a.act);
+            if (2 * i < m) {
                 if (GRADS) {
-                    static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(d[i] * u * slope_of(g, a.act));
-                    a.out2[at] = __float2bfloat16_rn(d[i] * act_of(g, a.act));
+                    o[i * step] = __float2bfloat16_rn(d[i] * u * t.slope);
+                    a.out2[at + i * step] = __float2bfloat16_rn(d[i] * t.value);
                 } else {
-                    static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(act_of(g, a.act) * u);
+                    o[i * step] = __float2bfloat16_rn(t.value * u);
                 }
             }
         }
     } else {
-        const int64_t k = un.tw * 128 + 32 * q4 + lane;
+        const int pl = KIND == DGRAD ? (lane & ~7) + value_at8(lane & 7) : (lane & ~3) + value_at4(lane & 3);
+        const int64_t k = un.tw * 128 + 32 * q4 + pl;
         if (k >= a.K) return;
-        const int64_t at = (un.tn * a.NT + c) * a.K + k;
+        const int64_t at = col * a.K + k;
         if (KIND == WGRAD && a.out_fp32) {
             float *o = static_cast<float *>(a.out) + at;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                if (c + i < ncols) o[i * a.K] = add ? o[i * a.K] + v[i] : v[i];
+                if (i < n) o[i * a.K] = add ? o[i * a.K] + v[i] : v[i];
         } else {
             __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.out) + at;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (c + i < ncols)
-                    o[i * a.K] = __float2bfloat16_rn(KIND == DGRAD ? v[i] * a.row_pow[un.tn * a.NT + c + i] : v[i]);
+            for (int i = 0; i < 16; ++i) {
+                const float4 p4 = pw[KIND == WGRAD ? 0 : i >> 2];
+                const float f = (i & 3) == 0 ? p4.x : (i & 3) == 1 ? p4.y : (i & 3) == 2 ? p4.z : p4.w;
+                if (i < n) o[i * a.K] = __float2bfloat16_rn(KIND == DGRAD ? v[i] * f : v[i]);
+            }
         }
     }
 }
 
 template <int KIND, bool GRADS>
-__global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_constant__ CUtensorMap tm0,
-                                                                 const __grid_constant__ CUtensorMap tm1,
+__global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_constant__ Maps tm,
                                                                  const __grid_constant__ Args a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Smem *sm = reinterpret_cast<Smem *>(base + (size_t)a.stages * a.stage_bytes);
+    uint8_t *raw = base + (size_t)a.stages * a.stage_bytes;
+    Smem *sm = reinterpret_cast<Smem *>(raw + (size_t)a.raws * Raw<KIND>::BYTES);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int NS = a.stages;
+    const int NS = a.stages, NR = a.raws;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
-            mbar_init(&sm->full[s], 1 + EXPAND_WARPS);
+            mbar_init(&sm->full[s], 1 + WPG);
             mbar_init(&sm->empty[s], 1);
+        }
+        for (int s = 0; s < NR; ++s) {
+            mbar_init(&sm->rawf[s], 1);
+            mbar_init(&sm->rawe[s], WPG);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sm->accf[b], 1);
-            mbar_init(&sm->acce[b], 4);
+            mbar_init(&sm->acce[b], OUT_WARPS);
         }
         sm->abort = 0;
         fence_mbar_init();
     }
-    if (warp == 13) {
+    if (warp == W_MMA) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sm->tmem_base)),
                      "r"(512u)
                      : "memory");
@@ -477,112 +579,175 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
 
     if (warp < EXPAND_WARPS) {
         // ------------------------------------------------ expansion of A
-        const int t = threadIdx.x;
+        const int grp = warp / WPG;
+        const Place<KIND> place(threadIdx.x % TPG);
         int total = 0;
         for (int64_t u = blockIdx.x; u < a.units; u += gridDim.x) {
             const Unit un = unit_of(a, u);
             total += un.b1 - un.b0;
         }
-        Loader<KIND> ld;
-        ld.u = blockIdx.x;
-        ld.begin(a, t);
-        Chunk<KIND> ch[LOOKAHEAD];
-#pragma unroll
-        for (int j = 0; j < LOOKAHEAD; ++j)
-            if (j < total) ld.load(a, t, ch[j]);
-        int slot = 0;
+        int slot = grp, rs = grp;
+        uint32_t phase = 0, rphase = 0;
+        for (int n = grp; n < total; n += GROUPS) {
+            if (!warp_wait(&sm->rawf[rs], rphase, sm, a.status)) break;
+            if (!warp_wait(&sm->empty[slot], phase ^ 1u, sm, a.status)) break;
+            expand_store<KIND>(smem_addr(raw + (size_t)rs * Raw<KIND>::BYTES), smem_addr(base + (size_t)slot * a.stage_bytes), place);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMA reads them
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sm->full[slot]);
+                mbar_arrive(&sm->rawe[rs]);
+            }
+            slot += GROUPS;
+            if (slot >= NS) { slot -= NS; phase ^= 1u; }
+            rs += GROUPS;
+            if (rs >= NR) { rs -= NR; rphase ^= 1u; }
+        }
+    } else if (warp == W_B) {
+        // ------------------------------------------------ B by TMA
+        if (KIND != WGRAD) asm volatile("griddepcontrol.wait;" ::: "memory");  // B is row_prep_kernel's
+        int slot = 0, issued = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int i = 0; i < total && ok; i += LOOKAHEAD) {
-#pragma unroll
-            for (int j = 0; j < LOOKAHEAD; ++j) {
-                if (i + j >= total) break;
+        const uint32_t bytes = a.stage_bytes - A_BYTES;
+        for (int64_t u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
+            const Unit un = unit_of(a, u);
+            const int c0 = (int)(un.tn * a.NT);
+            for (int kb = un.b0; kb < un.b1; ++kb) {
                 if (!warp_wait(&sm->empty[slot], phase ^ 1u, sm, a.status)) { ok = false; break; }
-                expand_store<KIND>(ch[j], smem_addr(base + (size_t)slot * a.stage_bytes), t);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMA reads them
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm->full[slot]);
-                if (i + j + LOOKAHEAD < total) ld.load(a, t, ch[j]);
-                if (++slot == NS) { slot = 0; phase ^= 1u; }
-            }
-        }
-    } else if (warp == 12) {
-        // ------------------------------------------------ B by TMA
-        if (lane == 0) {
-            if (KIND != WGRAD) asm volatile("griddepcontrol.wait;" ::: "memory");  // B is row_prep_kernel's
-            int slot = 0, issued = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            const uint32_t bytes = a.stage_bytes - A_BYTES;
-            for (int64_t u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
-                const Unit un = unit_of(a, u);
-                const int c0 = (int)(un.tn * a.NT);
-                for (int kb = un.b0; kb < un.b1; ++kb) {
-                    if (!wait1(&sm->empty[slot], phase ^ 1u, sm, a.status)) { ok = false; break; }
+                if (elect_one()) {
                     uint8_t *dst = base + (size_t)slot * a.stage_bytes + A_BYTES;
                     mbar_arrive_expect_tx(&sm->full[slot], bytes);
                     if (KIND == WGRAD) {
                         for (uint32_t o = 0; o < bytes; o += 8192u)  // 64 columns of dY a box
-                            tma_load_2d(dst + o, &tm0, c0 + (int)(o >> 7), kb * BK, &sm->full[slot]);
+                            tma_load_2d(dst + o, &tm.b[0], c0 + (int)(o >> 7), kb * BK, &sm->full[slot]);
                     } else if (KIND == DGRAD && kb >= a.KB0) {
-                        tma_load_2d(dst, &tm1, (kb - a.KB0) * BK, c0, &sm->full[slot]);
+                        tma_load_2d(dst, &tm.b[1], (kb - a.KB0) * BK, c0, &sm->full[slot]);
                     } else {
-                        tma_load_2d(dst, &tm0, kb * BK, c0, &sm->full[slot]);
+                        tma_load_2d(dst, &tm.b[0], kb * BK, c0, &sm->full[slot]);
                     }
-                    ++issued;
-                    if (++slot == NS) { slot = 0; phase ^= 1u; }
                 }
+                __syncwarp();
+                ++issued;
+                if (++slot == NS) { slot = 0; phase ^= 1u; }
             }
-            // no copy may land after the CTA exits
+        }
+        // no copy may land after the CTA exits
+        if (lane == 0)
             for (int i = issued > NS ? issued - NS : 0; i < issued; ++i)
                 (void)mbar_wait_bounded(&sm->full[i % NS], (uint32_t)(i / NS) & 1u, a.status);
-        }
         __syncwarp();
-    } else if (warp == 13) {
+    } else if (warp >= W_S) {
+        // ------------------------------------------------ codes and scales, stage i by warp W_S + i % GROUPS
+        constexpr int AHEAD = 2;  // of the warp's stages, on their way
+        const int first = warp - W_S;
+        int total = 0;
+        for (int64_t u = blockIdx.x; u < a.units; u += gridDim.x) {
+            const Unit un = unit_of(a, u);
+            total += un.b1 - un.b0;
+        }
+        const int own = (total - first + GROUPS - 1) / GROUPS;
+        Walk w, wq;  // of the scales, and of the codes AHEAD stages behind
+        (void)w.start(a);
+        w.skip(a, first);
+        wq = w;
+        Scales<KIND> v[AHEAD];
+#pragma unroll
+        for (int d = 0; d < AHEAD; ++d)
+            if (d < own) {
+                v[d].fetch(a, w, lane);
+                w.skip(a, GROUPS);
+            }
+        int rs = first, issued = 0;
+        uint32_t rphase = 0;
+        bool ok = true;
+        for (int n = 0; n < own && ok; n += AHEAD) {
+#pragma unroll
+            for (int d = 0; d < AHEAD; ++d) {
+                if (n + d >= own) break;
+                if (!warp_wait(&sm->rawe[rs], rphase ^ 1u, sm, a.status)) { ok = false; break; }
+                uint8_t *dst = raw + (size_t)rs * Raw<KIND>::BYTES;
+                v[d].store(a, dst, lane);
+                __syncwarp();
+                if (elect_one()) {
+                    const int tw = (int)wq.un.tw, kb = wq.kb;
+                    mbar_arrive_expect_tx(&sm->rawf[rs], Raw<KIND>::CODES);
+                    if (KIND == FWD) {
+                        tma_load_2d(dst, &tm.q[0], kb * (BK / 2), tw * 64, &sm->rawf[rs]);
+                        tma_load_2d(dst + 2048, &tm.q[1], kb * (BK / 2), tw * 64, &sm->rawf[rs]);
+                    } else if (KIND == DGRAD && kb >= a.KB0) {
+                        tma_load_2d(dst, &tm.q[1], tw * 64, (kb - a.KB0) * BK, &sm->rawf[rs]);
+                    } else {
+                        tma_load_2d(dst, &tm.q[0], tw * (KIND == DGRAD ? 64 : 128), kb * BK, &sm->rawf[rs]);
+                    }
+                }
+                __syncwarp();
+                wq.skip(a, GROUPS);
+                if (n + d + AHEAD < own) {
+                    v[d].fetch(a, w, lane);
+                    w.skip(a, GROUPS);
+                }
+                rs += GROUPS;
+                if (rs >= NR) { rs -= NR; rphase ^= 1u; }
+                ++issued;
+            }
+        }
+        // no copy may land after the CTA exits: this warp's last ones
+        if (lane == 0)
+            for (int i = issued > NR / GROUPS ? issued - NR / GROUPS : 0; i < issued; ++i) {
+                const int st = first + i * GROUPS;
+                (void)mbar_wait_bounded(&sm->rawf[st % NR], (uint32_t)(st / NR) & 1u, a.status);
+            }
+        __syncwarp();
+    } else if (warp == W_MMA) {
         // ------------------------------------------------ MMA issue
-        if (lane == 0) {
-            // D fp32, A and B fp16 (0) or bf16 (1), M = 128, N = NT; A (and B in WGRAD) contiguous
-            // along M (N)
-            const uint32_t idesc = (1u << 4) | (KIND == WGRAD ? (1u << 7) | (1u << 10) : 0u) | (KIND != FWD ? 1u << 15 : 0u) |
-                                   (KIND == WGRAD ? 1u << 16 : 0u) | ((uint32_t)(a.NT >> 3) << 17) | (8u << 24);
-            // low word: address / 16 | leading offset / 16 (K-major: unused; MN-major: 8192 bytes
-            // between the 64-element atoms); a K step of 16 is 32 bytes, or 16 rows of 128
-            constexpr uint32_t alead = KIND == FWD ? 1u << 16 : 512u << 16, astep = KIND == FWD ? 2u : 128u;
-            constexpr uint32_t blead = KIND == WGRAD ? 512u << 16 : 1u << 16, bstep = KIND == WGRAD ? 128u : 2u;
-            int slot = 0, done = 0, n = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int64_t u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
-                const Unit un = unit_of(a, u);
-                for (int s0 = un.b0; s0 < un.b1 && ok; s0 += a.seg, ++n) {
-                    const int s1 = un.b1 - s0 < a.seg ? un.b1 : s0 + a.seg;
-                    const int buf = n & 1;
-                    if (!wait1(&sm->acce[buf], ((uint32_t)(n >> 1) & 1u) ^ 1u, sm, a.status)) { ok = false; break; }
+        // D fp32, A and B fp16 (0) or bf16 (1), M = 128, N = NT; A (and B in WGRAD) contiguous
+        // along M (N)
+        const uint32_t idesc = (1u << 4) | (KIND == WGRAD ? (1u << 7) | (1u << 10) : 0u) | (KIND != FWD ? 1u << 15 : 0u) |
+                               (KIND == WGRAD ? 1u << 16 : 0u) | ((uint32_t)(a.NT >> 3) << 17) | (8u << 24);
+        // low word: address / 16 | leading offset / 16 (K-major: unused; MN-major: 8192 bytes
+        // between the 64-element atoms); a K step of 16 is 32 bytes, or 16 rows of 128
+        constexpr uint32_t alead = KIND == FWD ? 1u << 16 : 512u << 16, astep = KIND == FWD ? 2u : 128u;
+        constexpr uint32_t blead = KIND == WGRAD ? 512u << 16 : 1u << 16, bstep = KIND == WGRAD ? 128u : 2u;
+        const uint32_t sbase = smem_addr(base);
+        int slot = 0, done = 0, n = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int64_t u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
+            const Unit un = unit_of(a, u);
+            for (int s0 = un.b0; s0 < un.b1 && ok; s0 += a.seg, ++n) {
+                const int s1 = un.b1 - s0 < a.seg ? un.b1 : s0 + a.seg;
+                const int buf = n & 1;
+                if (!warp_wait(&sm->acce[buf], ((uint32_t)(n >> 1) & 1u) ^ 1u, sm, a.status)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t d = tmem + (uint32_t)(buf * 256);
+                for (int kb = s0; kb < s1; ++kb) {
+                    if (!warp_wait(&sm->full[slot], phase, sm, a.status)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t d = tmem + (uint32_t)(buf * 256);
-                    for (int kb = s0; kb < s1; ++kb) {
-                        if (!wait1(&sm->full[slot], phase, sm, a.status)) { ok = false; break; }
-                        tc_fence_after();
-                        const uint32_t sa = smem_addr(base + (size_t)slot * a.stage_bytes);
-                        const uint32_t alo = (sa >> 4) | alead, blo = ((sa + A_BYTES) >> 4) | blead;
+                    const uint32_t sa = sbase + (uint32_t)slot * a.stage_bytes;
+                    const uint32_t alo = (sa >> 4) | alead, blo = ((sa + A_BYTES) >> 4) | blead;
+                    if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < BK / 16; ++kk)
                             mma(d, alo + kk * astep, blo + kk * bstep, idesc, kb > s0 || kk > 0 ? 1u : 0u);
                         mma_commit(&sm->empty[slot]);
-                        ++done;
-                        if (++slot == NS) { slot = 0; phase ^= 1u; }
+                        if (kb + 1 == s1) mma_commit(&sm->accf[buf]);
                     }
-                    if (ok) mma_commit(&sm->accf[buf]);
+                    __syncwarp();
+                    ++done;
+                    if (++slot == NS) { slot = 0; phase ^= 1u; }
                 }
             }
-            // no commit may arrive after the CTA exits
+        }
+        // no commit may arrive after the CTA exits
+        if (lane == 0)
             for (int i = done > NS ? done - NS : 0; i < done; ++i)
                 (void)mbar_wait_bounded(&sm->empty[i % NS], (uint32_t)(i / NS) & 1u, a.status);
-        }
         __syncwarp();
     } else {
-        // ------------------------------------------------ results (lane 32 q4 + lane of the tile)
-        const int q4 = warp & 3, r = q4 * 32 + lane;
+        // ------------------------------------------------ results (lane 32 q4 + lane of the tile;
+        // of each quarter's two warps one takes the even groups of 16 columns, one the odd ones)
+        const int q4 = warp & 3, r = q4 * 32 + lane, c0 = 16 * ((warp - W_OUT) >> 2);
         const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
         if (KIND != WGRAD) asm volatile("griddepcontrol.wait;" ::: "memory");  // row_pow too
         int n = 0;
@@ -596,13 +761,14 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
                 const int buf = n & 1;
                 if (!warp_wait(&sm->accf[buf], (uint32_t)(n >> 1) & 1u, sm, a.status)) { ok = false; break; }
                 tc_fence_after();
-                for (int c = 0; c < ncols; c += 16) {
-                    uint32_t raw[16];
-                    tmem_ld16(tl + (uint32_t)(buf * 256 + c), raw);
-                    tmem_wait_ld(raw);
+#pragma unroll 1
+                for (int c = c0; c < ncols; c += 32) {
+                    uint32_t raw16[16];
+                    tmem_ld16(tl + (uint32_t)(buf * 256 + c), raw16);
+                    tmem_wait_ld(raw16);
                     float v[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(raw[i]);
+                    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(raw16[i]);
                     if (a.S > 1) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
@@ -610,7 +776,7 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
                             *p = s0 > un.b0 ? *p + v[i] : v[i];
                         }
                     } else {
-                        emit<KIND, GRADS>(a, un, q4, lane, c, ncols, v, s0 > un.b0);
+                        emit<KIND, GRADS>(a, un, q4, lane, c, ncols - c, v, s0 > un.b0);
                     }
                 }
                 tc_fence_before();
@@ -620,32 +786,35 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
             if (!ok || a.S == 1) continue;
             __threadfence();
             __syncwarp();
+            uint32_t *cnt = a.cnt + un.tile * OUT_WARPS + (warp - W_OUT);
             uint32_t old = 0;
-            if (lane == 0) old = atomicAdd(a.cnt + un.tile * 4 + q4, 1u);
+            if (lane == 0) old = atomicAdd(cnt, 1u);
             old = __shfl_sync(FULL, old, 0);
             if (old != (uint32_t)(a.S - 1)) continue;
-            // the last part of this tile's 32 lanes: add all parts in order
+            // the last part of these lanes and columns: add all parts in order
             __threadfence();
             const float *p0 = a.part + ((size_t)(un.tile * a.S) * a.NT) * 128 + r;
-            for (int c = 0; c < ncols; c += 16) {
+#pragma unroll 1
+            for (int c = c0; c < ncols; c += 32) {
                 float v[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) v[i] = __ldcg(p0 + (size_t)(c + i) * 128);
+#pragma unroll 1
                 for (int s = 1; s < a.S; ++s) {
                     const float *p = p0 + (size_t)s * a.NT * 128;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] += __ldcg(p + (size_t)(c + i) * 128);
                 }
-                emit<KIND, GRADS>(a, un, q4, lane, c, ncols, v, false);
+                emit<KIND, GRADS>(a, un, q4, lane, c, ncols - c, v, false);
             }
-            if (lane == 0) a.cnt[un.tile * 4 + q4] = 0u;  // ready for the next call
+            if (lane == 0) *cnt = 0u;  // ready for the next call
         }
     }
 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 13)
+    if (warp == W_MMA)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
@@ -664,6 +833,7 @@ struct Prep {
     float *row_pow;               // [M]
     int64_t M, K;
     int tensors;
+    int pairs;                    // each eight columns in expand8's order (the reduction of FWD)
 };
 
 // a non-finite value takes no part in the maximum
@@ -675,14 +845,15 @@ __device__ __forceinline__ float finite_abs(float v) {
 template <bool CKPT> __device__ __forceinline__ void prep_read(const Prep &p, int t, int64_t m, int64_t i, float (&v)[8]) {
     if (CKPT) {
         const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p.x8 + m * p.K) + i);
-        const Pow2 f = pow2_of(__ldg(p.xs + m * (p.K >> 5) + (i >> 2)));
-        uint32_t o[4];
-        expand4(w.x, f, o[0], o[1]);
-        expand4(w.y, f, o[2], o[3]);
+        const uint32_t b = __ldg(p.xs + m * (p.K >> 5) + (i >> 2));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = bf16_lo(o[j]);
-            v[2 * j + 1] = bf16_hi(o[j]);
+        for (int j = 0; j < 2; ++j) {
+            uint32_t o[2];
+            expand4_any(j ? w.y : w.x, b, o[0], o[1]);
+            v[4 * j] = bf16_lo(o[0]);
+            v[4 * j + 2] = bf16_hi(o[0]);
+            v[4 * j + 1] = bf16_lo(o[1]);
+            v[4 * j + 3] = bf16_hi(o[1]);
         }
     } else {
         const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p.x[t] + m * p.K) + i);
@@ -725,7 +896,8 @@ template <bool CKPT> __global__ void __launch_bounds__(256) row_prep_kernel(cons
                 uint32_t o[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const __half2 h = __floats2half2_rn(v[2 * j] * f, v[2 * j + 1] * f);
+                    const float lo = p.pairs ? v[j] : v[2 * j], hi = p.pairs ? v[j + 4] : v[2 * j + 1];
+                    const __half2 h = __floats2half2_rn(lo * f, hi * f);
                     o[j] = *reinterpret_cast<const uint32_t *>(&h);
                 }
                 reinterpret_cast<uint4 *>(p.y[t] + m * p.K)[i] = make_uint4(o[0], o[1], o[2], o[3]);
@@ -759,30 +931,41 @@ inline w4_status launch_prep(const Prep &p, cudaStream_t stream) {
 
 struct Plan {
     int64_t Tw, Tn, units;
-    int NT, S, KB, KB0, seg, stages;
+    int NT, S, KB, KB0, seg, stages, raws;
     uint32_t stage_bytes;
     size_t bytes;                   // of the workspace, 0 where S is 1
 };
 
 // The workspace starts with the arrival counters, in a region of one size for all shapes (what
 // one call leaves as partial sums is never another's counter), then holds the partial sums.
-constexpr int64_t MAX_SPLIT_TILES = 4096;
-constexpr size_t CNT_BYTES = MAX_SPLIT_TILES * 4 * sizeof(uint32_t);
+constexpr int64_t MAX_SPLIT_TILES = 2048;
+constexpr size_t CNT_BYTES = MAX_SPLIT_TILES * OUT_WARPS * sizeof(uint32_t);
 
 // lanes: weight rows per projection (FWD) or columns K; cols: the other side; red: length of the
 // reduction (per source), sources 1 or 2; max_rows: reduction that one accumulator may sum.
 inline Plan make_plan(int kind, int64_t lanes, int64_t cols, int64_t red, int sources, int64_t max_rows, int sms) {
     Plan p;
     p.Tw = kind == FWD ? (lanes + 63) / 64 : (lanes + 127) / 128;
-    p.Tn = (cols + 255) / 256;
+    // WGRAD: 192 columns at most, so that four stages of operands and four of codes fit
+    const int64_t widest = kind == WGRAD ? 192 : 256;
+    p.Tn = (cols + widest - 1) / widest;
     p.NT = (int)(((cols + p.Tn - 1) / p.Tn + 15) / 16 * 16);
     p.KB0 = (int)((red + BK - 1) / BK);
     p.KB = p.KB0 * sources;
     p.seg = max_rows > 0 && max_rows / BK < p.KB ? (int)(max_rows / BK) : p.KB;
     const uint32_t bb = kind == WGRAD ? (uint32_t)((p.NT + 63) / 64) * 8192u : (uint32_t)p.NT * 128u;
     p.stage_bytes = A_BYTES + bb;
-    p.stages = (int)(SMEM_RING / p.stage_bytes);
-    if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
+    // A wait tells only neighbouring laps of a ring apart, so each slot's previous lap must be known
+    // to be over when a warp waits for the next one. The codes' ring has a multiple of GROUPS
+    // slots: a slot then belongs to one group and one scale warp, which see its laps in order. The
+    // operands' ring has GROUPS slots at least: a group that filled stage i - GROUPS waited for
+    // the MMAs of the lap before it, which complete in order.
+    const uint32_t rb = kind == WGRAD ? Raw<WGRAD>::BYTES : Raw<FWD>::BYTES, room = SMEM_MAX - 2048;
+    p.stages = MIN_STAGES;
+    p.raws = GROUPS;
+    if (p.stages * p.stage_bytes + 2 * GROUPS * rb <= room) p.raws = 2 * GROUPS;
+    while (p.stages < MAX_STAGES && (p.stages + 1) * p.stage_bytes + p.raws * rb <= room) ++p.stages;
+    while (p.raws + GROUPS <= MAX_RAW && p.stages * p.stage_bytes + (p.raws + GROUPS) * rb <= room) p.raws += GROUPS;
     // Parts of the reduction: the count with the least estimated time. In cycles: a stage takes
     // its MMAs (2 per column) or its expansion (about 300), a unit about 2500 to start and end,
     // and the last part of a tile reads S partial sums at about 60 bytes per cycle.
@@ -820,6 +1003,18 @@ inline EncodeTiledFn encode_fn() {
     return fn;
 }
 
+// 8-bit [rows, width], plain boxes; what lies outside reads as zero
+inline bool make_raw_map(CUtensorMap *tm, const void *p, int64_t rows, int64_t width, int box_width, int box_rows) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)width};
+    const cuuint32_t box[2] = {(cuuint32_t)box_width, (cuuint32_t)box_rows}, es[2] = {1, 1};
+    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(p), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 16-bit [rows, width], boxes of 64 columns x box_rows with the 128-byte swizzle; what lies outside
 // reads as zero
 inline bool make_map(CUtensorMap *tm, const void *p, int64_t rows, int64_t width, int box_rows) {
@@ -834,8 +1029,16 @@ inline bool make_map(CUtensorMap *tm, const void *p, int64_t rows, int64_t width
 }
 
 template <int KIND, bool GRADS>
-w4_status launch(const Plan &p, const CUtensorMap &tm0, const CUtensorMap &tm1, Args a, void *workspace, int sms,
-                 cudaStream_t stream) {
+w4_status launch(const Plan &p, Maps &tm, Args a, void *workspace, int sms, cudaStream_t stream) {
+    bool maps = true;
+    if (KIND == WGRAD) {
+        maps = make_raw_map(&tm.q[0], a.x8, a.rows, a.K, 128, BK);
+        tm.q[1] = tm.q[0];
+    } else {
+        for (int i = 0; i < 2; ++i)
+            maps = maps && make_raw_map(&tm.q[i], a.w[i].codes, a.rows, a.K / 2, KIND == FWD ? BK / 2 : 64, BK);
+    }
+    if (!maps) return W4_ERR_CUDA;
     a.units = p.units;
     a.Tw = (int)p.Tw;
     a.S = p.S;
@@ -843,20 +1046,22 @@ w4_status launch(const Plan &p, const CUtensorMap &tm0, const CUtensorMap &tm1, 
     a.KB0 = p.KB0;
     a.seg = p.seg;
     a.NT = p.NT;
+    a.asym = a.w[0].zeros != nullptr ? 1 : 0;
     a.stages = p.stages;
+    a.raws = p.raws;
     a.stage_bytes = p.stage_bytes;
     a.cnt = static_cast<uint32_t *>(workspace);
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + CNT_BYTES);
     a.status = device_status_ptr();
     if (!a.status) return W4_ERR_CUDA;
-    const int smem = (int)(p.stages * p.stage_bytes) + 2048;
+    const int smem = (int)(p.stages * p.stage_bytes + p.raws * Raw<KIND>::BYTES) + 2048;
     static std::atomic<uint64_t> attr_done{0};  // one bit per device
     int dev = 0;
     cudaGetDevice(&dev);
     const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t)1 << dev : 0;
     if (!(attr_done.load(std::memory_order_relaxed) & bit)) {
         if (cudaFuncSetAttribute(expand_gemm_kernel<KIND, GRADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)SMEM_RING + 2048) != cudaSuccess)
+                                 (int)SMEM_MAX) != cudaSuccess)
             return W4_ERR_CUDA;
         attr_done.fetch_or(bit, std::memory_order_relaxed);
     }
@@ -873,7 +1078,7 @@ w4_status launch(const Plan &p, const CUtensorMap &tm0, const CUtensorMap &tm1, 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = KIND == WGRAD ? 0 : 1;
-    if (cudaLaunchKernelEx(&cfg, expand_gemm_kernel<KIND, GRADS>, tm0, tm1, a) != cudaSuccess) return W4_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, expand_gemm_kernel<KIND, GRADS>, tm, a) != cudaSuccess) return W4_ERR_CUDA;
     return launch_status();
 }
 

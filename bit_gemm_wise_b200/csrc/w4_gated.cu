@@ -29,7 +29,7 @@ __global__ void gated_kernel(const __nv_bfloat16 *x, int64_t M, Weight wg, Weigh
             g = fmaf(xv, weight_at(wg, h, k, K, gshift), g);
             u = fmaf(xv, weight_at(wu, h, k, K, gshift), u);
         }
-        y[i] = __float2bfloat16_rn(act_of(g, act) * u);
+        y[i] = __float2bfloat16_rn(act_of(g, act).value * u);
     }
 }
 
@@ -93,8 +93,9 @@ W4_API w4_status w4a16_gated(const void *X_bf16, int64_t M, const uint8_t *codes
     const xg::PrepPlace q = xg::place_prep(p.bytes, M * K, M);
     if (!workspace || workspace_bytes < q.end) return W4_ERR_WORKSPACE;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    CUtensorMap tm;
-    if (!xg::make_map(&tm, ws + q.y, M, K, p.NT)) return W4_ERR_CUDA;
+    xg::Maps tm;
+    if (!xg::make_map(&tm.b[0], ws + q.y, M, K, p.NT)) return W4_ERR_CUDA;
+    tm.b[1] = tm.b[0];
     xg::Prep prep = {};
     prep.x[0] = static_cast<const __nv_bfloat16 *>(X_bf16);
     prep.y[0] = reinterpret_cast<__half *>(ws + q.y);
@@ -102,6 +103,7 @@ W4_API w4_status w4a16_gated(const void *X_bf16, int64_t M, const uint8_t *codes
     prep.M = M;
     prep.K = K;
     prep.tensors = 1;
+    prep.pairs = 1;
     st = xg::launch_prep(prep, stream);
     if (st != W4_OK) return st;
     xg::Args a = {};
@@ -114,7 +116,7 @@ W4_API w4_status w4a16_gated(const void *X_bf16, int64_t M, const uint8_t *codes
     a.cols = M;
     a.gshift = group_shift(group);
     a.act = act;
-    return xg::launch<xg::FWD, false>(p, tm, tm, a, workspace, sms, stream);
+    return xg::launch<xg::FWD, false>(p, tm, a, workspace, sms, stream);
 }
 
 namespace {
@@ -172,9 +174,10 @@ W4_API w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const 
     prep.M = M;
     prep.K = K;
     prep.tensors = 1;
+    prep.pairs = 1;
     st = xg::launch_prep(prep, stream);
     if (st != W4_OK) return st;
-    CUtensorMap tm0, tm1;
+    xg::Maps tm;
     xg::Args a = {};
     a.w[0] = {codes_gate, scales_gate, zeros_gate};
     a.w[1] = {codes_up, scales_up, zeros_up};
@@ -187,8 +190,9 @@ W4_API w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const 
     a.out = dG_bf16;
     a.out2 = static_cast<__nv_bfloat16 *>(dU_bf16);
     a.row_pow = prep.row_pow;
-    if (!xg::make_map(&tm0, prep.y[0], M, K, l.grads.NT)) return W4_ERR_CUDA;
-    st = xg::launch<xg::FWD, true>(l.grads, tm0, tm0, a, workspace, sms, stream);
+    if (!xg::make_map(&tm.b[0], prep.y[0], M, K, l.grads.NT)) return W4_ERR_CUDA;
+    tm.b[1] = tm.b[0];
+    st = xg::launch<xg::FWD, true>(l.grads, tm, a, workspace, sms, stream);
     if (st != W4_OK || !dX_bf16) return st;
     prep.x[0] = static_cast<const __nv_bfloat16 *>(dG_bf16);
     prep.x[1] = static_cast<const __nv_bfloat16 *>(dU_bf16);
@@ -196,14 +200,15 @@ W4_API w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const 
     prep.y[1] = prep.y[0] + M * H;
     prep.K = H;
     prep.tensors = 2;
+    prep.pairs = 0;
     st = xg::launch_prep(prep, stream);
     if (st != W4_OK) return st;
-    if (!xg::make_map(&tm0, prep.y[0], M, H, l.dx.NT) || !xg::make_map(&tm1, prep.y[1], M, H, l.dx.NT))
+    if (!xg::make_map(&tm.b[0], prep.y[0], M, H, l.dx.NT) || !xg::make_map(&tm.b[1], prep.y[1], M, H, l.dx.NT))
         return W4_ERR_CUDA;
     a.dh = nullptr;
     a.out = dX_bf16;
     a.out2 = nullptr;
-    return xg::launch<xg::DGRAD, false>(l.dx, tm0, tm1, a, workspace, sms, stream);
+    return xg::launch<xg::DGRAD, false>(l.dx, tm, a, workspace, sms, stream);
 }
 
 W4_API size_t w4a16_dgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int group) {
@@ -226,8 +231,9 @@ W4_API w4_status w4a16_dgrad(const void *dY_bf16, int64_t M, const uint8_t *code
     const xg::PrepPlace q = xg::place_prep(p.bytes, M * N, M);
     if (!workspace || workspace_bytes < q.end) return W4_ERR_WORKSPACE;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    CUtensorMap tm;
-    if (!xg::make_map(&tm, ws + q.y, M, N, p.NT)) return W4_ERR_CUDA;
+    xg::Maps tm;
+    if (!xg::make_map(&tm.b[0], ws + q.y, M, N, p.NT)) return W4_ERR_CUDA;
+    tm.b[1] = tm.b[0];
     xg::Prep prep = {};
     prep.x[0] = static_cast<const __nv_bfloat16 *>(dY_bf16);
     prep.y[0] = reinterpret_cast<__half *>(ws + q.y);
@@ -245,5 +251,5 @@ W4_API w4_status w4a16_dgrad(const void *dY_bf16, int64_t M, const uint8_t *code
     a.K = K;
     a.cols = M;
     a.gshift = group_shift(group);
-    return xg::launch<xg::DGRAD, false>(p, tm, tm, a, workspace, sms, stream);
+    return xg::launch<xg::DGRAD, false>(p, tm, a, workspace, sms, stream);
 }
