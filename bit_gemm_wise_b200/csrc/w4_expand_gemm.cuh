@@ -15,19 +15,20 @@
 // 16-byte chunks of eight k, at the place that the 128-byte swizzle gives them.
 //
 // One persistent CTA per SM takes units (tile, part of the reduction), stages of 64 along it:
-//   warps 0-7    expand A, in two groups that take the stages in turn. A thread takes two chunks of
-//                32 consecutive values (half of a row's 64 columns, or a quarter of a row of 128), so
-//                that a chunk has a single group scale, and touches shared memory only;
-//   warps 8-15   read the fp32 accumulators (two buffers in TMEM, so that a tile's results leave while
+//   warps 0-15   expand A, in four groups that take the stages in turn (a wait costs a warp some
+//                200 cycles even when it is over, so a group alone cannot keep up). A thread takes
+//                two chunks of 32 consecutive values (half of a row's 64 columns, or a quarter of a
+//                row of 128), so that a chunk has a single group scale, which it loads itself a turn
+//                ahead;
+//   warps 16-19  read the fp32 accumulators (two buffers in TMEM, so that a tile's results leave while
 //                the next one is multiplied) and finish them;
-//   warp 16      loads B by TMA; warp 17 issues the MMAs (M = 128, N = the token tile, K = 16);
-//   warps 18-19  load the codes by TMA, into a ring of their own, fetch the scales and hand the
-//                expansion the constants of each chunk.
+//   warp 20      loads B by TMA; warp 21 issues the MMAs (M = 128, N = the token tile, K = 16);
+//   warp 22      loads the codes by TMA, into a ring of their own.
 // Lanes are weights and columns are tokens: a small batch takes a small N and the MMAs shrink with
 // it, while the expansion is shared by all tokens of a tile. What bounds a stage is the instructions
 // that the SM issues for it (about 1900 at first: 1.0 us a stage, twice its MMAs): the codes' pairs
 // (i, i + 4) of eight stay in that order, and B's rows (FWD) or the results' lanes (DGRAD, WGRAD)
-// are permuted instead; the constants come ready; a waiting warp sleeps.
+// are permuted instead; a thread's scale addresses move by one addition.
 //
 // Where the tiles are too few for the SMs, the reduction is cut into S parts: each part's fp32 sums
 // go to the workspace and the last part to finish adds them in order, so results do not depend on
@@ -45,13 +46,13 @@ namespace xg {
 
 enum Kind { FWD = 0, DGRAD = 1, WGRAD = 2 };
 
-constexpr int EXPAND_WARPS = 8;
-constexpr int GROUPS = 2;                     // of expansion warps; stage i is group i % GROUPS's
+constexpr int EXPAND_WARPS = 16;
+constexpr int GROUPS = 4;                     // of expansion warps; stage i is group i % GROUPS's
 constexpr int WPG = EXPAND_WARPS / GROUPS;    // warps per group
 constexpr int TPG = WPG * 32;                 // threads per group: two chunks of 32 values each
-constexpr int OUT_WARPS = 8;                  // two for each quarter of the lanes, 16 columns in turn
-constexpr int W_OUT = EXPAND_WARPS, W_B = W_OUT + OUT_WARPS, W_MMA = W_B + 1, W_S = W_B + 2;
-constexpr int THREADS = (W_S + GROUPS) * 32;
+constexpr int OUT_WARPS = 4;                  // one for each quarter of the lanes
+constexpr int W_OUT = EXPAND_WARPS, W_B = W_OUT + OUT_WARPS, W_MMA = W_B + 1, W_Q = W_B + 2;
+constexpr int THREADS = (W_Q + 1) * 32;
 constexpr int BK = 64;                        // reduction per stage
 constexpr uint32_t A_BYTES = 128 * BK * 2;    // an expanded stage
 constexpr int MAX_STAGES = 8;
@@ -63,7 +64,7 @@ constexpr long long kWaitCycles = 4000000000ll;
 struct Smem {
     uint64_t full[MAX_STAGES];    // B landed (TMA bytes) and A expanded (one arrival per warp)
     uint64_t empty[MAX_STAGES];   // the stage's MMAs completed (commit)
-    uint64_t rawf[MAX_RAW];       // codes landed (TMA bytes) and scales stored (the arrival)
+    uint64_t rawf[MAX_RAW];       // codes landed (TMA bytes)
     uint64_t rawe[MAX_RAW];       // the group's warps read them (one arrival per warp)
     uint64_t accf[2];             // an accumulator is complete (commit)
     uint64_t acce[2];             // its columns were read (one arrival per warp)
@@ -72,12 +73,9 @@ struct Smem {
 };
 static_assert(sizeof(Smem) <= 1024, "control block");
 
-// one stage of codes (128 x 64 values of 4 or 8 bits), of two words for each of its 256 chunks, and
-// whether the words are constants or what the general expansion starts from
+// one stage of codes (128 x 64 values of 4 or 8 bits)
 template <int KIND> struct Raw {
-    static constexpr uint32_t CODES = KIND == WGRAD ? 8192 : 4096;
-    static constexpr uint32_t FLAG = CODES + 2048;
-    static constexpr uint32_t BYTES = FLAG + 128;
+    static constexpr uint32_t BYTES = KIND == WGRAD ? 8192 : 4096;
 };
 static_assert(TPG == 128 && MIN_STAGES >= GROUPS, "warp roles");
 static_assert(MIN_STAGES * (A_BYTES + 256 * 128 + Raw<FWD>::BYTES) <= SMEM_MAX - 2048 &&
@@ -98,7 +96,7 @@ struct Args {
     __nv_bfloat16 *out2;      // FWD with dh: dU
     const float *row_pow;     // FWD, DGRAD: the power of two that each token's row was divided by
     float *part;              // partial sums [tile][part][column][lane]
-    uint32_t *cnt;            // arrival counters [tile][8], zero between calls
+    uint32_t *cnt;            // arrival counters [tile][4], zero between calls
     int *status;
     int64_t rows;             // weight rows (FWD, DGRAD: of one source) or tokens (WGRAD)
     int64_t K;                // columns of the expanded matrix
@@ -335,77 +333,55 @@ struct Walk {
     }
 };
 
-// The scales of a stage's 256 chunks, eight a lane of the warp that fetches them: FWD rows lane + 32 i
-// (64 of the gate, then 64 of up), both halves; else rows lane and lane + 32, columns 32 i. fetch()
-// only issues loads, from addresses that always exist, and nothing waits for them before store(): no
-// branch and no arithmetic on a loaded value may stand between the two, or each stage costs a memory
-// latency.
+// The scales of the two chunks that a thread expands in a stage. fetch() only issues loads, from
+// addresses that always exist, and nothing waits for them before word(): no branch and no arithmetic
+// on a loaded value may stand between the two, or each stage costs a memory latency.
 template <int KIND> struct Scales {
-    uint16_t s[8], z[8];      // fp16 scales and zero points; WGRAD: scale bytes in s
-    uint32_t there;           // bit i: chunk i exists
+    uint16_t s[2], z[2];      // fp16 scales and zero points; WGRAD: scale bytes in s
+    bool there[2];
 
-    __device__ __forceinline__ void fetch(const Args &a, const Walk &w, int lane) {
-        const int64_t J = KIND == WGRAD ? a.K >> 5 : a.K >> a.gshift;
-        const int gmask = (1 << a.gshift) - 1;
-        const int src = KIND == DGRAD && w.kb >= a.KB0 ? 1 : 0;
-        const int64_t kb = w.kb - (src ? a.KB0 : 0);
-        there = 0;
+    // k: the thread's column (in stage 0 for FWD); row: its first row (in stage 0 for the others)
+    __device__ __forceinline__ void fetch(const Args &a, const Walk &w, int tt) {
+        if (KIND == WGRAD) {
+            const int64_t J = a.K >> 5, m = (int64_t)w.kb * BK + (tt >> 2), k = w.un.tw * 128 + 32 * (tt & 3);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            // row of the matrix and column of the chunk
-            const int part = KIND == FWD ? i >> 1 : i >> 2, in = KIND == FWD ? i & 1 : i & 3;
-            const int64_t row = KIND == FWD ? w.un.tw * 64 + lane + 32 * (part & 1) : kb * BK + lane + 32 * part;
-            const int64_t k = KIND == FWD ? (int64_t)w.kb * BK + 32 * in : w.un.tw * 128 + 32 * in;
-            const bool ok = row < a.rows && k < a.K;
-            there |= ok ? 1u << i : 0u;
-            if (KIND == WGRAD) {
-                s[i] = __ldg(a.xs + (ok ? row * J + (k >> 5) : 0));
-            } else if (in > 0 && ((32 * in) & gmask) != 0) {
-                s[i] = s[i > 0 ? i - 1 : 0];  // the group of the chunk before
-                z[i] = z[i > 0 ? i - 1 : 0];
-            } else {
-                const Weight &m = a.w[KIND == FWD ? part >> 1 : src];
-                const int64_t j = ok ? row * J + (k >> a.gshift) : 0;
-                s[i] = __ldg(m.scales + j);
-                if (a.asym) z[i] = __ldg(reinterpret_cast<const uint16_t *>(m.zeros) + j);
+            for (int j = 0; j < 2; ++j) {
+                there[j] = k < a.K && m + 32 * j < a.rows;
+                s[j] = __ldg(a.xs + (there[j] ? (m + 32 * j) * J + (k >> 5) : 0));
             }
+            return;
+        }
+        const int64_t J = a.K >> a.gshift;
+        const int src = KIND == DGRAD && w.kb >= a.KB0 ? 1 : 0;
+        const int64_t row = KIND == FWD ? w.un.tw * 64 + (tt >> 1) : (int64_t)(w.kb - (src ? a.KB0 : 0)) * BK + (tt >> 2);
+        const int64_t k = KIND == FWD ? (int64_t)w.kb * BK + 32 * (tt & 1) : w.un.tw * 128 + 32 * (tt & 3);
+        const int64_t at = row * J + (k >> a.gshift);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const Weight &m = a.w[KIND == FWD ? j : src];
+            there[j] = k < a.K && row + (KIND == FWD ? 0 : 32 * j) < a.rows;
+            const int64_t i = there[j] ? at + (KIND == FWD ? 0 : 32 * j) * J : 0;
+            s[j] = __ldg(m.scales + i);
+            // symmetric weights: the scale again, for the sake of one instruction stream
+            z[j] = __ldg((a.asym ? reinterpret_cast<const uint16_t *>(m.zeros) : m.scales) + i);
         }
     }
     // fp16 scale with the zero point above it, or the scale byte; a chunk that does not exist has
     // scale 0 (its codes read as zero)
-    __device__ __forceinline__ uint32_t word(const Args &a, int i) const {
-        if (KIND == WGRAD) return (there >> i) & 1u ? (uint32_t)s[i] : 127u;
-        return (there >> i) & 1u ? (uint32_t)s[i] | ((a.asym ? (uint32_t)z[i] : 8u) << 16) : 8u << 16;
-    }
-    // the words that the expansion reads, and the stage's flag
-    __device__ __forceinline__ void store(const Args &a, uint8_t *raw, int lane) const {
-        bool odd = false;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) odd = odd || (KIND == WGRAD ? word(a, i) > 134u : !is_near(word(a, i)));
-        odd = __any_sync(FULL, odd);
-        uint4 *sc = reinterpret_cast<uint4 *>(raw + Raw<KIND>::CODES);  // two chunks each
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint2 x = make_uint2(word(a, 2 * i), 0u), y = make_uint2(word(a, 2 * i + 1), 0u);
-            if (!odd) {
-                x = KIND == WGRAD ? make_uint2(pow2_one(x.x), 0u) : near_words(x.x);
-                y = KIND == WGRAD ? make_uint2(pow2_one(y.x), 0u) : near_words(y.x);
-            }
-            const int at = KIND == FWD ? lane + 32 * i : 2 * (lane + 32 * (i >> 1)) + (i & 1);
-            sc[at] = make_uint4(x.x, x.y, y.x, y.y);
-        }
-        if (lane == 0) *reinterpret_cast<uint32_t *>(raw + Raw<KIND>::FLAG) = odd ? 1u : 0u;
+    __device__ __forceinline__ uint32_t word(const Args &a, int j) const {
+        if (KIND == WGRAD) return there[j] ? (uint32_t)s[j] : 127u;
+        return there[j] ? (uint32_t)s[j] | ((a.asym ? (uint32_t)z[j] : 8u) << 16) : 8u << 16;
     }
 };
 
 // Chunk c of a stage is 32 values of a row: FWD row c / 2 (64 of the gate, then 64 of up), half
 // c % 2; else row c / 4, columns 32 (c % 4). In FWD the rows go to the lanes 16 of the gate, 16 of
 // up, 16 of the gate, ..., so that a warp of the results has both of a feature. Its codes are at
-// c * 16 (WGRAD: c * 32) of the stage's codes, its words at c * 8 behind them.
+// c * 16 (WGRAD: c * 32) of the stage's codes.
 // A thread's place in that: chunks tt and tt + 128, whose rows in the A tile are 16 (FWD) or 32 apart.
 template <int KIND> struct Place {
     static constexpr uint32_t NEXT = KIND == FWD ? 16 * 128 : 32 * 128;
-    uint32_t codes, words;    // of the first chunk, from the start of the stage's codes
+    uint32_t codes;           // of the first chunk, from the start of the stage's codes
     uint32_t swap;            // DGRAD, WGRAD: which half of the codes comes first
     uint32_t out[4];          // of its four 16-byte pieces, from the start of the A tile
     __device__ __forceinline__ explicit Place(int tt) {
@@ -418,15 +394,17 @@ template <int KIND> struct Place {
 #pragma unroll
         for (int i = 0; i < 4; ++i) out[i] = at + ((((uint32_t)(tt & 1) << 6) + 16u * i) ^ flip ^ ((uint32_t)(row & 7) << 4));
         codes = (uint32_t)tt * (KIND == WGRAD ? 32u : 16u);
-        words = Raw<KIND>::CODES + (uint32_t)tt * 8u;
         swap = flip ? (KIND == WGRAD ? 16u : 8u) : 0u;
     }
 };
 
-template <int KIND> __device__ __forceinline__ void expand_store(uint32_t raw, uint32_t base, const Place<KIND> &p) {
-    const bool any = lds32(raw + Raw<KIND>::FLAG) != 0u;
+template <int KIND>
+__device__ __forceinline__ void expand_store(uint32_t raw, uint32_t base, const Place<KIND> &p, uint32_t s0, uint32_t s1) {
+    const uint32_t sz[2] = {s0, s1};
+    // One branch for the whole warp: scales outside the usual range are rare, and their arithmetic
+    // beside the other in one instruction stream cost a third of the expansion's rate.
+    const bool any = __any_sync(FULL, KIND == WGRAD ? s0 > 134u || s1 > 134u : !is_near(s0) || !is_near(s1));
     uint32_t q[2][KIND == WGRAD ? 8 : 4];
-    uint2 k[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const uint32_t at = raw + p.codes + (KIND == WGRAD ? 128u * 32u : 128u * 16u) * j;
@@ -442,22 +420,23 @@ template <int KIND> __device__ __forceinline__ void expand_store(uint32_t raw, u
             q[j][KIND == WGRAD ? 4 : 0] = u.x; q[j][KIND == WGRAD ? 5 : 1] = u.y;
             q[j][KIND == WGRAD ? 6 : 2] = u.z; q[j][KIND == WGRAD ? 7 : 3] = u.w;
         }
-        k[j] = lds64(raw + p.words + 128u * 8u * j);
     }
     if (!any) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2; ++j) {
+            const uint2 k = KIND == WGRAD ? make_uint2(pow2_one(sz[j]), 0u) : near_words(sz[j]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 uint32_t o[4];
                 if (KIND == WGRAD) {
-                    expand4(q[j][KIND == WGRAD ? 2 * i : 0], k[j].x, o[0], o[1]);
-                    expand4(q[j][KIND == WGRAD ? 2 * i + 1 : 0], k[j].x, o[2], o[3]);
+                    expand4(q[j][KIND == WGRAD ? 2 * i : 0], k.x, o[0], o[1]);
+                    expand4(q[j][KIND == WGRAD ? 2 * i + 1 : 0], k.x, o[2], o[3]);
                 } else {
-                    expand8(q[j][i], k[j].x, k[j].y, o);
+                    expand8(q[j][i], k.x, k.y, o);
                 }
                 sts128(base + p.out[i] + Place<KIND>::NEXT * j, o[0], o[1], o[2], o[3]);
             }
+        }
     } else {
         // rare, and kept small
 #pragma unroll
@@ -466,10 +445,10 @@ template <int KIND> __device__ __forceinline__ void expand_store(uint32_t raw, u
             for (int i = 0; i < 4; ++i) {
                 uint32_t o[4];
                 if (KIND == WGRAD) {
-                    expand4_any(q[j][KIND == WGRAD ? 2 * i : 0], k[j].x, o[0], o[1]);
-                    expand4_any(q[j][KIND == WGRAD ? 2 * i + 1 : 0], k[j].x, o[2], o[3]);
+                    expand4_any(q[j][KIND == WGRAD ? 2 * i : 0], sz[j], o[0], o[1]);
+                    expand4_any(q[j][KIND == WGRAD ? 2 * i + 1 : 0], sz[j], o[2], o[3]);
                 } else {
-                    expand8_any(q[j][i], k[j].x, o);
+                    expand8_any(q[j][i], sz[j], o);
                 }
                 sts128(base + p.out[i] + Place<KIND>::NEXT * j, o[0], o[1], o[2], o[3]);
             }
@@ -579,19 +558,30 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
 
     if (warp < EXPAND_WARPS) {
         // ------------------------------------------------ expansion of A
-        const int grp = warp / WPG;
-        const Place<KIND> place(threadIdx.x % TPG);
+        const int grp = warp / WPG, tt = threadIdx.x % TPG;
+        const Place<KIND> place(tt);
         int total = 0;
         for (int64_t u = blockIdx.x; u < a.units; u += gridDim.x) {
             const Unit un = unit_of(a, u);
             total += un.b1 - un.b0;
         }
+        Walk w;  // of the scales, one of the group's stages ahead
+        (void)w.start(a);
+        w.skip(a, grp);
+        Scales<KIND> next;
+        if (grp < total) next.fetch(a, w, tt);
         int slot = grp, rs = grp;
         uint32_t phase = 0, rphase = 0;
         for (int n = grp; n < total; n += GROUPS) {
+            const uint32_t s0 = next.word(a, 0), s1 = next.word(a, 1);
+            if (n + GROUPS < total) {
+                w.skip(a, GROUPS);
+                next.fetch(a, w, tt);
+            }
             if (!warp_wait(&sm->rawf[rs], rphase, sm, a.status)) break;
             if (!warp_wait(&sm->empty[slot], phase ^ 1u, sm, a.status)) break;
-            expand_store<KIND>(smem_addr(raw + (size_t)rs * Raw<KIND>::BYTES), smem_addr(base + (size_t)slot * a.stage_bytes), place);
+            expand_store<KIND>(smem_addr(raw + (size_t)rs * Raw<KIND>::BYTES), smem_addr(base + (size_t)slot * a.stage_bytes),
+                               place, s0, s1);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMA reads them
             __syncwarp();
             if (lane == 0) {
@@ -637,41 +627,19 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
             for (int i = issued > NS ? issued - NS : 0; i < issued; ++i)
                 (void)mbar_wait_bounded(&sm->full[i % NS], (uint32_t)(i / NS) & 1u, a.status);
         __syncwarp();
-    } else if (warp >= W_S) {
-        // ------------------------------------------------ codes and scales, stage i by warp W_S + i % GROUPS
-        constexpr int AHEAD = 2;  // of the warp's stages, on their way
-        const int first = warp - W_S;
-        int total = 0;
-        for (int64_t u = blockIdx.x; u < a.units; u += gridDim.x) {
-            const Unit un = unit_of(a, u);
-            total += un.b1 - un.b0;
-        }
-        const int own = (total - first + GROUPS - 1) / GROUPS;
-        Walk w, wq;  // of the scales, and of the codes AHEAD stages behind
-        (void)w.start(a);
-        w.skip(a, first);
-        wq = w;
-        Scales<KIND> v[AHEAD];
-#pragma unroll
-        for (int d = 0; d < AHEAD; ++d)
-            if (d < own) {
-                v[d].fetch(a, w, lane);
-                w.skip(a, GROUPS);
-            }
-        int rs = first, issued = 0;
+    } else if (warp == W_Q) {
+        // ------------------------------------------------ codes by TMA
+        int rs = 0, issued = 0;
         uint32_t rphase = 0;
         bool ok = true;
-        for (int n = 0; n < own && ok; n += AHEAD) {
-#pragma unroll
-            for (int d = 0; d < AHEAD; ++d) {
-                if (n + d >= own) break;
+        for (int64_t u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
+            const Unit un = unit_of(a, u);
+            const int tw = (int)un.tw;
+            for (int kb = un.b0; kb < un.b1; ++kb) {
                 if (!warp_wait(&sm->rawe[rs], rphase ^ 1u, sm, a.status)) { ok = false; break; }
-                uint8_t *dst = raw + (size_t)rs * Raw<KIND>::BYTES;
-                v[d].store(a, dst, lane);
-                __syncwarp();
                 if (elect_one()) {
-                    const int tw = (int)wq.un.tw, kb = wq.kb;
-                    mbar_arrive_expect_tx(&sm->rawf[rs], Raw<KIND>::CODES);
+                    uint8_t *dst = raw + (size_t)rs * Raw<KIND>::BYTES;
+                    mbar_arrive_expect_tx(&sm->rawf[rs], Raw<KIND>::BYTES);
                     if (KIND == FWD) {
                         tma_load_2d(dst, &tm.q[0], kb * (BK / 2), tw * 64, &sm->rawf[rs]);
                         tma_load_2d(dst + 2048, &tm.q[1], kb * (BK / 2), tw * 64, &sm->rawf[rs]);
@@ -682,22 +650,14 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
                     }
                 }
                 __syncwarp();
-                wq.skip(a, GROUPS);
-                if (n + d + AHEAD < own) {
-                    v[d].fetch(a, w, lane);
-                    w.skip(a, GROUPS);
-                }
-                rs += GROUPS;
-                if (rs >= NR) { rs -= NR; rphase ^= 1u; }
                 ++issued;
+                if (++rs == NR) { rs = 0; rphase ^= 1u; }
             }
         }
-        // no copy may land after the CTA exits: this warp's last ones
+        // no copy may land after the CTA exits
         if (lane == 0)
-            for (int i = issued > NR / GROUPS ? issued - NR / GROUPS : 0; i < issued; ++i) {
-                const int st = first + i * GROUPS;
-                (void)mbar_wait_bounded(&sm->rawf[st % NR], (uint32_t)(st / NR) & 1u, a.status);
-            }
+            for (int i = issued > NR ? issued - NR : 0; i < issued; ++i)
+                (void)mbar_wait_bounded(&sm->rawf[i % NR], (uint32_t)(i / NR) & 1u, a.status);
         __syncwarp();
     } else if (warp == W_MMA) {
         // ------------------------------------------------ MMA issue
@@ -745,9 +705,8 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
                 (void)mbar_wait_bounded(&sm->empty[i % NS], (uint32_t)(i / NS) & 1u, a.status);
         __syncwarp();
     } else {
-        // ------------------------------------------------ results (lane 32 q4 + lane of the tile;
-        // of each quarter's two warps one takes the even groups of 16 columns, one the odd ones)
-        const int q4 = warp & 3, r = q4 * 32 + lane, c0 = 16 * ((warp - W_OUT) >> 2);
+        // ------------------------------------------------ results (lane 32 q4 + lane of the tile)
+        const int q4 = warp & 3, r = q4 * 32 + lane;
         const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
         if (KIND != WGRAD) asm volatile("griddepcontrol.wait;" ::: "memory");  // row_pow too
         int n = 0;
@@ -762,7 +721,7 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
                 if (!warp_wait(&sm->accf[buf], (uint32_t)(n >> 1) & 1u, sm, a.status)) { ok = false; break; }
                 tc_fence_after();
 #pragma unroll 1
-                for (int c = c0; c < ncols; c += 32) {
+                for (int c = 0; c < ncols; c += 16) {
                     uint32_t raw16[16];
                     tmem_ld16(tl + (uint32_t)(buf * 256 + c), raw16);
                     tmem_wait_ld(raw16);
@@ -795,7 +754,7 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
             __threadfence();
             const float *p0 = a.part + ((size_t)(un.tile * a.S) * a.NT) * 128 + r;
 #pragma unroll 1
-            for (int c = c0; c < ncols; c += 32) {
+            for (int c = 0; c < ncols; c += 16) {
                 float v[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) v[i] = __ldcg(p0 + (size_t)(c + i) * 128);
@@ -938,7 +897,7 @@ struct Plan {
 
 // The workspace starts with the arrival counters, in a region of one size for all shapes (what
 // one call leaves as partial sums is never another's counter), then holds the partial sums.
-constexpr int64_t MAX_SPLIT_TILES = 2048;
+constexpr int64_t MAX_SPLIT_TILES = 4096;
 constexpr size_t CNT_BYTES = MAX_SPLIT_TILES * OUT_WARPS * sizeof(uint32_t);
 
 // lanes: weight rows per projection (FWD) or columns K; cols: the other side; red: length of the
@@ -957,13 +916,12 @@ inline Plan make_plan(int kind, int64_t lanes, int64_t cols, int64_t red, int so
     p.stage_bytes = A_BYTES + bb;
     // A wait tells only neighbouring laps of a ring apart, so each slot's previous lap must be known
     // to be over when a warp waits for the next one. The codes' ring has a multiple of GROUPS
-    // slots: a slot then belongs to one group and one scale warp, which see its laps in order. The
+    // slots: a slot then belongs to one group, which sees its laps in order. The
     // operands' ring has GROUPS slots at least: a group that filled stage i - GROUPS waited for
     // the MMAs of the lap before it, which complete in order.
     const uint32_t rb = kind == WGRAD ? Raw<WGRAD>::BYTES : Raw<FWD>::BYTES, room = SMEM_MAX - 2048;
     p.stages = MIN_STAGES;
     p.raws = GROUPS;
-    if (p.stages * p.stage_bytes + 2 * GROUPS * rb <= room) p.raws = 2 * GROUPS;
     while (p.stages < MAX_STAGES && (p.stages + 1) * p.stage_bytes + p.raws * rb <= room) ++p.stages;
     while (p.raws + GROUPS <= MAX_RAW && p.stages * p.stage_bytes + (p.raws + GROUPS) * rb <= room) p.raws += GROUPS;
     // Parts of the reduction: the count with the least estimated time. In cycles: a stage takes
