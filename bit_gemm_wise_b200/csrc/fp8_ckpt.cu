@@ -1,8 +1,10 @@
 // The 8-bit activation checkpoint (fp8_ckpt_save, fp8_ckpt_load) and the weight gradient from it
 // (fp8_ckpt_wgrad).
 //
-// First form of the checkpoint: one thread per block of 32 columns. The weight gradient is a
-// product of w4_expand_gemm.cuh.
+// Save and load are bound by memory traffic: 2 bytes read (written) and 1 + 1/32 written (read) a
+// value. A thread of the save takes 8 values, four threads a block of 32 (two shuffles for its
+// maximum); a thread of the load 16 values. Four such pieces of a block's range are in flight per
+// thread. The weight gradient is a product of w4_expand_gemm.cuh.
 #include "w4_common.cuh"
 #include "w4_expand_gemm.cuh"
 
@@ -13,14 +15,6 @@ namespace ckpt {
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // e in [-126, 127]
 
-// 2^e of a scale byte; 255 is NaN
-__device__ __forceinline__ float scale_of(uint8_t b) { return b == 255 ? __int_as_float(0x7fffffff) : pow2((int)b - 127); }
-
-__device__ __forceinline__ float e4m3(uint8_t v) {
-    const __half_raw h = __nv_cvt_fp8_to_halfraw(v, __NV_E4M3);
-    return __half2float(__half(h));
-}
-
 // e of the block maximum `amax` (finite): the smallest e >= -124 with amax <= 448 * 2^e. 448 is
 // 1.75 * 2^8, so e is the exponent of amax less 8, and one more where its mantissa is over 1.75.
 __device__ __forceinline__ int exponent_of(float amax) {
@@ -28,29 +22,83 @@ __device__ __forceinline__ int exponent_of(float amax) {
     return e < -124 ? -124 : e;
 }
 
-__global__ void save_kernel(const __nv_bfloat16 *x, int64_t n, uint8_t *x8, uint8_t *scale) {
-    for (int64_t b = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; b < n; b += (int64_t)gridDim.x * blockDim.x) {
-        float amax = 0.0f;
-        bool bad = false;
-        for (int i = 0; i < 32; ++i) {
-            const float v = fabsf(__bfloat162float(x[b * 32 + i]));
-            bad = bad || !(v <= 3.4e38f);
-            amax = fmaxf(amax, v);
+constexpr int THREADS = 256, PIECES = 4;  // pieces of THREADS x 8 (save) or 16 (load) values
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {  // two values, round to nearest even
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+// n: blocks of 32 values
+__global__ void __launch_bounds__(THREADS) save_kernel(const uint4 *__restrict__ x, int64_t n, uint2 *__restrict__ x8,
+                                                       uint8_t *__restrict__ scale) {
+    const int64_t i0 = (int64_t)blockIdx.x * (THREADS * PIECES) + threadIdx.x, end = 4 * n;
+    uint4 v[PIECES];
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) {
+        const int64_t i = i0 + p * THREADS;
+        v[p] = i < end ? ldg_stream(x + i) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) {
+        const int64_t i = i0 + p * THREADS;
+        const uint32_t w[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
+        // the largest magnitude, by its bits (a block that is not finite has 0x7F80 or more)
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = __vmaxu2(top, w[j] & 0x7FFF7FFFu);
+        top = __vmaxu2(top, __shfl_xor_sync(FULL, top, 1));
+        top = __vmaxu2(top, __shfl_xor_sync(FULL, top, 2));
+        const uint32_t mx = max(top & 0xFFFFu, top >> 16);
+        const bool bad = mx >= 0x7F80u;
+        const int e = bad ? 0 : exponent_of(__uint_as_float(mx << 16));
+        const float f = pow2(-e);
+        // x 2^-e is exact; at e = 120 values stop at 240: 256 * 2^120 would leave bf16's range
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float lo = bf16_lo(w[j]) * f, hi = bf16_hi(w[j]) * f;
+            if (e == 120) {
+                lo = fminf(fmaxf(lo, -240.0f), 240.0f);
+                hi = fminf(fmaxf(hi, -240.0f), 240.0f);
+            }
+            o[j] = bad ? 0x7F7Fu : e4m3x2(lo, hi);
         }
-        const int e = bad ? 0 : exponent_of(amax);
-        const float top = e == 120 ? 240.0f : 448.0f;  // 256 * 2^120 would leave bf16's range
-        for (int i = 0; i < 32; ++i)
-            x8[b * 32 + i] = bad ? 0x7F
-                                 : (uint8_t)__nv_cvt_float_to_fp8(
-                                       fminf(fmaxf(__bfloat162float(x[b * 32 + i]) * pow2(-e), -top), top),
-                                       __NV_SATFINITE, __NV_E4M3);
-        scale[b] = bad ? 255 : (uint8_t)(e + 127);
+        if (i < end) {
+            x8[i] = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+            if ((threadIdx.x & 3) == 0) scale[i >> 2] = bad ? 255 : (uint8_t)(e + 127);
+        }
     }
 }
 
-__global__ void load_kernel(const uint8_t *x8, const uint8_t *scale, int64_t n, __nv_bfloat16 *x) {
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x)
-        x[i] = __float2bfloat16_rn(e4m3(x8[i]) * scale_of(scale[i >> 5]));
+// n: pieces of 16 values
+__global__ void __launch_bounds__(THREADS) load_kernel(const uint4 *__restrict__ x8, const uint8_t *__restrict__ scale,
+                                                       int64_t n, uint4 *__restrict__ x) {
+    const int64_t i0 = (int64_t)blockIdx.x * (THREADS * PIECES) + threadIdx.x;
+    uint4 v[PIECES];
+    uint32_t b[PIECES];
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) {
+        const int64_t i = i0 + p * THREADS;
+        v[p] = i < n ? ldg_stream(x8 + i) : make_uint4(0, 0, 0, 0);
+        b[p] = i < n ? __ldg(scale + (i >> 1)) : 127u;
+    }
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) {
+        const int64_t i = i0 + p * THREADS;
+        const uint32_t w[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
+        uint32_t o[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t even, odd;
+            xg::expand4_any(w[j], b[p], even, odd);
+            o[2 * j] = __byte_perm(even, odd, 0x5410);
+            o[2 * j + 1] = __byte_perm(even, odd, 0x7632);
+        }
+        if (i < n) {
+            x[2 * i] = make_uint4(o[0], o[1], o[2], o[3]);
+            x[2 * i + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+    }
 }
 
 }  // namespace ckpt
@@ -66,9 +114,10 @@ bool ckpt_shape_ok(int64_t M, int64_t K) {
     return M >= 1 && M <= kMaxRows && K >= 32 && K <= kMaxRows && K % 32 == 0;
 }
 
-unsigned blocks_for(int64_t n) {
-    const int64_t b = (n + 255) / 256;
-    return (unsigned)(b < 65536 ? b : 65536);
+// blocks of THREADS threads with PIECES pieces each; 0 where the grid would be too large
+unsigned blocks_for(int64_t pieces) {
+    const int64_t b = (pieces + ckpt::THREADS * ckpt::PIECES - 1) / (ckpt::THREADS * ckpt::PIECES);
+    return b <= 0x7fffffff ? (unsigned)b : 0u;
 }
 
 }  // namespace
@@ -79,7 +128,10 @@ W4_API w4_status fp8_ckpt_save(const void *X_bf16, int64_t M, int64_t K, uint8_t
     if (!ckpt_shape_ok(M, K)) return W4_ERR_SHAPE;
     if (!aligned16(X_bf16) || !aligned16(X_e4m3) || !aligned16(X_scale)) return W4_ERR_ALIGN;
     const int64_t n = M * (K / 32);
-    ckpt::save_kernel<<<blocks_for(n), 256, 0, stream>>>((const __nv_bfloat16 *)X_bf16, n, X_e4m3, X_scale);
+    const unsigned grid = blocks_for(4 * n);
+    if (!grid) return W4_ERR_SHAPE;
+    ckpt::save_kernel<<<grid, ckpt::THREADS, 0, stream>>>(static_cast<const uint4 *>(X_bf16), n,
+                                                          reinterpret_cast<uint2 *>(X_e4m3), X_scale);
     return launch_status();
 }
 
@@ -88,7 +140,11 @@ W4_API w4_status fp8_ckpt_load(const uint8_t *X_e4m3, const uint8_t *X_scale, in
     if (!X_bf16 || !X_e4m3 || !X_scale) return W4_ERR_NULL;
     if (!ckpt_shape_ok(M, K)) return W4_ERR_SHAPE;
     if (!aligned16(X_bf16) || !aligned16(X_e4m3) || !aligned16(X_scale)) return W4_ERR_ALIGN;
-    ckpt::load_kernel<<<blocks_for(M * K), 256, 0, stream>>>(X_e4m3, X_scale, M * K, (__nv_bfloat16 *)X_bf16);
+    const int64_t n = M * (K / 16);
+    const unsigned grid = blocks_for(n);
+    if (!grid) return W4_ERR_SHAPE;
+    ckpt::load_kernel<<<grid, ckpt::THREADS, 0, stream>>>(reinterpret_cast<const uint4 *>(X_e4m3), X_scale, n,
+                                                          static_cast<uint4 *>(X_bf16));
     return launch_status();
 }
 

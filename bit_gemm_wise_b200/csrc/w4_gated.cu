@@ -1,8 +1,21 @@
 // The gated feed-forward block over canonical 4-bit weights (w4a16_gated), its backward pass
 // (w4a16_gated_bwd) and the input gradient of a 4-bit layer (w4a16_dgrad).
 //
-// The products of many rows are those of w4_expand_gemm.cuh; for up to 16 rows w4a16_gated has one
-// thread per output, the weight dequantized to fp32 as it is read.
+// The products of many rows are those of w4_expand_gemm.cuh. Up to 16 rows w4a16_gated is a decode
+// step, which reads every weight once for a handful of products, so the kernel below is built around
+// the weight stream:
+//   - a warp takes 16 features (the 16 gate rows and the 16 up rows of a matrix fragment each) and
+//     every W-th block of 128 columns; its codes go from memory straight into registers (16 bytes a
+//     lane and row where the group allows), a block ahead, and are there the A operand of
+//     mma.m16n8k16, which may sum its 16 columns in any order: lane t of a row's four holds a quarter
+//     of each group. The M <= 8 (16) tokens are the N = 8 columns of one (two) products;
+//   - two shifts' worth of work per weight: a nibble OR-ed into the mantissa of bf16 128.0 is 128 + q,
+//     exactly; the products with bf16 activations are exact too, and
+//         y += s (sum (128 + q) x - (128 + z) sum x)
+//     in fp32 after each group, with sum x from a product with a matrix of ones. (The legacy mma is
+//     no bottleneck here: 24 products for 4096 weights; a tcgen05 tile would spend its time loading
+//     TMEM.)
+//   - the W warps' sums meet in shared memory, in order; the activation and the product follow there.
 #include "w4_common.cuh"
 #include "w4_expand_gemm.cuh"
 
@@ -12,25 +25,199 @@ namespace gated {
 using xg::Weight;
 using xg::act_of;
 
-__device__ __forceinline__ float weight_at(const Weight &w, int64_t n, int64_t k, int64_t K, int gshift) {
-    const int q = (w.codes[n * (K / 2) + (k >> 1)] >> (4 * (k & 1))) & 15;
-    const int64_t j = n * (K >> gshift) + (k >> gshift);
-    const int z = w.zeros ? w.zeros[j] : 8;
-    return (float)(q - z) * __half2float(__ushort_as_half(w.scales[j]));
+constexpr int WARPS = 8;          // of a block: they share its features' columns
+constexpr int SCALE_WORDS = 6144;  // of shared memory for a run of groups (24 KB; 18 KB hold the sums)
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// codes i and i + 4 of eight as the bf16 pair 128 + q
+__device__ __forceinline__ uint32_t codes_pair(uint32_t w, int i) { return ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u; }
+
+struct FewArgs {
+    const __nv_bfloat16 *x;   // [M, K]
+    Weight w[2];              // gate, up
+    __nv_bfloat16 *y;         // [M, H]
+    int64_t H, K;
+    int M, gshift, act;
+    int run;                  // groups whose scales are in shared memory at a time
+};
+
+// A lane's codes of one block of 128 columns: rows r and r + 8 of the gate's and the up's fragment,
+// 16 bytes each. GB is the group, or 128 for groups of 256 (whose halves share a scale): lane t has
+// bytes [GB/8 t, GB/8 (t + 1)) of each group's GB/2.
+template <int GB> struct Codes {
+    uint32_t w[2][2][4];
+    __device__ __forceinline__ void load(const uint8_t *const (&p)[2][2], int64_t k0, int64_t K, int t) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint8_t *q = p[m][h] + (k0 >> 1) + t * (GB / 8);
+                if (GB == 128) {
+                    const uint4 v = ldg_stream(q);
+                    w[m][h][0] = v.x; w[m][h][1] = v.y; w[m][h][2] = v.z; w[m][h][3] = v.w;
+                } else {
+#pragma unroll
+                    for (int g = 0; g < 128 / GB; ++g) {
+                        const bool in = k0 + g * GB < K;  // the last block may be cut at a group
+                        if (GB == 64) {
+                            const uint2 v = in ? __ldg(reinterpret_cast<const uint2 *>(q + 32 * g)) : make_uint2(0, 0);
+                            w[m][h][(2 * g) & 3] = v.x;
+                            w[m][h][(2 * g + 1) & 3] = v.y;
+                        } else {
+                            w[m][h][g & 3] = in ? __ldg(reinterpret_cast<const uint32_t *>(q + 16 * g)) : 0u;
+                        }
+                    }
+                }
+            }
+    }
+};
+
+template <int GB, int NB>
+__global__ void __launch_bounds__(WARPS * 32) gated_few_kernel(const FewArgs a) {
+    extern __shared__ uint32_t sc[];                         // [group of the run][32 rows]: s | z << 16
+    __shared__ float sums[WARPS][NB][32][9];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
+    const int64_t h0 = (int64_t)blockIdx.x * 16, J = a.K >> a.gshift;
+    const uint8_t *p[2][2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t row = h0 + r + 8 * h;
+            p[m][h] = a.w[m].codes + (row < a.H ? row : a.H - 1) * (a.K >> 1);
+        }
+    const __nv_bfloat16 *xp[NB];
+    bool tok[NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+        tok[n] = r + 8 * n < a.M;
+        xp[n] = a.x + (int64_t)(tok[n] ? r + 8 * n : 0) * a.K;
+    }
+    float acc[2][NB][4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
+
+    const int64_t blocks = (a.K + 127) / 128, per_run = ((int64_t)a.run << a.gshift) / 128;
+    Codes<GB> next;
+    int64_t b = warp;
+    if (b < blocks) next.load(p, b * 128, a.K, t);
+    for (int64_t run0 = 0; run0 < blocks; run0 += per_run) {
+        const int64_t run1 = run0 + per_run < blocks ? run0 + per_run : blocks;
+        const int64_t j0 = (run0 * 128) >> a.gshift, j1 = j0 + a.run < J ? j0 + a.run : J;
+        __syncthreads();  // the previous run's readers
+        for (int row = warp; row < 32; row += WARPS) {
+            const Weight &w = a.w[row >> 4];
+            const int64_t h = h0 + (row & 15) < a.H ? h0 + (row & 15) : a.H - 1;
+            for (int64_t j = j0 + lane; j < j1; j += 32) {
+                const uint32_t s = __ldg(w.scales + h * J + j);
+                const uint32_t z = w.zeros ? (uint32_t)(uint16_t)__ldg(w.zeros + h * J + j) : 8u;
+                sc[(j - j0) * 32 + row] = s | (z << 16);
+            }
+        }
+        __syncthreads();
+        for (; b < run1; b += WARPS) {
+            const Codes<GB> c = next;
+            if (b + WARPS < blocks) next.load(p, (b + WARPS) * 128, a.K, t);
+            const int64_t k0 = b * 128;
+#pragma unroll
+            for (int g = 0; g < 128 / GB; ++g) {
+                if (k0 + g * GB >= a.K) break;
+                float P[2][NB][4], X[NB][4];
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) P[0][n][i] = P[1][n][i] = X[n][i] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < GB / 32; ++i) {
+                    const int wi = (GB / 32) * g + i;
+                    uint32_t xb[NB][4];
+#pragma unroll
+                    for (int n = 0; n < NB; ++n) {
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (tok[n]) v = __ldg(reinterpret_cast<const uint4 *>(xp[n] + k0 + g * GB + (GB / 4) * t + 8 * i));
+                        xb[n][0] = __byte_perm(v.x, v.z, 0x5410);
+                        xb[n][1] = __byte_perm(v.x, v.z, 0x7632);
+                        xb[n][2] = __byte_perm(v.y, v.w, 0x5410);
+                        xb[n][3] = __byte_perm(v.y, v.w, 0x7632);
+                    }
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            const uint32_t a0 = codes_pair(c.w[m][0][wi], 2 * s), a1 = codes_pair(c.w[m][1][wi], 2 * s);
+                            const uint32_t a2 = codes_pair(c.w[m][0][wi], 2 * s + 1), a3 = codes_pair(c.w[m][1][wi], 2 * s + 1);
+#pragma unroll
+                            for (int n = 0; n < NB; ++n) mma16816(P[m][n], a0, a1, a2, a3, xb[n][2 * s], xb[n][2 * s + 1]);
+                        }
+#pragma unroll
+                        for (int n = 0; n < NB; ++n)
+                            mma16816(X[n], 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, xb[n][2 * s], xb[n][2 * s + 1]);
+                    }
+                }
+                const uint32_t *sg = sc + (((k0 + g * GB) >> a.gshift) - j0) * 32;
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t sz = sg[16 * m + r + 8 * h];
+                        const float s = __half2float(__ushort_as_half((unsigned short)(sz & 0xFFFFu)));
+                        const float z = (float)(128 + (int)(int16_t)(sz >> 16));
+#pragma unroll
+                        for (int n = 0; n < NB; ++n)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                acc[m][n][2 * h + i] = fmaf(s, fmaf(-z, X[n][i], P[m][n][2 * h + i]), acc[m][n][2 * h + i]);
+                    }
+            }
+        }
+    }
+    // rows r and r + 8 of each fragment, tokens 2 t and 2 t + 1
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sums[warp][n][16 * m + r + 8 * (i >> 1)][2 * t + (i & 1)] = acc[m][n][i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < NB * 128; i += WARPS * 32) {
+        const int f = i & 15, c = (i >> 4) & 7, n = i >> 7;
+        float g = 0.0f, u = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            g += sums[w][n][f][c];
+            u += sums[w][n][16 + f][c];
+        }
+        if (h0 + f < a.H && 8 * n + c < a.M)
+            a.y[(int64_t)(8 * n + c) * a.H + h0 + f] = __float2bfloat16_rn(act_of(g, a.act).value * u);
+    }
 }
 
-__global__ void gated_kernel(const __nv_bfloat16 *x, int64_t M, Weight wg, Weight wu, int64_t H, int64_t K, int gshift,
-                             int act, __nv_bfloat16 *y) {
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < M * H; i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t m = i / H, h = i % H;
-        float g = 0.0f, u = 0.0f;
-        for (int64_t k = 0; k < K; ++k) {
-            const float xv = __bfloat162float(x[m * K + k]);
-            g = fmaf(xv, weight_at(wg, h, k, K, gshift), g);
-            u = fmaf(xv, weight_at(wu, h, k, K, gshift), u);
-        }
-        y[i] = __float2bfloat16_rn(act_of(g, act).value * u);
-    }
+template <int GB> w4_status launch_few(const FewArgs &a, cudaStream_t stream) {
+    const unsigned grid = (unsigned)((a.H + 15) / 16);
+    const size_t smem = (size_t)a.run * 32 * sizeof(uint32_t);
+    if (a.M <= 8)
+        gated_few_kernel<GB, 1><<<grid, WARPS * 32, smem, stream>>>(a);
+    else
+        gated_few_kernel<GB, 2><<<grid, WARPS * 32, smem, stream>>>(a);
+    return launch_status();
+}
+
+inline w4_status gated_few(FewArgs a, int group, cudaStream_t stream) {
+    // a run holds whole blocks of 128 columns and of the group
+    const int64_t J = a.K >> a.gshift;
+    a.run = SCALE_WORDS / 32;
+    if (J < a.run) a.run = (int)((J + 3) / 4 * 4);
+    return group == 32 ? launch_few<32>(a, stream) : group == 64 ? launch_few<64>(a, stream) : launch_few<128>(a, stream);
 }
 
 }  // namespace gated
@@ -58,11 +245,6 @@ w4_status weight_ok(const uint8_t *codes, const uint16_t *scales, const int16_t 
     return W4_OK;
 }
 
-unsigned blocks_for(int64_t n) {
-    const int64_t b = (n + 255) / 256;
-    return (unsigned)(b < 65536 ? b : 65536);
-}
-
 }  // namespace
 
 W4_API size_t w4a16_gated_workspace_bytes(int64_t M, int64_t H, int64_t K, int group) {
@@ -83,10 +265,17 @@ W4_API w4_status w4a16_gated(const void *X_bf16, int64_t M, const uint8_t *codes
     if (st != W4_OK) return st;
     if (!aligned16(X_bf16) || !aligned16(Y_bf16) || (workspace && !aligned16(workspace))) return W4_ERR_ALIGN;
     if (M <= kFewRows) {
-        gated::gated_kernel<<<blocks_for(M * H), 256, 0, stream>>>(
-            (const __nv_bfloat16 *)X_bf16, M, {codes_gate, scales_gate, zeros_gate}, {codes_up, scales_up, zeros_up}, H,
-            K, group_shift(group), act, (__nv_bfloat16 *)Y_bf16);
-        return launch_status();
+        gated::FewArgs f = {};
+        f.x = static_cast<const __nv_bfloat16 *>(X_bf16);
+        f.w[0] = {codes_gate, scales_gate, zeros_gate};
+        f.w[1] = {codes_up, scales_up, zeros_up};
+        f.y = static_cast<__nv_bfloat16 *>(Y_bf16);
+        f.H = H;
+        f.K = K;
+        f.M = (int)M;
+        f.gshift = group_shift(group);
+        f.act = act;
+        return gated::gated_few(f, group, stream);
     }
     const int sms = num_sms();
     const xg::Plan p = xg::make_plan(xg::FWD, H, M, K, 1, 0, sms);
