@@ -377,41 +377,39 @@ def _act(act) -> int:
     return int(act)
 
 
-def _buf(name, t, need):
-    """Pointer of a contiguous CUDA tensor that must hold `need` bytes; None stays None. The C
-    entry points take bare pointers, so a tensor of the wrong size is caught here."""
+def _buf(name, t, need, dev):
+    """Pointer of a contiguous tensor on CUDA device `dev` that must hold `need` bytes; None stays
+    None. The C entry points take bare pointers, so a tensor of the wrong size or of another
+    device is caught here."""
     if t is None:
         return None
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor on the first argument's device")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.numel() * t.element_size() < need:
-        raise ValueError(f"{name} holds {t.numel() * t.element_size()} bytes, {need} are needed")
+    if t.nbytes < need:
+        raise ValueError(f"{name} holds {t.nbytes} bytes, {need} are needed")
     return t.data_ptr()
 
 
-def _weight4(name, w, N, K, group):
+def _weight4(name, w, N, K, group, dev):
     """Pointers of a canonical weight (codes, scales, zeros or None) of W[N, K]."""
-    codes, scales, zeros = w
-    if group not in (32, 64, 128, 256) or N < 1 or K < 1:
-        J = 0  # refused by the C entry point
-    else:
-        J = N * (K // group) * 2
-    return (_buf(name + " codes", codes, N * K // 2), _buf(name + " scales", scales, J),
-            _buf(name + " zeros", zeros, J))
+    # a group or size that the C entry point refuses asks for nothing here
+    J = N * (K // group) * 2 if group in (32, 64, 128, 256) and N > 0 and K > 0 else 0
+    return (_buf(name, w[0], N * K // 2, dev), _buf(name, w[1], J, dev), _buf(name, w[2], J, dev))
 
 
-def _ws(workspace):
-    if workspace is None:
-        return None, 0
-    return _ptr(workspace), workspace.numel() * workspace.element_size()
+def _ws(workspace, dev):
+    return (None, 0) if workspace is None else (_buf("workspace", workspace, 0, dev), workspace.nbytes)
 
 
-def _check_device(first, *rest):
-    for t in rest:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}: one device is wanted")
+def _call(name, dev, stream, *args):
+    """The C entry point `name` on device `dev`, on `stream` or that device's current stream."""
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return _call(name, dev, stream, *args)
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    _check(name, getattr(lib(), name)(*args, s))
 
 
 def w4a16_gated_workspace_bytes(M, H, K, group) -> int:
@@ -422,13 +420,10 @@ def w4a16_gated(X, M, gate, up, H, K, group, mode, act, Y, workspace=None, strea
     """Y = act(X Wg^T) * (X Wu^T). gate, up: (codes, scales, zeros) as w4_quantize writes them
     (zeros None for symmetric weights); act: "silu" or "gelu_tanh"; workspace:
     alloc_gated_workspace(M, H, K, group). Runs on X's device."""
-    x, y = _buf("X", X, 2 * M * K), _buf("Y", Y, 2 * M * H)
-    g, u = _weight4("gate", gate, H, K, group), _weight4("up", up, H, K, group)
-    _check_device(X, Y, workspace, *gate, *up)
-    ws, n = _ws(workspace)
-    with torch.cuda.device(X.device):
-        rc = lib().w4a16_gated(x, M, *g, *u, H, K, group, _mode(mode), _act(act), y, ws, n, _stream(stream))
-    _check("w4a16_gated", rc)
+    d = X.get_device()
+    _call("w4a16_gated", d, stream, _buf("X", X, 2 * M * K, d), M, *_weight4("gate", gate, H, K, group, d),
+          *_weight4("up", up, H, K, group, d), H, K, group, _mode(mode), _act(act), _buf("Y", Y, 2 * M * H, d),
+          *_ws(workspace, d))
 
 
 def w4a16_gated_bwd_workspace_bytes(M, H, K, group, from_ckpt) -> int:
@@ -440,15 +435,12 @@ def w4a16_gated_bwd(dH, M, gate, up, H, K, group, mode, act, dG, dU, dX, workspa
     """dG, dU (the gradients of X Wg^T and X Wu^T) and dX from dH, with X as bf16 or as the 8-bit
     checkpoint X8, x_scale (fp8_ckpt_save). dX may be None. workspace:
     alloc_gated_bwd_workspace(M, H, K, group, from_ckpt=X8 is not None)."""
-    p = [_buf("dH", dH, 2 * M * H), _buf("X", X, 2 * M * K), _buf("X8", X8, M * K),
-         _buf("x_scale", x_scale, M * (K // 32))]
-    o = [_buf("dG", dG, 2 * M * H), _buf("dU", dU, 2 * M * H), _buf("dX", dX, 2 * M * K)]
-    g, u = _weight4("gate", gate, H, K, group), _weight4("up", up, H, K, group)
-    _check_device(dH, X, X8, x_scale, dG, dU, dX, workspace, *gate, *up)
-    ws, n = _ws(workspace)
-    with torch.cuda.device(dH.device):
-        rc = lib().w4a16_gated_bwd(*p, M, *g, *u, H, K, group, _mode(mode), _act(act), *o, ws, n, _stream(stream))
-    _check("w4a16_gated_bwd", rc)
+    d = dH.get_device()
+    _call("w4a16_gated_bwd", d, stream, _buf("dH", dH, 2 * M * H, d), _buf("X", X, 2 * M * K, d),
+          _buf("X8", X8, M * K, d), _buf("x_scale", x_scale, M * (K // 32), d), M,
+          *_weight4("gate", gate, H, K, group, d), *_weight4("up", up, H, K, group, d), H, K, group, _mode(mode),
+          _act(act), _buf("dG", dG, 2 * M * H, d), _buf("dU", dU, 2 * M * H, d), _buf("dX", dX, 2 * M * K, d),
+          *_ws(workspace, d))
 
 
 def w4a16_dgrad_workspace_bytes(M, N, K, group) -> int:
@@ -458,31 +450,23 @@ def w4a16_dgrad_workspace_bytes(M, N, K, group) -> int:
 def w4a16_dgrad(dY, M, weight, N, K, group, mode, dX, workspace=None, stream=None):
     """dX = dY W of a 4-bit linear layer; weight: (codes, scales, zeros) of W[N, K]; workspace:
     alloc_dgrad_workspace(M, N, K, group)."""
-    dy, dx = _buf("dY", dY, 2 * M * N), _buf("dX", dX, 2 * M * K)
-    w = _weight4("weight", weight, N, K, group)
-    _check_device(dY, dX, workspace, *weight)
-    ws, n = _ws(workspace)
-    with torch.cuda.device(dY.device):
-        rc = lib().w4a16_dgrad(dy, M, *w, N, K, group, _mode(mode), dx, ws, n, _stream(stream))
-    _check("w4a16_dgrad", rc)
+    d = dY.get_device()
+    _call("w4a16_dgrad", d, stream, _buf("dY", dY, 2 * M * N, d), M, *_weight4("weight", weight, N, K, group, d), N, K,
+          group, _mode(mode), _buf("dX", dX, 2 * M * K, d), *_ws(workspace, d))
 
 
 def fp8_ckpt_save(X, M, K, X8, x_scale, stream=None):
     """The 8-bit checkpoint of X [M, K]: X8 uint8 (or float8_e4m3fn) [M, K], x_scale uint8 [M, K/32]."""
-    p = _buf("X", X, 2 * M * K), M, K, _buf("X8", X8, M * K), _buf("x_scale", x_scale, M * (K // 32))
-    _check_device(X, X8, x_scale)
-    with torch.cuda.device(X.device):
-        rc = lib().fp8_ckpt_save(*p, _stream(stream))
-    _check("fp8_ckpt_save", rc)
+    d = X.get_device()
+    _call("fp8_ckpt_save", d, stream, _buf("X", X, 2 * M * K, d), M, K, _buf("X8", X8, M * K, d),
+          _buf("x_scale", x_scale, M * (K // 32), d))
 
 
 def fp8_ckpt_load(X8, x_scale, M, K, X, stream=None):
     """X [M, K] bf16 from its 8-bit checkpoint, exactly."""
-    p = _buf("X8", X8, M * K), _buf("x_scale", x_scale, M * (K // 32)), M, K, _buf("X", X, 2 * M * K)
-    _check_device(X8, X, x_scale)
-    with torch.cuda.device(X8.device):
-        rc = lib().fp8_ckpt_load(*p, _stream(stream))
-    _check("fp8_ckpt_load", rc)
+    d = X8.get_device()
+    _call("fp8_ckpt_load", d, stream, _buf("X8", X8, M * K, d), _buf("x_scale", x_scale, M * (K // 32), d), M, K,
+          _buf("X", X, 2 * M * K, d))
 
 
 def fp8_ckpt_wgrad_workspace_bytes(M, N, K) -> int:
@@ -492,13 +476,10 @@ def fp8_ckpt_wgrad_workspace_bytes(M, N, K) -> int:
 def fp8_ckpt_wgrad(dY, X8, x_scale, M, N, K, dW, flags=0, workspace=None, stream=None):
     """dW [N, K] = dY^T X from the 8-bit checkpoint of X; bf16, or fp32 with W4_OUT_FP32 in flags;
     workspace: alloc_ckpt_wgrad_workspace(M, N, K)."""
-    p = (_buf("dY", dY, 2 * M * N), _buf("X8", X8, M * K), _buf("x_scale", x_scale, M * (K // 32)), M, N, K,
-         _buf("dW", dW, (4 if int(flags) & W4_OUT_FP32 else 2) * N * K))
-    _check_device(dY, X8, x_scale, dW, workspace)
-    ws, n = _ws(workspace)
-    with torch.cuda.device(dY.device):
-        rc = lib().fp8_ckpt_wgrad(*p, int(flags), ws, n, _stream(stream))
-    _check("fp8_ckpt_wgrad", rc)
+    d, f = dY.get_device(), int(flags)
+    _call("fp8_ckpt_wgrad", d, stream, _buf("dY", dY, 2 * M * N, d), _buf("X8", X8, M * K, d),
+          _buf("x_scale", x_scale, M * (K // 32), d), M, N, K, _buf("dW", dW, (4 if f & W4_OUT_FP32 else 2) * N * K, d),
+          f, *_ws(workspace, d))
 
 
 def w4_device_status(stream=None) -> int:
