@@ -58,7 +58,7 @@ constexpr uint32_t A_BYTES = 128 * BK * 2;    // an expanded stage
 constexpr int MAX_STAGES = 8;
 constexpr int MIN_STAGES = 4;
 constexpr int MAX_RAW = 16;                   // stages of codes
-constexpr uint32_t SMEM_MAX = 224 * 1024;     // rings and control
+constexpr uint32_t SMEM_MAX = 227 * 1024;     // rings, control and alignment
 constexpr long long kWaitCycles = 4000000000ll;
 
 struct Smem {
@@ -70,16 +70,18 @@ struct Smem {
     uint64_t acce[2];             // its columns were read (one arrival per warp)
     uint32_t tmem_base;
     int abort;
+    alignas(16) float row_pow[OUT_WARPS][256];  // of the current tile's tokens, a copy for each warp
 };
-static_assert(sizeof(Smem) <= 1024, "control block");
+constexpr uint32_t CONTROL = 5 * 1024;
+static_assert(sizeof(Smem) <= CONTROL, "control block");
 
 // one stage of codes (128 x 64 values of 4 or 8 bits)
 template <int KIND> struct Raw {
     static constexpr uint32_t BYTES = KIND == WGRAD ? 8192 : 4096;
 };
 static_assert(TPG == 128 && MIN_STAGES >= GROUPS, "warp roles");
-static_assert(MIN_STAGES * (A_BYTES + 256 * 128 + Raw<FWD>::BYTES) <= SMEM_MAX - 2048 &&
-                  MIN_STAGES * (A_BYTES + 192 * 128 + Raw<WGRAD>::BYTES) <= SMEM_MAX - 2048,
+static_assert(MIN_STAGES * (A_BYTES + 256 * 128 + Raw<FWD>::BYTES) <= SMEM_MAX - CONTROL - 1024 &&
+                  MIN_STAGES * (A_BYTES + 192 * 128 + Raw<WGRAD>::BYTES) <= SMEM_MAX - CONTROL - 1024,
               "four stages of each ring");
 
 struct Weight {
@@ -95,15 +97,16 @@ struct Args {
     void *out;                // FWD: Y or dG [cols, rows]; DGRAD: dX [cols, K]; WGRAD: dW [cols, K]
     __nv_bfloat16 *out2;      // FWD with dh: dU
     const float *row_pow;     // FWD, DGRAD: the power of two that each token's row was divided by
-    float *part;              // partial sums [tile][part][column][lane]
+    float *part;              // partial sums [tile][part][column / 4][lane][4]
     uint32_t *cnt;            // arrival counters [tile][4], zero between calls
     int *status;
     int64_t rows;             // weight rows (FWD, DGRAD: of one source) or tokens (WGRAD)
     int64_t K;                // columns of the expanded matrix
     int64_t cols;             // tokens, or dY's columns (WGRAD)
-    int64_t units;            // Tw * Tn * S
+    int units;                // Tw * Tn * S
     int Tw, S;                // lane tiles, parts of the reduction
     int KB, KB0;              // stages of the whole reduction, and of the first source
+    int part_kb, part_more;   // stages of a part, and how many parts have one more
     int seg;                  // stages that one fp32 accumulator sums at most
     int NT;                   // columns per tile, a multiple of 16
     int stages, raws;         // of the expanded operands and of the codes
@@ -293,43 +296,52 @@ __device__ __forceinline__ Act act_of(float g, int act) {
 }
 
 // A unit: its tile, its part of the reduction (stages [b0, b1)) and its place in the partial sums.
+// 32 bits throughout: the plan has fewer than 2^31 units, and a 64-bit division costs hundreds of
+// instructions (six of them at a kernel's start took 4 us).
 struct Unit {
-    int64_t tile, tw, tn, s;
+    uint32_t tile, tw, tn, s;
     int b0, b1;
 };
-__device__ __forceinline__ Unit unit_of(const Args &a, int64_t u) {
+__device__ __forceinline__ Unit unit_of(const Args &a, uint32_t u) {
     Unit t;
-    t.tw = u % a.Tw;
-    const int64_t r = u / a.Tw;
-    t.s = r % a.S;
-    t.tn = r / a.S;
-    t.tile = t.tn * a.Tw + t.tw;
-    t.b0 = (int)(t.s * a.KB / a.S);
-    t.b1 = (int)((t.s + 1) * a.KB / a.S);
+    const uint32_t r = u / (uint32_t)a.Tw;
+    t.tw = u - r * (uint32_t)a.Tw;
+    if (a.S == 1) {
+        t.s = 0;
+        t.tn = r;
+        t.b0 = 0;
+        t.b1 = a.KB;
+    } else {
+        t.tn = r / (uint32_t)a.S;
+        t.s = r - t.tn * (uint32_t)a.S;
+        // parts of a.part stages; the first a.more of them have one more
+        t.b0 = (int)(t.s * (uint32_t)a.part_kb + (t.s < (uint32_t)a.part_more ? t.s : (uint32_t)a.part_more));
+        t.b1 = t.b0 + a.part_kb + (t.s < (uint32_t)a.part_more ? 1 : 0);
+    }
+    t.tile = t.tn * (uint32_t)a.Tw + t.tw;
     return t;
 }
 
 // The stages of this CTA's units, one after the other.
 struct Walk {
-    int64_t u;
+    uint32_t u;
     Unit un;
     int kb;
-    __device__ __forceinline__ bool start(const Args &a) {
+    __device__ __forceinline__ void start(const Args &a) {  // the grid has a unit for every CTA
         u = blockIdx.x;
-        if (u >= a.units) return false;
         un = unit_of(a, u);
         kb = un.b0;
-        return true;
     }
-    __device__ __forceinline__ void skip(const Args &a, int n) {
+    __device__ __forceinline__ bool skip(const Args &a, int n) {  // false: there are no more
         kb += n;
         while (kb >= un.b1) {
             const int over = kb - un.b1;
             u += gridDim.x;
-            if (u >= a.units) return;
+            if (u >= (uint32_t)a.units) return false;
             un = unit_of(a, u);
             kb = un.b0 + over;
         }
+        return true;
     }
 };
 
@@ -343,7 +355,7 @@ template <int KIND> struct Scales {
     // k: the thread's column (in stage 0 for FWD); row: its first row (in stage 0 for the others)
     __device__ __forceinline__ void fetch(const Args &a, const Walk &w, int tt) {
         if (KIND == WGRAD) {
-            const int64_t J = a.K >> 5, m = (int64_t)w.kb * BK + (tt >> 2), k = w.un.tw * 128 + 32 * (tt & 3);
+            const int64_t J = a.K >> 5, m = (int64_t)w.kb * BK + (tt >> 2), k = (int64_t)w.un.tw * 128 + 32 * (tt & 3);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 there[j] = k < a.K && m + 32 * j < a.rows;
@@ -353,8 +365,8 @@ template <int KIND> struct Scales {
         }
         const int64_t J = a.K >> a.gshift;
         const int src = KIND == DGRAD && w.kb >= a.KB0 ? 1 : 0;
-        const int64_t row = KIND == FWD ? w.un.tw * 64 + (tt >> 1) : (int64_t)(w.kb - (src ? a.KB0 : 0)) * BK + (tt >> 2);
-        const int64_t k = KIND == FWD ? (int64_t)w.kb * BK + 32 * (tt & 1) : w.un.tw * 128 + 32 * (tt & 3);
+        const int64_t row = KIND == FWD ? (int64_t)w.un.tw * 64 + (tt >> 1) : (int64_t)(w.kb - (src ? a.KB0 : 0)) * BK + (tt >> 2);
+        const int64_t k = KIND == FWD ? (int64_t)w.kb * BK + 32 * (tt & 1) : (int64_t)w.un.tw * 128 + 32 * (tt & 3);
         const int64_t at = row * J + (k >> a.gshift);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -460,19 +472,19 @@ __host__ __device__ __forceinline__ constexpr int value_at4(int place) { return 
 
 // Results of columns [c, c + 16) of a tile, of which n exist, for this thread's lane.
 template <int KIND, bool GRADS>
-__device__ __forceinline__ void emit(const Args &a, const Unit &un, int q4, int lane, int c, int n, const float (&v)[16],
-                                     bool add) {
-    const int64_t col = un.tn * a.NT + c;
+__device__ __forceinline__ void emit(const Args &a, const float *row_pow, const Unit &un, int q4, int lane, int c, int n,
+                                     const float (&v)[16], bool add) {
+    const int64_t col = (int64_t)un.tn * a.NT + c;
     float4 pw[KIND == WGRAD ? 1 : 4];
     if (KIND != WGRAD) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) pw[KIND == WGRAD ? 0 : i] = reinterpret_cast<const float4 *>(a.row_pow + col)[i];
+        for (int i = 0; i < 4; ++i) pw[KIND == WGRAD ? 0 : i] = reinterpret_cast<const float4 *>(row_pow + c)[i];
     }
     if (KIND == FWD) {
         // lanes 0-15 of a warp hold gate rows, lanes 16-31 the same features' up rows: of each pair
         // of tokens the lower half takes the even one and the upper half the odd one
         const int up = lane >> 4;
-        const int64_t h = un.tw * 64 + 16 * q4 + (lane & 15);
+        const int64_t h = (int64_t)un.tw * 64 + 16 * q4 + (lane & 15);
         const int64_t at = (col + up) * a.rows + h, step = 2 * a.rows;
         const int m = h < a.rows ? n - up : 0;  // this lane's tokens are those with 2 i < m
         float d[8];
@@ -499,7 +511,7 @@ __device__ __forceinline__ void emit(const Args &a, const Unit &un, int q4, int 
         }
     } else {
         const int pl = KIND == DGRAD ? (lane & ~7) + value_at8(lane & 7) : (lane & ~3) + value_at4(lane & 3);
-        const int64_t k = un.tw * 128 + 32 * q4 + pl;
+        const int64_t k = (int64_t)un.tw * 128 + 32 * q4 + pl;
         if (k >= a.K) return;
         const int64_t at = col * a.K + k;
         if (KIND == WGRAD && a.out_fp32) {
@@ -560,24 +572,17 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
         // ------------------------------------------------ expansion of A
         const int grp = warp / WPG, tt = threadIdx.x % TPG;
         const Place<KIND> place(tt);
-        int total = 0;
-        for (int64_t u = blockIdx.x; u < a.units; u += gridDim.x) {
-            const Unit un = unit_of(a, u);
-            total += un.b1 - un.b0;
-        }
         Walk w;  // of the scales, one of the group's stages ahead
-        (void)w.start(a);
-        w.skip(a, grp);
+        w.start(a);
+        bool more = w.skip(a, grp);
         Scales<KIND> next;
-        if (grp < total) next.fetch(a, w, tt);
+        if (more) next.fetch(a, w, tt);
         int slot = grp, rs = grp;
         uint32_t phase = 0, rphase = 0;
-        for (int n = grp; n < total; n += GROUPS) {
+        while (more) {
             const uint32_t s0 = next.word(a, 0), s1 = next.word(a, 1);
-            if (n + GROUPS < total) {
-                w.skip(a, GROUPS);
-                next.fetch(a, w, tt);
-            }
+            more = w.skip(a, GROUPS);
+            if (more) next.fetch(a, w, tt);
             if (!warp_wait(&sm->rawf[rs], rphase, sm, a.status)) break;
             if (!warp_wait(&sm->empty[slot], phase ^ 1u, sm, a.status)) break;
             expand_store<KIND>(smem_addr(raw + (size_t)rs * Raw<KIND>::BYTES), smem_addr(base + (size_t)slot * a.stage_bytes),
@@ -600,7 +605,7 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
         uint32_t phase = 0;
         bool ok = true;
         const uint32_t bytes = a.stage_bytes - A_BYTES;
-        for (int64_t u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
+        for (uint32_t u = blockIdx.x; u < (uint32_t)a.units && ok; u += gridDim.x) {
             const Unit un = unit_of(a, u);
             const int c0 = (int)(un.tn * a.NT);
             for (int kb = un.b0; kb < un.b1; ++kb) {
@@ -632,7 +637,7 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
         int rs = 0, issued = 0;
         uint32_t rphase = 0;
         bool ok = true;
-        for (int64_t u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
+        for (uint32_t u = blockIdx.x; u < (uint32_t)a.units && ok; u += gridDim.x) {
             const Unit un = unit_of(a, u);
             const int tw = (int)un.tw;
             for (int kb = un.b0; kb < un.b1; ++kb) {
@@ -673,7 +678,7 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
         int slot = 0, done = 0, n = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int64_t u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
+        for (uint32_t u = blockIdx.x; u < (uint32_t)a.units && ok; u += gridDim.x) {
             const Unit un = unit_of(a, u);
             for (int s0 = un.b0; s0 < un.b1 && ok; s0 += a.seg, ++n) {
                 const int s1 = un.b1 - s0 < a.seg ? un.b1 : s0 + a.seg;
@@ -709,13 +714,19 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
         const int q4 = warp & 3, r = q4 * 32 + lane;
         const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
         if (KIND != WGRAD) asm volatile("griddepcontrol.wait;" ::: "memory");  // row_pow too
+        float *row_pow = sm->row_pow[warp - W_OUT];
         int n = 0;
         bool ok = true;
-        for (int64_t u = blockIdx.x; u < a.units && ok; u += gridDim.x) {
+        for (uint32_t u = blockIdx.x; u < (uint32_t)a.units && ok; u += gridDim.x) {
             const Unit un = unit_of(a, u);
-            const int64_t left = a.cols - un.tn * a.NT;
+            __syncwarp();  // the previous tile's readers of row_pow
+            const int64_t left = a.cols - (int64_t)un.tn * a.NT;
             const int ncols = left < a.NT ? (int)left : a.NT;
-            float *part = a.S > 1 ? a.part + ((size_t)(un.tile * a.S + un.s) * a.NT) * 128 + r : nullptr;
+            // partial sums: [column / 4][lane][4 columns]
+            float4 *part = reinterpret_cast<float4 *>(a.part) + ((size_t)un.tile * a.S + un.s) * (a.NT * 32) + r;
+            if (KIND != WGRAD)
+                for (int c = lane; c < ncols; c += 32) row_pow[c] = a.row_pow[(int64_t)un.tn * a.NT + c];
+            __syncwarp();
             for (int s0 = un.b0; s0 < un.b1; s0 += a.seg, ++n) {
                 const int buf = n & 1;
                 if (!warp_wait(&sm->accf[buf], (uint32_t)(n >> 1) & 1u, sm, a.status)) { ok = false; break; }
@@ -730,12 +741,17 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
                     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(raw16[i]);
                     if (a.S > 1) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float *p = part + (size_t)(c + i) * 128;
-                            *p = s0 > un.b0 ? *p + v[i] : v[i];
+                        for (int i = 0; i < 4; ++i) {
+                            float4 f = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                            float4 *p = part + (c / 4 + i) * 128;
+                            if (s0 > un.b0) {
+                                const float4 o = *p;
+                                f = make_float4(f.x + o.x, f.y + o.y, f.z + o.z, f.w + o.w);
+                            }
+                            *p = f;
                         }
                     } else {
-                        emit<KIND, GRADS>(a, un, q4, lane, c, ncols - c, v, s0 > un.b0);
+                        emit<KIND, GRADS>(a, row_pow, un, q4, lane, c, ncols - c, v, s0 > un.b0);
                     }
                 }
                 tc_fence_before();
@@ -745,26 +761,44 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
             if (!ok || a.S == 1) continue;
             __threadfence();
             __syncwarp();
-            uint32_t *cnt = a.cnt + un.tile * OUT_WARPS + (warp - W_OUT);
+            uint32_t *cnt = a.cnt + (size_t)un.tile * OUT_WARPS + (warp - W_OUT);
             uint32_t old = 0;
             if (lane == 0) old = atomicAdd(cnt, 1u);
             old = __shfl_sync(FULL, old, 0);
             if (old != (uint32_t)(a.S - 1)) continue;
             // the last part of these lanes and columns: add all parts in order
             __threadfence();
-            const float *p0 = a.part + ((size_t)(un.tile * a.S) * a.NT) * 128 + r;
+            const float4 *p0 = reinterpret_cast<const float4 *>(a.part) + (size_t)un.tile * a.S * (a.NT * 32) + r;
 #pragma unroll 1
             for (int c = 0; c < ncols; c += 16) {
                 float v[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = __ldcg(p0 + (size_t)(c + i) * 128);
+                for (int i = 0; i < 16; ++i) v[i] = 0.0f;
 #pragma unroll 1
-                for (int s = 1; s < a.S; ++s) {
-                    const float *p = p0 + (size_t)s * a.NT * 128;
+                for (int s = 0; s < a.S; s += 2) {  // two parts' loads in flight
+                    const float4 *p = p0 + (size_t)s * (a.NT * 32) + c / 4 * 128;
+                    const bool two = s + 1 < a.S;
+                    const float4 *p2 = two ? p + a.NT * 32 : p;
+                    float4 x[4], y[4];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] += __ldcg(p + (size_t)(c + i) * 128);
+                    for (int i = 0; i < 4; ++i) x[i] = __ldcg(p + i * 128);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[i] = __ldcg(p2 + i * 128);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        v[4 * i] += x[i].x;
+                        v[4 * i + 1] += x[i].y;
+                        v[4 * i + 2] += x[i].z;
+                        v[4 * i + 3] += x[i].w;
+                        if (two) {
+                            v[4 * i] += y[i].x;
+                            v[4 * i + 1] += y[i].y;
+                            v[4 * i + 2] += y[i].z;
+                            v[4 * i + 3] += y[i].w;
+                        }
+                    }
                 }
-                emit<KIND, GRADS>(a, un, q4, lane, c, ncols - c, v, false);
+                emit<KIND, GRADS>(a, row_pow, un, q4, lane, c, ncols - c, v, false);
             }
             if (lane == 0) *cnt = 0u;  // ready for the next call
         }
@@ -919,7 +953,7 @@ inline Plan make_plan(int kind, int64_t lanes, int64_t cols, int64_t red, int so
     // slots: a slot then belongs to one group, which sees its laps in order. The
     // operands' ring has GROUPS slots at least: a group that filled stage i - GROUPS waited for
     // the MMAs of the lap before it, which complete in order.
-    const uint32_t rb = kind == WGRAD ? Raw<WGRAD>::BYTES : Raw<FWD>::BYTES, room = SMEM_MAX - 2048;
+    const uint32_t rb = kind == WGRAD ? Raw<WGRAD>::BYTES : Raw<FWD>::BYTES, room = SMEM_MAX - CONTROL - 1024;
     p.stages = MIN_STAGES;
     p.raws = GROUPS;
     while (p.stages < MAX_STAGES && (p.stages + 1) * p.stage_bytes + p.raws * rb <= room) ++p.stages;
@@ -988,6 +1022,7 @@ inline bool make_map(CUtensorMap *tm, const void *p, int64_t rows, int64_t width
 
 template <int KIND, bool GRADS>
 w4_status launch(const Plan &p, Maps &tm, Args a, void *workspace, int sms, cudaStream_t stream) {
+    if (p.units > (1 << 30)) return W4_ERR_SHAPE;  // more than the kernel counts
     bool maps = true;
     if (KIND == WGRAD) {
         maps = make_raw_map(&tm.q[0], a.x8, a.rows, a.K, 128, BK);
@@ -997,7 +1032,9 @@ w4_status launch(const Plan &p, Maps &tm, Args a, void *workspace, int sms, cuda
             maps = maps && make_raw_map(&tm.q[i], a.w[i].codes, a.rows, a.K / 2, KIND == FWD ? BK / 2 : 64, BK);
     }
     if (!maps) return W4_ERR_CUDA;
-    a.units = p.units;
+    a.units = (int)p.units;
+    a.part_kb = p.KB / p.S;
+    a.part_more = p.KB % p.S;
     a.Tw = (int)p.Tw;
     a.S = p.S;
     a.KB = p.KB;
@@ -1012,7 +1049,7 @@ w4_status launch(const Plan &p, Maps &tm, Args a, void *workspace, int sms, cuda
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + CNT_BYTES);
     a.status = device_status_ptr();
     if (!a.status) return W4_ERR_CUDA;
-    const int smem = (int)(p.stages * p.stage_bytes + p.raws * Raw<KIND>::BYTES) + 2048;
+    const int smem = (int)(p.stages * p.stage_bytes + p.raws * Raw<KIND>::BYTES + CONTROL) + 1024;
     static std::atomic<uint64_t> attr_done{0};  // one bit per device
     int dev = 0;
     cudaGetDevice(&dev);
