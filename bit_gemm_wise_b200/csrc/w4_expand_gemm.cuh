@@ -253,25 +253,25 @@ __device__ __forceinline__ void expand4_any(uint32_t w, uint32_t b, uint32_t &o0
     o1 = bmul(o1, pow2_two(b));
 }
 
-// A wait for the whole warp, polled by one lane: every lane's try_wait is an operation of its own
-// on shared memory. Bounded by the SM's clock (4e9 cycles, about 2 s).
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, Smem *sm, int *status) {
-    bool r = true;
-    if ((threadIdx.x & 31) == 0) {
-        r = mbar_try_wait(bar, parity);
-        if (!r) {
-            const long long t0 = clock64();
-            while (!(r = mbar_try_wait(bar, parity))) {
-                if (*(volatile int *)&sm->abort) break;
-                if (clock64() - t0 > kWaitCycles) {
-                    *(volatile int *)&sm->abort = 1;
-                    record_status(status, W4_ERR_TIMEOUT);
-                    break;
-                }
-            }
+// A wait by all lanes of a warp, with one result for all of them (a vote, so that what follows stays
+// uniform). A phase that is over costs some 50 cycles this way; a poll by one lane with the rest
+// reconverging behind it took over 110. Bounded by the SM's clock (4e9 cycles, about 2 s).
+static __device__ __noinline__ bool slow_wait(uint64_t *bar, uint32_t parity, int *abort, int *status) {
+    const long long t0 = clock64();
+    bool r;
+    while (!(r = __all_sync(FULL, mbar_try_wait(bar, parity)))) {
+        if (__any_sync(FULL, *(volatile int *)abort != 0)) break;
+        if (__any_sync(FULL, clock64() - t0 > kWaitCycles)) {
+            *(volatile int *)abort = 1;
+            record_status(status, W4_ERR_TIMEOUT);
+            break;
         }
     }
-    return __all_sync(FULL, r);
+    return r;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, Smem *sm, int *status) {
+    if (__all_sync(FULL, mbar_try_wait_short(bar, parity))) return true;
+    return slow_wait(bar, parity, &sm->abort, status);
 }
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
@@ -352,27 +352,28 @@ template <int KIND> struct Scales {
     uint16_t s[2], z[2];      // fp16 scales and zero points; WGRAD: scale bytes in s
     bool there[2];
 
-    // k: the thread's column (in stage 0 for FWD); row: its first row (in stage 0 for the others)
     __device__ __forceinline__ void fetch(const Args &a, const Walk &w, int tt) {
+        const int K = (int)a.K, rows = (int)a.rows;  // at most 2^24
         if (KIND == WGRAD) {
-            const int64_t J = a.K >> 5, m = (int64_t)w.kb * BK + (tt >> 2), k = (int64_t)w.un.tw * 128 + 32 * (tt & 3);
+            const int m = w.kb * BK + (tt >> 2), k = (int)w.un.tw * 128 + 32 * (tt & 3);
+            const int64_t at = (int64_t)m * (K >> 5) + (k >> 5);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                there[j] = k < a.K && m + 32 * j < a.rows;
-                s[j] = __ldg(a.xs + (there[j] ? (m + 32 * j) * J + (k >> 5) : 0));
+                there[j] = k < K && m + 32 * j < rows;
+                s[j] = __ldg(a.xs + (there[j] ? at + j * K : 0));  // 32 rows of K / 32 further
             }
             return;
         }
-        const int64_t J = a.K >> a.gshift;
+        const int J = K >> a.gshift;
         const int src = KIND == DGRAD && w.kb >= a.KB0 ? 1 : 0;
-        const int64_t row = KIND == FWD ? (int64_t)w.un.tw * 64 + (tt >> 1) : (int64_t)(w.kb - (src ? a.KB0 : 0)) * BK + (tt >> 2);
-        const int64_t k = KIND == FWD ? (int64_t)w.kb * BK + 32 * (tt & 1) : (int64_t)w.un.tw * 128 + 32 * (tt & 3);
-        const int64_t at = row * J + (k >> a.gshift);
+        const int row = KIND == FWD ? (int)w.un.tw * 64 + (tt >> 1) : (w.kb - (src ? a.KB0 : 0)) * BK + (tt >> 2);
+        const int k = KIND == FWD ? w.kb * BK + 32 * (tt & 1) : (int)w.un.tw * 128 + 32 * (tt & 3);
+        const int64_t at = (int64_t)row * J + (k >> a.gshift);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const Weight &m = a.w[KIND == FWD ? j : src];
-            there[j] = k < a.K && row + (KIND == FWD ? 0 : 32 * j) < a.rows;
-            const int64_t i = there[j] ? at + (KIND == FWD ? 0 : 32 * j) * J : 0;
+            there[j] = k < K && row + (KIND == FWD ? 0 : 32 * j) < rows;
+            const int64_t i = there[j] ? at + (KIND == FWD ? 0 : 32 * j * J) : 0;
             s[j] = __ldg(m.scales + i);
             // symmetric weights: the scale again, for the sake of one instruction stream
             z[j] = __ldg((a.asym ? reinterpret_cast<const uint16_t *>(m.zeros) : m.scales) + i);
