@@ -273,6 +273,22 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, Smem *
     if (__all_sync(FULL, mbar_try_wait_short(bar, parity))) return true;
     return slow_wait(bar, parity, &sm->abort, status);
 }
+// The same by the one thread that runs a producer's or the MMA issuer's loop.
+static __device__ __noinline__ bool slow_wait1(uint64_t *bar, uint32_t parity, int *abort, int *status) {
+    const long long t0 = clock64();
+    while (!mbar_try_wait_short(bar, parity)) {
+        if (*(volatile int *)abort) return false;
+        if (clock64() - t0 > kWaitCycles) {
+            *(volatile int *)abort = 1;
+            record_status(status, W4_ERR_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool wait1(uint64_t *bar, uint32_t parity, Smem *sm, int *status) {
+    return mbar_try_wait_short(bar, parity) || slow_wait1(bar, parity, &sm->abort, status);
+}
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
@@ -602,6 +618,7 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
     } else if (warp == W_B) {
         // ------------------------------------------------ B by TMA
         if (KIND != WGRAD) asm volatile("griddepcontrol.wait;" ::: "memory");  // B is row_prep_kernel's
+        if (elect_one()) {
         int slot = 0, issued = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -610,8 +627,8 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
             const Unit un = unit_of(a, u);
             const int c0 = (int)(un.tn * a.NT);
             for (int kb = un.b0; kb < un.b1; ++kb) {
-                if (!warp_wait(&sm->empty[slot], phase ^ 1u, sm, a.status)) { ok = false; break; }
-                if (elect_one()) {
+                if (!wait1(&sm->empty[slot], phase ^ 1u, sm, a.status)) { ok = false; break; }
+                {
                     uint8_t *dst = base + (size_t)slot * a.stage_bytes + A_BYTES;
                     mbar_arrive_expect_tx(&sm->full[slot], bytes);
                     if (KIND == WGRAD) {
@@ -623,18 +640,18 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
                         tma_load_2d(dst, &tm.b[0], kb * BK, c0, &sm->full[slot]);
                     }
                 }
-                __syncwarp();
                 ++issued;
                 if (++slot == NS) { slot = 0; phase ^= 1u; }
             }
         }
         // no copy may land after the CTA exits
-        if (lane == 0)
-            for (int i = issued > NS ? issued - NS : 0; i < issued; ++i)
+        for (int i = issued > NS ? issued - NS : 0; i < issued; ++i)
                 (void)mbar_wait_bounded(&sm->full[i % NS], (uint32_t)(i / NS) & 1u, a.status);
+        }
         __syncwarp();
     } else if (warp == W_Q) {
         // ------------------------------------------------ codes by TMA
+        if (elect_one()) {
         int rs = 0, issued = 0;
         uint32_t rphase = 0;
         bool ok = true;
@@ -642,8 +659,8 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
             const Unit un = unit_of(a, u);
             const int tw = (int)un.tw;
             for (int kb = un.b0; kb < un.b1; ++kb) {
-                if (!warp_wait(&sm->rawe[rs], rphase ^ 1u, sm, a.status)) { ok = false; break; }
-                if (elect_one()) {
+                if (!wait1(&sm->rawe[rs], rphase ^ 1u, sm, a.status)) { ok = false; break; }
+                {
                     uint8_t *dst = raw + (size_t)rs * Raw<KIND>::BYTES;
                     mbar_arrive_expect_tx(&sm->rawf[rs], Raw<KIND>::BYTES);
                     if (KIND == FWD) {
@@ -655,15 +672,14 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
                         tma_load_2d(dst, &tm.q[0], tw * (KIND == DGRAD ? 64 : 128), kb * BK, &sm->rawf[rs]);
                     }
                 }
-                __syncwarp();
                 ++issued;
                 if (++rs == NR) { rs = 0; rphase ^= 1u; }
             }
         }
         // no copy may land after the CTA exits
-        if (lane == 0)
-            for (int i = issued > NR ? issued - NR : 0; i < issued; ++i)
+        for (int i = issued > NR ? issued - NR : 0; i < issued; ++i)
                 (void)mbar_wait_bounded(&sm->rawf[i % NR], (uint32_t)(i / NR) & 1u, a.status);
+        }
         __syncwarp();
     } else if (warp == W_MMA) {
         // ------------------------------------------------ MMA issue
@@ -676,6 +692,7 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
         constexpr uint32_t alead = KIND == FWD ? 1u << 16 : 512u << 16, astep = KIND == FWD ? 2u : 128u;
         constexpr uint32_t blead = KIND == WGRAD ? 512u << 16 : 1u << 16, bstep = KIND == WGRAD ? 128u : 2u;
         const uint32_t sbase = smem_addr(base);
+        if (elect_one()) {
         int slot = 0, done = 0, n = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -684,31 +701,30 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
             for (int s0 = un.b0; s0 < un.b1 && ok; s0 += a.seg, ++n) {
                 const int s1 = un.b1 - s0 < a.seg ? un.b1 : s0 + a.seg;
                 const int buf = n & 1;
-                if (!warp_wait(&sm->acce[buf], ((uint32_t)(n >> 1) & 1u) ^ 1u, sm, a.status)) { ok = false; break; }
+                if (!wait1(&sm->acce[buf], ((uint32_t)(n >> 1) & 1u) ^ 1u, sm, a.status)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(buf * 256);
                 for (int kb = s0; kb < s1; ++kb) {
-                    if (!warp_wait(&sm->full[slot], phase, sm, a.status)) { ok = false; break; }
+                    if (!wait1(&sm->full[slot], phase, sm, a.status)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t sa = sbase + (uint32_t)slot * a.stage_bytes;
                     const uint32_t alo = (sa >> 4) | alead, blo = ((sa + A_BYTES) >> 4) | blead;
-                    if (elect_one()) {
+                    {
 #pragma unroll
                         for (int kk = 0; kk < BK / 16; ++kk)
                             mma(d, alo + kk * astep, blo + kk * bstep, idesc, kb > s0 || kk > 0 ? 1u : 0u);
                         mma_commit(&sm->empty[slot]);
                         if (kb + 1 == s1) mma_commit(&sm->accf[buf]);
                     }
-                    __syncwarp();
                     ++done;
                     if (++slot == NS) { slot = 0; phase ^= 1u; }
                 }
             }
         }
         // no commit may arrive after the CTA exits
-        if (lane == 0)
-            for (int i = done > NS ? done - NS : 0; i < done; ++i)
+        for (int i = done > NS ? done - NS : 0; i < done; ++i)
                 (void)mbar_wait_bounded(&sm->empty[i % NS], (uint32_t)(i / NS) & 1u, a.status);
+        }
         __syncwarp();
     } else {
         // ------------------------------------------------ results (lane 32 q4 + lane of the tile)
