@@ -70,7 +70,8 @@ struct Smem {
     uint64_t acce[2];             // its columns were read (one arrival per warp)
     uint32_t tmem_base;
     int abort;
-    alignas(16) float row_pow[OUT_WARPS][256];  // of the current tile's tokens, a copy for each warp
+    uint32_t arrived[OUT_WARPS];  // parts of the tile's lanes that came before
+    alignas(16) float row_pow[OUT_WARPS][256];  // of the current tile's tokens, a copy for each quarter
 };
 constexpr uint32_t CONTROL = 5 * 1024;
 static_assert(sizeof(Smem) <= CONTROL, "control block");
@@ -558,6 +559,15 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int NS = a.stages, NR = a.raws;
 
+    // the expansion's first scales, on their way while the CTA sets up
+    Walk w;
+    bool more = false;
+    Scales<KIND> next;
+    if (warp < EXPAND_WARPS) {
+        w.start(a);
+        more = w.skip(a, warp / WPG);
+        if (more) next.fetch(a, w, threadIdx.x % TPG);
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
             mbar_init(&sm->full[s], 1 + WPG);
@@ -589,11 +599,6 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
         // ------------------------------------------------ expansion of A
         const int grp = warp / WPG, tt = threadIdx.x % TPG;
         const Place<KIND> place(tt);
-        Walk w;  // of the scales, one of the group's stages ahead
-        w.start(a);
-        bool more = w.skip(a, grp);
-        Scales<KIND> next;
-        if (more) next.fetch(a, w, tt);
         int slot = grp, rs = grp;
         uint32_t phase = 0, rphase = 0;
         while (more) {
@@ -619,66 +624,66 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
         // ------------------------------------------------ B by TMA
         if (KIND != WGRAD) asm volatile("griddepcontrol.wait;" ::: "memory");  // B is row_prep_kernel's
         if (elect_one()) {
-        int slot = 0, issued = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        const uint32_t bytes = a.stage_bytes - A_BYTES;
-        for (uint32_t u = blockIdx.x; u < (uint32_t)a.units && ok; u += gridDim.x) {
-            const Unit un = unit_of(a, u);
-            const int c0 = (int)(un.tn * a.NT);
-            for (int kb = un.b0; kb < un.b1; ++kb) {
-                if (!wait1(&sm->empty[slot], phase ^ 1u, sm, a.status)) { ok = false; break; }
-                {
-                    uint8_t *dst = base + (size_t)slot * a.stage_bytes + A_BYTES;
-                    mbar_arrive_expect_tx(&sm->full[slot], bytes);
-                    if (KIND == WGRAD) {
-                        for (uint32_t o = 0; o < bytes; o += 8192u)  // 64 columns of dY a box
-                            tma_load_2d(dst + o, &tm.b[0], c0 + (int)(o >> 7), kb * BK, &sm->full[slot]);
-                    } else if (KIND == DGRAD && kb >= a.KB0) {
-                        tma_load_2d(dst, &tm.b[1], (kb - a.KB0) * BK, c0, &sm->full[slot]);
-                    } else {
-                        tma_load_2d(dst, &tm.b[0], kb * BK, c0, &sm->full[slot]);
+            int slot = 0, issued = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            const uint32_t bytes = a.stage_bytes - A_BYTES;
+            for (uint32_t u = blockIdx.x; u < (uint32_t)a.units && ok; u += gridDim.x) {
+                const Unit un = unit_of(a, u);
+                const int c0 = (int)(un.tn * a.NT);
+                for (int kb = un.b0; kb < un.b1; ++kb) {
+                    if (!wait1(&sm->empty[slot], phase ^ 1u, sm, a.status)) { ok = false; break; }
+                    {
+                        uint8_t *dst = base + (size_t)slot * a.stage_bytes + A_BYTES;
+                        mbar_arrive_expect_tx(&sm->full[slot], bytes);
+                        if (KIND == WGRAD) {
+                            for (uint32_t o = 0; o < bytes; o += 8192u)  // 64 columns of dY a box
+                                tma_load_2d(dst + o, &tm.b[0], c0 + (int)(o >> 7), kb * BK, &sm->full[slot]);
+                        } else if (KIND == DGRAD && kb >= a.KB0) {
+                            tma_load_2d(dst, &tm.b[1], (kb - a.KB0) * BK, c0, &sm->full[slot]);
+                        } else {
+                            tma_load_2d(dst, &tm.b[0], kb * BK, c0, &sm->full[slot]);
+                        }
                     }
+                    ++issued;
+                    if (++slot == NS) { slot = 0; phase ^= 1u; }
                 }
-                ++issued;
-                if (++slot == NS) { slot = 0; phase ^= 1u; }
             }
-        }
-        // no copy may land after the CTA exits
-        for (int i = issued > NS ? issued - NS : 0; i < issued; ++i)
-                (void)mbar_wait_bounded(&sm->full[i % NS], (uint32_t)(i / NS) & 1u, a.status);
+            // no copy may land after the CTA exits
+            for (int i = issued > NS ? issued - NS : 0; i < issued; ++i)
+                    (void)mbar_wait_bounded(&sm->full[i % NS], (uint32_t)(i / NS) & 1u, a.status);
         }
         __syncwarp();
     } else if (warp == W_Q) {
         // ------------------------------------------------ codes by TMA
         if (elect_one()) {
-        int rs = 0, issued = 0;
-        uint32_t rphase = 0;
-        bool ok = true;
-        for (uint32_t u = blockIdx.x; u < (uint32_t)a.units && ok; u += gridDim.x) {
-            const Unit un = unit_of(a, u);
-            const int tw = (int)un.tw;
-            for (int kb = un.b0; kb < un.b1; ++kb) {
-                if (!wait1(&sm->rawe[rs], rphase ^ 1u, sm, a.status)) { ok = false; break; }
-                {
-                    uint8_t *dst = raw + (size_t)rs * Raw<KIND>::BYTES;
-                    mbar_arrive_expect_tx(&sm->rawf[rs], Raw<KIND>::BYTES);
-                    if (KIND == FWD) {
-                        tma_load_2d(dst, &tm.q[0], kb * (BK / 2), tw * 64, &sm->rawf[rs]);
-                        tma_load_2d(dst + 2048, &tm.q[1], kb * (BK / 2), tw * 64, &sm->rawf[rs]);
-                    } else if (KIND == DGRAD && kb >= a.KB0) {
-                        tma_load_2d(dst, &tm.q[1], tw * 64, (kb - a.KB0) * BK, &sm->rawf[rs]);
-                    } else {
-                        tma_load_2d(dst, &tm.q[0], tw * (KIND == DGRAD ? 64 : 128), kb * BK, &sm->rawf[rs]);
+            int rs = 0, issued = 0;
+            uint32_t rphase = 0;
+            bool ok = true;
+            for (uint32_t u = blockIdx.x; u < (uint32_t)a.units && ok; u += gridDim.x) {
+                const Unit un = unit_of(a, u);
+                const int tw = (int)un.tw;
+                for (int kb = un.b0; kb < un.b1; ++kb) {
+                    if (!wait1(&sm->rawe[rs], rphase ^ 1u, sm, a.status)) { ok = false; break; }
+                    {
+                        uint8_t *dst = raw + (size_t)rs * Raw<KIND>::BYTES;
+                        mbar_arrive_expect_tx(&sm->rawf[rs], Raw<KIND>::BYTES);
+                        if (KIND == FWD) {
+                            tma_load_2d(dst, &tm.q[0], kb * (BK / 2), tw * 64, &sm->rawf[rs]);
+                            tma_load_2d(dst + 2048, &tm.q[1], kb * (BK / 2), tw * 64, &sm->rawf[rs]);
+                        } else if (KIND == DGRAD && kb >= a.KB0) {
+                            tma_load_2d(dst, &tm.q[1], tw * 64, (kb - a.KB0) * BK, &sm->rawf[rs]);
+                        } else {
+                            tma_load_2d(dst, &tm.q[0], tw * (KIND == DGRAD ? 64 : 128), kb * BK, &sm->rawf[rs]);
+                        }
                     }
+                    ++issued;
+                    if (++rs == NR) { rs = 0; rphase ^= 1u; }
                 }
-                ++issued;
-                if (++rs == NR) { rs = 0; rphase ^= 1u; }
             }
-        }
-        // no copy may land after the CTA exits
-        for (int i = issued > NR ? issued - NR : 0; i < issued; ++i)
-                (void)mbar_wait_bounded(&sm->rawf[i % NR], (uint32_t)(i / NR) & 1u, a.status);
+            // no copy may land after the CTA exits
+            for (int i = issued > NR ? issued - NR : 0; i < issued; ++i)
+                    (void)mbar_wait_bounded(&sm->rawf[i % NR], (uint32_t)(i / NR) & 1u, a.status);
         }
         __syncwarp();
     } else if (warp == W_MMA) {
@@ -693,63 +698,81 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
         constexpr uint32_t blead = KIND == WGRAD ? 512u << 16 : 1u << 16, bstep = KIND == WGRAD ? 128u : 2u;
         const uint32_t sbase = smem_addr(base);
         if (elect_one()) {
-        int slot = 0, done = 0, n = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        for (uint32_t u = blockIdx.x; u < (uint32_t)a.units && ok; u += gridDim.x) {
-            const Unit un = unit_of(a, u);
-            for (int s0 = un.b0; s0 < un.b1 && ok; s0 += a.seg, ++n) {
-                const int s1 = un.b1 - s0 < a.seg ? un.b1 : s0 + a.seg;
-                const int buf = n & 1;
-                if (!wait1(&sm->acce[buf], ((uint32_t)(n >> 1) & 1u) ^ 1u, sm, a.status)) { ok = false; break; }
-                tc_fence_after();
-                const uint32_t d = tmem + (uint32_t)(buf * 256);
-                for (int kb = s0; kb < s1; ++kb) {
-                    if (!wait1(&sm->full[slot], phase, sm, a.status)) { ok = false; break; }
+            int slot = 0, done = 0, n = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (uint32_t u = blockIdx.x; u < (uint32_t)a.units && ok; u += gridDim.x) {
+                const Unit un = unit_of(a, u);
+                for (int s0 = un.b0; s0 < un.b1 && ok; s0 += a.seg, ++n) {
+                    const int s1 = un.b1 - s0 < a.seg ? un.b1 : s0 + a.seg;
+                    const int buf = n & 1;
+                    if (!wait1(&sm->acce[buf], ((uint32_t)(n >> 1) & 1u) ^ 1u, sm, a.status)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t sa = sbase + (uint32_t)slot * a.stage_bytes;
-                    const uint32_t alo = (sa >> 4) | alead, blo = ((sa + A_BYTES) >> 4) | blead;
-                    {
+                    const uint32_t d = tmem + (uint32_t)(buf * 256);
+                    for (int kb = s0; kb < s1; ++kb) {
+                        if (!wait1(&sm->full[slot], phase, sm, a.status)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint32_t sa = sbase + (uint32_t)slot * a.stage_bytes;
+                        const uint32_t alo = (sa >> 4) | alead, blo = ((sa + A_BYTES) >> 4) | blead;
+                        {
 #pragma unroll
-                        for (int kk = 0; kk < BK / 16; ++kk)
-                            mma(d, alo + kk * astep, blo + kk * bstep, idesc, kb > s0 || kk > 0 ? 1u : 0u);
-                        mma_commit(&sm->empty[slot]);
-                        if (kb + 1 == s1) mma_commit(&sm->accf[buf]);
+                            for (int kk = 0; kk < BK / 16; ++kk)
+                                mma(d, alo + kk * astep, blo + kk * bstep, idesc, kb > s0 || kk > 0 ? 1u : 0u);
+                            mma_commit(&sm->empty[slot]);
+                            if (kb + 1 == s1) mma_commit(&sm->accf[buf]);
+                        }
+                        ++done;
+                        if (++slot == NS) { slot = 0; phase ^= 1u; }
                     }
-                    ++done;
-                    if (++slot == NS) { slot = 0; phase ^= 1u; }
                 }
             }
-        }
-        // no commit may arrive after the CTA exits
-        for (int i = done > NS ? done - NS : 0; i < done; ++i)
-                (void)mbar_wait_bounded(&sm->empty[i % NS], (uint32_t)(i / NS) & 1u, a.status);
+            // no commit may arrive after the CTA exits
+            for (int i = done > NS ? done - NS : 0; i < done; ++i)
+                    (void)mbar_wait_bounded(&sm->empty[i % NS], (uint32_t)(i / NS) & 1u, a.status);
         }
         __syncwarp();
-    } else {
-        // ------------------------------------------------ results (lane 32 q4 + lane of the tile)
-        const int q4 = warp & 3, r = q4 * 32 + lane;
+    }
+
+    if (warp < W_B) {
+        // ------------------------------------------------ results (lane 32 q4 + lane of the tile), 16
+        // columns at a time. The CTA's last tile has nothing behind it to overlap with: there the
+        // expansion warps, whose work is done, share the columns (ranks 0-3, the result warps are
+        // rank 4). Where a tile is summed up in several accumulators, they do not.
+        const int q4 = warp & 3, r = q4 * 32 + lane, rank = warp >> 2;
         const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
+        const bool helper = warp < EXPAND_WARPS, shared = a.seg >= a.KB;
+        const uint32_t before = ((uint32_t)a.units - 1u - blockIdx.x) / gridDim.x;  // this CTA's units but the last
+        float *row_pow = sm->row_pow[q4];
         if (KIND != WGRAD) asm volatile("griddepcontrol.wait;" ::: "memory");  // row_pow too
-        float *row_pow = sm->row_pow[warp - W_OUT];
-        int n = 0;
+        uint32_t u = helper ? blockIdx.x + before * gridDim.x : blockIdx.x;
+        if (helper && !shared) u = (uint32_t)a.units;
+        int n = helper ? (int)before : 0;
         bool ok = true;
-        for (uint32_t u = blockIdx.x; u < (uint32_t)a.units && ok; u += gridDim.x) {
+        // A wait that ran out ends this warp's work, but not its way to the last tile: the ranks of
+        // a quarter meet there at barriers that have no time limit of their own.
+        for (; u < (uint32_t)a.units; u += gridDim.x) {
+            const bool last = shared && (uint32_t)a.units - u <= gridDim.x;
+            if (!ok && !last) continue;
             const Unit un = unit_of(a, u);
-            __syncwarp();  // the previous tile's readers of row_pow
             const int64_t left = a.cols - (int64_t)un.tn * a.NT;
             const int ncols = left < a.NT ? (int)left : a.NT;
+            const int c0 = last ? 16 * rank : 0, cstep = last ? 16 * (W_B / 4) : 16;
             // partial sums: [column / 4][lane][4 columns]
             float4 *part = reinterpret_cast<float4 *>(a.part) + ((size_t)un.tile * a.S + un.s) * (a.NT * 32) + r;
-            if (KIND != WGRAD)
-                for (int c = lane; c < ncols; c += 32) row_pow[c] = a.row_pow[(int64_t)un.tn * a.NT + c];
-            __syncwarp();
-            for (int s0 = un.b0; s0 < un.b1; s0 += a.seg, ++n) {
+            if (KIND != WGRAD) {
+                if (last) named_bar_sync(1 + q4, W_B / 4 * 32);  // readers of the previous tile's
+                __syncwarp();
+                if (!helper)
+                    for (int c = lane; c < ncols; c += 32) row_pow[c] = a.row_pow[(int64_t)un.tn * a.NT + c];
+                if (last) named_bar_sync(1 + q4, W_B / 4 * 32);
+                __syncwarp();
+            }
+            for (int s0 = un.b0; s0 < un.b1 && ok; s0 += a.seg, ++n) {
                 const int buf = n & 1;
                 if (!warp_wait(&sm->accf[buf], (uint32_t)(n >> 1) & 1u, sm, a.status)) { ok = false; break; }
                 tc_fence_after();
 #pragma unroll 1
-                for (int c = 0; c < ncols; c += 16) {
+                for (int c = c0; c < ncols; c += cstep) {
                     uint32_t raw16[16];
                     tmem_ld16(tl + (uint32_t)(buf * 256 + c), raw16);
                     tmem_wait_ld(raw16);
@@ -773,21 +796,22 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm->acce[buf]);
+                if (lane == 0 && !helper) mbar_arrive(&sm->acce[buf]);
             }
-            if (!ok || a.S == 1) continue;
+            if (a.S == 1) continue;
+            // the last part of a tile's 32 lanes to arrive adds all parts in order
+            uint32_t *cnt = a.cnt + (size_t)un.tile * OUT_WARPS + q4;
             __threadfence();
+            if (last) named_bar_sync(1 + q4, W_B / 4 * 32);
             __syncwarp();
-            uint32_t *cnt = a.cnt + (size_t)un.tile * OUT_WARPS + (warp - W_OUT);
-            uint32_t old = 0;
-            if (lane == 0) old = atomicAdd(cnt, 1u);
-            old = __shfl_sync(FULL, old, 0);
-            if (old != (uint32_t)(a.S - 1)) continue;
-            // the last part of these lanes and columns: add all parts in order
+            if (!helper && lane == 0) sm->arrived[q4] = atomicAdd(cnt, 1u);
+            if (last) named_bar_sync(1 + q4, W_B / 4 * 32);
+            __syncwarp();
+            if (sm->arrived[q4] != (uint32_t)(a.S - 1) || !ok) continue;
             __threadfence();
             const float4 *p0 = reinterpret_cast<const float4 *>(a.part) + (size_t)un.tile * a.S * (a.NT * 32) + r;
 #pragma unroll 1
-            for (int c = 0; c < ncols; c += 16) {
+            for (int c = c0; c < ncols; c += cstep) {
                 float v[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) v[i] = 0.0f;
@@ -817,7 +841,7 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
                 }
                 emit<KIND, GRADS>(a, row_pow, un, q4, lane, c, ncols - c, v, false);
             }
-            if (lane == 0) *cnt = 0u;  // ready for the next call
+            if (!helper && lane == 0) *cnt = 0u;  // ready for the next call
         }
     }
 
