@@ -633,17 +633,15 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
                 const int c0 = (int)(un.tn * a.NT);
                 for (int kb = un.b0; kb < un.b1; ++kb) {
                     if (!wait1(&sm->empty[slot], phase ^ 1u, sm, a.status)) { ok = false; break; }
-                    {
-                        uint8_t *dst = base + (size_t)slot * a.stage_bytes + A_BYTES;
-                        mbar_arrive_expect_tx(&sm->full[slot], bytes);
-                        if (KIND == WGRAD) {
-                            for (uint32_t o = 0; o < bytes; o += 8192u)  // 64 columns of dY a box
-                                tma_load_2d(dst + o, &tm.b[0], c0 + (int)(o >> 7), kb * BK, &sm->full[slot]);
-                        } else if (KIND == DGRAD && kb >= a.KB0) {
-                            tma_load_2d(dst, &tm.b[1], (kb - a.KB0) * BK, c0, &sm->full[slot]);
-                        } else {
-                            tma_load_2d(dst, &tm.b[0], kb * BK, c0, &sm->full[slot]);
-                        }
+                    uint8_t *dst = base + (size_t)slot * a.stage_bytes + A_BYTES;
+                    mbar_arrive_expect_tx(&sm->full[slot], bytes);
+                    if (KIND == WGRAD) {
+                        for (uint32_t o = 0; o < bytes; o += 8192u)  // 64 columns of dY a box
+                            tma_load_2d(dst + o, &tm.b[0], c0 + (int)(o >> 7), kb * BK, &sm->full[slot]);
+                    } else if (KIND == DGRAD && kb >= a.KB0) {
+                        tma_load_2d(dst, &tm.b[1], (kb - a.KB0) * BK, c0, &sm->full[slot]);
+                    } else {
+                        tma_load_2d(dst, &tm.b[0], kb * BK, c0, &sm->full[slot]);
                     }
                     ++issued;
                     if (++slot == NS) { slot = 0; phase ^= 1u; }
@@ -651,7 +649,7 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
             }
             // no copy may land after the CTA exits
             for (int i = issued > NS ? issued - NS : 0; i < issued; ++i)
-                    (void)mbar_wait_bounded(&sm->full[i % NS], (uint32_t)(i / NS) & 1u, a.status);
+                (void)mbar_wait_bounded(&sm->full[i % NS], (uint32_t)(i / NS) & 1u, a.status);
         }
         __syncwarp();
     } else if (warp == W_Q) {
@@ -665,17 +663,15 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
                 const int tw = (int)un.tw;
                 for (int kb = un.b0; kb < un.b1; ++kb) {
                     if (!wait1(&sm->rawe[rs], rphase ^ 1u, sm, a.status)) { ok = false; break; }
-                    {
-                        uint8_t *dst = raw + (size_t)rs * Raw<KIND>::BYTES;
-                        mbar_arrive_expect_tx(&sm->rawf[rs], Raw<KIND>::BYTES);
-                        if (KIND == FWD) {
-                            tma_load_2d(dst, &tm.q[0], kb * (BK / 2), tw * 64, &sm->rawf[rs]);
-                            tma_load_2d(dst + 2048, &tm.q[1], kb * (BK / 2), tw * 64, &sm->rawf[rs]);
-                        } else if (KIND == DGRAD && kb >= a.KB0) {
-                            tma_load_2d(dst, &tm.q[1], tw * 64, (kb - a.KB0) * BK, &sm->rawf[rs]);
-                        } else {
-                            tma_load_2d(dst, &tm.q[0], tw * (KIND == DGRAD ? 64 : 128), kb * BK, &sm->rawf[rs]);
-                        }
+                    uint8_t *dst = raw + (size_t)rs * Raw<KIND>::BYTES;
+                    mbar_arrive_expect_tx(&sm->rawf[rs], Raw<KIND>::BYTES);
+                    if (KIND == FWD) {
+                        tma_load_2d(dst, &tm.q[0], kb * (BK / 2), tw * 64, &sm->rawf[rs]);
+                        tma_load_2d(dst + 2048, &tm.q[1], kb * (BK / 2), tw * 64, &sm->rawf[rs]);
+                    } else if (KIND == DGRAD && kb >= a.KB0) {
+                        tma_load_2d(dst, &tm.q[1], tw * 64, (kb - a.KB0) * BK, &sm->rawf[rs]);
+                    } else {
+                        tma_load_2d(dst, &tm.q[0], tw * (KIND == DGRAD ? 64 : 128), kb * BK, &sm->rawf[rs]);
                     }
                     ++issued;
                     if (++rs == NR) { rs = 0; rphase ^= 1u; }
@@ -683,7 +679,7 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
             }
             // no copy may land after the CTA exits
             for (int i = issued > NR ? issued - NR : 0; i < issued; ++i)
-                    (void)mbar_wait_bounded(&sm->rawf[i % NR], (uint32_t)(i / NR) & 1u, a.status);
+                (void)mbar_wait_bounded(&sm->rawf[i % NR], (uint32_t)(i / NR) & 1u, a.status);
         }
         __syncwarp();
     } else if (warp == W_MMA) {
@@ -714,13 +710,11 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
                         tc_fence_after();
                         const uint32_t sa = sbase + (uint32_t)slot * a.stage_bytes;
                         const uint32_t alo = (sa >> 4) | alead, blo = ((sa + A_BYTES) >> 4) | blead;
-                        {
 #pragma unroll
-                            for (int kk = 0; kk < BK / 16; ++kk)
-                                mma(d, alo + kk * astep, blo + kk * bstep, idesc, kb > s0 || kk > 0 ? 1u : 0u);
-                            mma_commit(&sm->empty[slot]);
-                            if (kb + 1 == s1) mma_commit(&sm->accf[buf]);
-                        }
+                        for (int kk = 0; kk < BK / 16; ++kk)
+                            mma(d, alo + kk * astep, blo + kk * bstep, idesc, kb > s0 || kk > 0 ? 1u : 0u);
+                        mma_commit(&sm->empty[slot]);
+                        if (kb + 1 == s1) mma_commit(&sm->accf[buf]);
                         ++done;
                         if (++slot == NS) { slot = 0; phase ^= 1u; }
                     }
@@ -728,7 +722,7 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
             }
             // no commit may arrive after the CTA exits
             for (int i = done > NS ? done - NS : 0; i < done; ++i)
-                    (void)mbar_wait_bounded(&sm->empty[i % NS], (uint32_t)(i / NS) & 1u, a.status);
+                (void)mbar_wait_bounded(&sm->empty[i % NS], (uint32_t)(i / NS) & 1u, a.status);
         }
         __syncwarp();
     }
