@@ -1030,15 +1030,18 @@ inline EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// 8-bit [rows, width], plain boxes; what lies outside reads as zero
-inline bool make_raw_map(CUtensorMap *tm, const void *p, int64_t rows, int64_t width, int box_width, int box_rows) {
+// 8-bit [rows, width], plain boxes or boxes of 128 bytes' width with the 128-byte swizzle; what lies
+// outside reads as zero
+inline bool make_raw_map(CUtensorMap *tm, const void *p, int64_t rows, int64_t width, int box_width, int box_rows,
+                         bool swizzle = false) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)width};
     const cuuint32_t box[2] = {(cuuint32_t)box_width, (cuuint32_t)box_rows}, es[2] = {1, 1};
     return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(p), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1053,6 +1056,35 @@ inline bool make_map(CUtensorMap *tm, const void *p, int64_t rows, int64_t width
     return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p), dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Allows a kernel its dynamic shared memory, once per device (`done` has a bit for each).
+template <typename F> bool allow_smem(F *kernel, int bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t)1 << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
+
+// Launch that may start while the kernel before it on the stream is finishing (programmatic
+// dependent launch).
+template <typename... P, typename... A>
+w4_status launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream, A &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, P(args)...) != cudaSuccess) return W4_ERR_CUDA;
+    return launch_status();
 }
 
 template <int KIND, bool GRADS>
@@ -1085,30 +1117,14 @@ w4_status launch(const Plan &p, Maps &tm, Args a, void *workspace, int sms, cuda
     a.status = device_status_ptr();
     if (!a.status) return W4_ERR_CUDA;
     const int smem = (int)(p.stages * p.stage_bytes + p.raws * Raw<KIND>::BYTES + CONTROL) + 1024;
-    static std::atomic<uint64_t> attr_done{0};  // one bit per device
-    int dev = 0;
-    cudaGetDevice(&dev);
-    const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t)1 << dev : 0;
-    if (!(attr_done.load(std::memory_order_relaxed) & bit)) {
-        if (cudaFuncSetAttribute(expand_gemm_kernel<KIND, GRADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)SMEM_MAX) != cudaSuccess)
-            return W4_ERR_CUDA;
-        attr_done.fetch_or(bit, std::memory_order_relaxed);
-    }
+    static std::atomic<uint64_t> attr_done{0};
+    if (!allow_smem(expand_gemm_kernel<KIND, GRADS>, (int)SMEM_MAX, attr_done)) return W4_ERR_CUDA;
     const unsigned grid = (unsigned)(p.units < sms ? p.units : sms);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = stream;
     // FWD and DGRAD follow row_prep_kernel: they may start, and read weights, while it finishes.
     // Whatever came before on the stream was complete when it began.
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = KIND == WGRAD ? 0 : 1;
-    if (cudaLaunchKernelEx(&cfg, expand_gemm_kernel<KIND, GRADS>, tm, a) != cudaSuccess) return W4_ERR_CUDA;
+    if (KIND != WGRAD)
+        return launch_behind(expand_gemm_kernel<KIND, GRADS>, grid, THREADS, (size_t)smem, stream, tm, a);
+    expand_gemm_kernel<KIND, GRADS><<<grid, THREADS, smem, stream>>>(tm, a);
     return launch_status();
 }
 

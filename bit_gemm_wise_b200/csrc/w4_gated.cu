@@ -2,20 +2,34 @@
 // (w4a16_gated_bwd) and the input gradient of a 4-bit layer (w4a16_dgrad).
 //
 // The products of many rows are those of w4_expand_gemm.cuh. Up to 16 rows w4a16_gated is a decode
-// step, which reads every weight once for a handful of products, so the kernel below is built around
-// the weight stream:
-//   - a warp takes 16 features (the 16 gate rows and the 16 up rows of a matrix fragment each) and
-//     every W-th block of 128 columns; its codes go from memory straight into registers (16 bytes a
-//     lane and row where the group allows), a block ahead, and are there the A operand of
-//     mma.m16n8k16, which may sum its 16 columns in any order: lane t of a row's four holds a quarter
-//     of each group. The M <= 8 (16) tokens are the N = 8 columns of one (two) products;
-//   - two shifts' worth of work per weight: a nibble OR-ed into the mantissa of bf16 128.0 is 128 + q,
-//     exactly; the products with bf16 activations are exact too, and
-//         y += s (sum (128 + q) x - (128 + z) sum x)
-//     in fp32 after each group, with sum x from a product with a matrix of ones. (The legacy mma is
-//     no bottleneck here: 24 products for 4096 weights; a tcgen05 tile would spend its time loading
-//     TMEM.)
-//   - the W warps' sums meet in shared memory, in order; the activation and the product follow there.
+// step, which reads every weight once for a handful of products, so the two kernels below are built
+// around the weight stream. In both a warp takes 16 features (the 16 gate rows and the 16 up rows of a
+// matrix fragment each) and every W-th block of 128 columns, and its codes are in registers the A
+// operand of a warp-level product, which may sum its columns in any order: lane t of a row's four holds
+// a quarter of each group. The W warps' sums meet in shared memory, in order; the activation and the
+// product follow there. (The warp-level products are no bottleneck: 2 cycles an SM each, 24 or 8 of
+// them for 4096 weights, of which HBM brings 46 a cycle and SM. A tcgen05 tile would spend its time
+// filling TMEM.)
+//
+// gated_few_kernel, one launch: a nibble OR-ed into the mantissa of bf16 128.0 is 128 + q, exactly (a
+// shift and a mask for two of them); the products with bf16 activations are exact too, and
+//     y += s (sum (128 + q) x - (128 + z) sum x)
+// in fp32 after each group, with sum x from a product with a matrix of ones. M <= 8 (16) tokens are the
+// N = 8 columns of one (two) products. It is bound by instructions, about 400 a block of 4096 weights.
+//
+// gated_bytes_kernel, for one or two tokens of large layers: the activations become integers once, in a
+// small kernel before it. Each slice of a token (a group's columns) is divided by a power of two so that
+// its largest magnitude is under 2^22, rounded (exact for bf16 values within 2^14 of the largest, else
+// off by 2^-22 of it) and split in three signed bytes, a column each: x = (c0 + 2^8 c1 + 2^16 c2) 2^e.
+// Three instructions then make a word of eight codes two A registers of mma.m16n8k32 on unsigned and
+// signed bytes, and after each group, exact until then,
+//     y_c += (s f_c) (sum q c - z sum c),   f_c = 2^(e + 8 i),
+// in fp32 for each byte column; a token's three meet at the end. 277 instructions a block.
+//
+// Which one: one token through 14336 x 4096 takes 27.7 us with the first and 19.6 us with the second;
+// 5632 x 2048 takes 10.1 and 11.4 us, and small layers lose the second launch's 2 us. The bytes start at
+// 2^25 weights a matrix. Four tokens take 28 us either way, eight 29 and 34 us: more than two stay with
+// the first.
 #include "w4_common.cuh"
 #include "w4_expand_gemm.cuh"
 
@@ -25,8 +39,11 @@ namespace gated {
 using xg::Weight;
 using xg::act_of;
 
-constexpr int WARPS = 8;          // of a block: they share its features' columns
-constexpr int SCALE_WORDS = 6144;  // of shared memory for a run of groups (24 KB; 18 KB hold the sums)
+constexpr int WARPS = 8;           // of a block of gated_few_kernel
+constexpr int B_WARPS = 4;         // of gated_bytes_kernel: with two blocks ahead a warp, 96 KB an SM in flight
+constexpr int AHEAD = 2;           // column blocks of a warp in flight there (3: 20.2 us, 4: 30.5 us)
+constexpr int BLOCK_BYTES = 2048;  // codes of 32 rows and 128 columns
+constexpr int MAX_RUN = 192;       // groups whose scales are in shared memory at a time: 24 KB
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -38,8 +55,24 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 // codes i and i + 4 of eight as the bf16 pair 128 + q
 __device__ __forceinline__ uint32_t codes_pair(uint32_t w, int i) { return ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u; }
 
+__device__ __forceinline__ void mma16832(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The activations as bytes: column c = 3 m + i holds byte i of token m, each eight of its K values in
+// the order 0, 2, 4, 6, 1, 3, 5, 7 (the order in which a code word falls apart).
+struct Bytes {
+    int8_t *x;                // [3 M][K]
+    float *f;                 // [slice][columns] 2^(e + 8 i); columns are padded to whole products
+    int *sum;                 // [slice][columns] sum of the bytes
+};
 struct FewArgs {
     const __nv_bfloat16 *x;   // [M, K]
+    Bytes v;                  // gated_bytes_kernel
     Weight w[2];              // gate, up
     __nv_bfloat16 *y;         // [M, H]
     int64_t H, K;
@@ -202,21 +235,269 @@ __global__ void __launch_bounds__(WARPS * 32) gated_few_kernel(const FewArgs a) 
     }
 }
 
+// One warp per token and slice of GB columns.
+template <int GB> __global__ void __launch_bounds__(128) bytes_prep_kernel(const FewArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int lane = threadIdx.x & 31;
+    const int64_t slices = a.K / GB, i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (i >= slices * a.M) return;
+    const int64_t slice = i % slices;
+    const int m = (int)(i / slices);
+    const __nv_bfloat16 *x = a.x + (int64_t)m * a.K + slice * GB;
+    constexpr int N = GB / 32;
+    float v[N], top = 0.0f;
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        v[j] = __bfloat162float(x[lane + 32 * j]);
+        bad = bad || !(fabsf(v[j]) <= 3.4e38f);
+        top = fmaxf(top, fabsf(v[j]));
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
+    bad = __any_sync(FULL, bad);
+    int e = (int)(__float_as_uint(top) >> 23) - 127;  // 2^e <= top < 2^(e + 1)
+    e = e < -100 ? -100 : e;
+    const float scale = __uint_as_float((uint32_t)(21 - e + 127) << 23);
+    int sums[3] = {0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int k = lane + 32 * j, at = (k & ~7) + ((k & 1) << 2) + ((k & 7) >> 1);
+        const int q = bad ? 0 : __float2int_rn(v[j] * scale);  // under 2^22 in magnitude
+        const int c0 = (int)(int8_t)q, r1 = (q - c0) >> 8, c1 = (int)(int8_t)r1, c2 = (r1 - c1) >> 8;
+        int8_t *o = a.v.x + (int64_t)(3 * m) * a.K + slice * GB + at;
+        o[0] = (int8_t)c0;
+        o[a.K] = (int8_t)c1;
+        o[2 * a.K] = (int8_t)c2;
+        sums[0] += c0;
+        sums[1] += c1;
+        sums[2] += c2;
+    }
+#pragma unroll
+    for (int c = 0; c < 3; ++c) {
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) sums[c] += __shfl_xor_sync(FULL, sums[c], o);
+        if (lane == 0) {
+            const int ec = e - 21 + 8 * c;  // from -121; a slice that is not finite gives NaN
+            a.v.f[slice * 8 + 3 * m + c] = bad ? __int_as_float(0x7fffffff) : __uint_as_float((uint32_t)(ec + 127) << 23);
+            a.v.sum[slice * 8 + 3 * m + c] = sums[c];
+        }
+    }
+}
+
+// 16 bytes from global to shared memory, or 16 zero bytes
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Codes of one column block in a warp's shared memory: for the gate's and the up's fragment (m) and
+// rows r and r + 8 (h), 64 bytes a row, rows one after the other. GB is the group, or 128 for groups
+// of 256 (whose halves share a scale): lane t of a row takes bytes [GB/8 t, GB/8 (t + 1)) of each
+// group's GB/2 as words (GB/32) g + i.
+template <int GB> __device__ __forceinline__ void block_words(uint32_t at, int r, int t, uint32_t (&w)[2][2][4]) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t row = at + (uint32_t)((2 * m + h) * 512 + r * 64);
+            if (GB == 128) {
+                const uint4 v = xg::lds128(row + (uint32_t)t * 16u);
+                w[m][h][0] = v.x; w[m][h][1] = v.y; w[m][h][2] = v.z; w[m][h][3] = v.w;
+            } else if (GB == 64) {
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const uint2 v = xg::lds64(row + (uint32_t)(32 * g + 8 * t));
+                    w[m][h][2 * g] = v.x;
+                    w[m][h][2 * g + 1] = v.y;
+                }
+            } else {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) w[m][h][g] = xg::lds32(row + (uint32_t)(16 * g + 4 * t));
+            }
+        }
+}
+
+template <int GB> __global__ void __launch_bounds__(B_WARPS * 32, 8) gated_bytes_kernel(const FewArgs a) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    // [warp][AHEAD] column blocks, later the warps' sums; then [group of the run][32 rows] s | z << 16
+    uint32_t *sc = reinterpret_cast<uint32_t *>(smem + B_WARPS * AHEAD * BLOCK_BYTES);
+    float(*sums)[32][9] = reinterpret_cast<float(*)[32][9]>(smem);
+    static_assert(sizeof(float) * 32 * 9 <= AHEAD * BLOCK_BYTES, "sums of one warp");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
+    const int64_t h0 = (int64_t)blockIdx.x * 16, J = a.K >> a.gshift;
+    const int blocks = (int)((a.K + 127) / 128), per_run = (int)(((int64_t)a.run << a.gshift) / 128);
+    const uint32_t ring = smem_addr(smem) + (uint32_t)(warp * AHEAD * BLOCK_BYTES);
+
+    const uint8_t *p[2][2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t row = h0 + r + 8 * h;
+            p[m][h] = a.w[m].codes + (row < a.H ? row : a.H - 1) * (a.K >> 1) + 16 * t;
+        }
+    auto fetch = [&](int b, int slot) {
+        if (b < blocks) {
+            const bool in = GB == 128 || (int64_t)b * 128 + 32 * t < a.K;  // the last block may be cut at a group
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    copy16(ring + (uint32_t)(slot * BLOCK_BYTES + (2 * m + h) * 512 + lane * 16),
+                           in ? p[m][h] + (int64_t)b * 64 : a.w[m].codes, in);
+        }
+        copy_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) fetch(warp + i * B_WARPS, i);
+
+    // this lane's byte column of each product (one that does not exist repeats the last: its sums are
+    // not used)
+    const int8_t *xp = a.v.x + (int64_t)(r < 3 * a.M ? r : 3 * a.M - 1) * a.K + (GB / 4) * t;
+    float acc[2][4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][i] = 0.0f;
+
+    int b = warp, slot = 0;
+    for (int run0 = 0; run0 < blocks; run0 += per_run) {
+        const int run1 = run0 + per_run < blocks ? run0 + per_run : blocks;
+        const int j0 = (int)(((int64_t)run0 * 128) >> a.gshift), j1 = j0 + a.run < J ? j0 + a.run : (int)J;
+        if (run0 > 0) __syncthreads();  // the previous run's readers
+        for (int row = warp; row < 32; row += B_WARPS) {
+            const Weight &w = a.w[row >> 4];
+            const int64_t h = (h0 + (row & 15) < a.H ? h0 + (row & 15) : a.H - 1) * J;
+            for (int j = j0 + lane; j < j1; j += 32) {
+                const uint32_t s = __ldg(w.scales + h + j);
+                const uint32_t z = w.zeros ? (uint32_t)(uint16_t)__ldg(w.zeros + h + j) : 8u;
+                sc[(j - j0) * 32 + row] = s | (z << 16);
+            }
+        }
+        __syncthreads();
+        if (run0 == 0) asm volatile("griddepcontrol.wait;" ::: "memory");  // the bytes are bytes_prep_kernel's
+        for (; b < run1; b += B_WARPS) {
+            const int k0 = b * 128;
+            copy_wait<AHEAD - 1>();
+            __syncwarp();
+            uint32_t w[2][2][4];
+            block_words<GB>(ring + (uint32_t)(slot * BLOCK_BYTES), r, t, w);
+            __syncwarp();
+            fetch(b + AHEAD * B_WARPS, slot);
+            slot = slot + 1 == AHEAD ? 0 : slot + 1;
+#pragma unroll
+            for (int g = 0; g < 128 / GB; ++g) {
+                if (GB != 128 && k0 + g * GB >= a.K) break;
+                const int slice = (k0 + g * GB) / GB;
+                const uint32_t *sg = sc + (((k0 + g * GB) >> a.gshift) - j0) * 32;
+                float s[2][2];
+                int z[2][2];
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t sz = sg[16 * m + r + 8 * h];
+                        s[m][h] = __half2float(__ushort_as_half((unsigned short)(sz & 0xFFFFu)));
+                        z[m][h] = (int)(int16_t)(sz >> 16);
+                    }
+                // eight bytes of this lane's column for each of the group's words
+                uint32_t x[8];
+                const int8_t *q = xp + k0 + g * GB;
+                if (GB >= 64) {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(q);
+                    x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+                } else {
+                    const uint2 u = *reinterpret_cast<const uint2 *>(q);
+                    x[0] = u.x; x[1] = u.y;
+                }
+                if (GB == 128) {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(q + 16);
+                    x[4] = u.x; x[5] = u.y; x[6] = u.z; x[7] = u.w;
+                }
+                const float2 f = *reinterpret_cast<const float2 *>(a.v.f + (int64_t)slice * 8 + 2 * t);
+                const int2 d = *reinterpret_cast<const int2 *>(a.v.sum + (int64_t)slice * 8 + 2 * t);
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    int P[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int i = 0; i < GB / 32; ++i) {
+                        const uint32_t lo = w[m][0][(GB / 32) * g + i], hi = w[m][1][(GB / 32) * g + i];
+                        mma16832(P, lo & 0x0F0F0F0Fu, hi & 0x0F0F0F0Fu, (lo >> 4) & 0x0F0F0F0Fu, (hi >> 4) & 0x0F0F0F0Fu,
+                                 x[2 * i], x[2 * i + 1]);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        acc[m][2 * h] = fmaf(s[m][h] * f.x, (float)(P[2 * h] - z[m][h] * d.x), acc[m][2 * h]);
+                        acc[m][2 * h + 1] = fmaf(s[m][h] * f.y, (float)(P[2 * h + 1] - z[m][h] * d.y), acc[m][2 * h + 1]);
+                    }
+                }
+            }
+        }
+    }
+    // the warps' sums take the place of the codes: rows r and r + 8 of each fragment, columns 2 t and
+    // 2 t + 1
+    copy_wait<0>();
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sums[warp][16 * m + r + 8 * (i >> 1)][2 * t + (i & 1)] = acc[m][i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 16 * a.M; i += B_WARPS * 32) {
+        const int f = i & 15, c = 3 * (i >> 4);
+        float g = 0.0f, u = 0.0f;
+#pragma unroll
+        for (int k = 2; k >= 0; --k)  // the large bytes first
+#pragma unroll
+            for (int w = 0; w < B_WARPS; ++w) {
+                g += sums[w][f][c + k];
+                u += sums[w][16 + f][c + k];
+            }
+        if (h0 + f < a.H) a.y[(int64_t)(i >> 4) * a.H + h0 + f] = __float2bfloat16_rn(act_of(g, a.act).value * u);
+    }
+}
+
+// The kernel of the bytes, and its workspace (behind the arrival counters of the other shapes' calls,
+// which stay zero).
+inline bool by_bytes(int64_t M, int64_t H, int64_t K) { return M <= 2 && H * K >= ((int64_t)1 << 25); }
+
+struct BytesPlace {
+    size_t x, f, sum, end;
+};
+inline BytesPlace bytes_place(int64_t M, int64_t K, int group) {
+    const size_t slices = (size_t)(K / (group < 128 ? group : 128));
+    BytesPlace q;
+    q.x = xg::CNT_BYTES;
+    q.f = (q.x + (size_t)(3 * M * K) + 255) / 256 * 256;
+    q.sum = (q.f + slices * 8 * 4 + 255) / 256 * 256;
+    q.end = (q.sum + slices * 8 * 4 + 255) / 256 * 256;
+    return q;
+}
+
 template <int GB> w4_status launch_few(const FewArgs &a, cudaStream_t stream) {
     const unsigned grid = (unsigned)((a.H + 15) / 16);
-    const size_t smem = (size_t)a.run * 32 * sizeof(uint32_t);
+    const size_t scales = (size_t)a.run * 32 * sizeof(uint32_t);
+    if (by_bytes(a.M, a.H, a.K)) {
+        const int64_t warps = a.K / GB * a.M;
+        bytes_prep_kernel<GB><<<(unsigned)((warps + 3) / 4), 128, 0, stream>>>(a);
+        const w4_status st = launch_status();
+        return st != W4_OK ? st : xg::launch_behind(gated_bytes_kernel<GB>, grid, B_WARPS * 32,
+                                                    (size_t)(B_WARPS * AHEAD * BLOCK_BYTES) + scales, stream, a);
+    }
     if (a.M <= 8)
-        gated_few_kernel<GB, 1><<<grid, WARPS * 32, smem, stream>>>(a);
+        gated_few_kernel<GB, 1><<<grid, WARPS * 32, scales, stream>>>(a);
     else
-        gated_few_kernel<GB, 2><<<grid, WARPS * 32, smem, stream>>>(a);
+        gated_few_kernel<GB, 2><<<grid, WARPS * 32, scales, stream>>>(a);
     return launch_status();
 }
+static_assert(B_WARPS * AHEAD * BLOCK_BYTES + MAX_RUN * 128 <= 48 * 1024, "no opt-in to more shared memory");
 
 inline w4_status gated_few(FewArgs a, int group, cudaStream_t stream) {
     // a run holds whole blocks of 128 columns and of the group
     const int64_t J = a.K >> a.gshift;
-    a.run = SCALE_WORDS / 32;
-    if (J < a.run) a.run = (int)((J + 3) / 4 * 4);
+    a.run = J < MAX_RUN ? (int)((J + 3) / 4 * 4) : MAX_RUN;
     return group == 32 ? launch_few<32>(a, stream) : group == 64 ? launch_few<64>(a, stream) : launch_few<128>(a, stream);
 }
 
@@ -248,7 +529,8 @@ w4_status weight_ok(const uint8_t *codes, const uint16_t *scales, const int16_t 
 }  // namespace
 
 W4_API size_t w4a16_gated_workspace_bytes(int64_t M, int64_t H, int64_t K, int group) {
-    if (!gated_shape_ok(M, H, K) || !valid_group(group) || K % group != 0 || M <= kFewRows) return 0;
+    if (!gated_shape_ok(M, H, K) || !valid_group(group) || K % group != 0) return 0;
+    if (M <= kFewRows) return gated::by_bytes(M, H, K) ? gated::bytes_place(M, K, group).end : 0;
     return xg::place_prep(xg::make_plan(xg::FWD, H, M, K, 1, 0, num_sms()).bytes, M * K, M).end;
 }
 
@@ -266,6 +548,14 @@ W4_API w4_status w4a16_gated(const void *X_bf16, int64_t M, const uint8_t *codes
     if (!aligned16(X_bf16) || !aligned16(Y_bf16) || (workspace && !aligned16(workspace))) return W4_ERR_ALIGN;
     if (M <= kFewRows) {
         gated::FewArgs f = {};
+        if (gated::by_bytes(M, H, K)) {
+            const gated::BytesPlace q = gated::bytes_place(M, K, group);
+            if (!workspace || workspace_bytes < q.end) return W4_ERR_WORKSPACE;
+            uint8_t *ws = static_cast<uint8_t *>(workspace);
+            f.v.x = reinterpret_cast<int8_t *>(ws + q.x);
+            f.v.f = reinterpret_cast<float *>(ws + q.f);
+            f.v.sum = reinterpret_cast<int *>(ws + q.sum);
+        }
         f.x = static_cast<const __nv_bfloat16 *>(X_bf16);
         f.w[0] = {codes_gate, scales_gate, zeros_gate};
         f.w[1] = {codes_up, scales_up, zeros_up};

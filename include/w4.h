@@ -547,16 +547,18 @@ w4_status w4_nf4_gemv(const void *x_bf16, int64_t M, const uint8_t *codes, const
  *   codes, scales, zeros (gate and up)   device, w4_quantize's outputs for Wg[H, K] and Wu[H, K],
  *                the same group and mode for both; zeros NULL for W4_SYM, required for W4_ASYM
  *   Y_bf16       device, bf16 [M, H]
- *   workspace    NULL where w4a16_gated_workspace_bytes(M, H, K, group) is 0 (M <= 16), else device
- *                scratch of at least that many bytes (an fp16 copy of X; partial sums of outputs whose
- *                K range is shared by several SMs, and their arrival counters). Zero-fill it before its
+ *   workspace    NULL where w4a16_gated_workspace_bytes(M, H, K, group) is 0 (M <= 16, but for one or
+ *                two rows of layers from H * K = 2^25), else device scratch of at least that many bytes
+ *                (a copy of X in the kernels' own form; partial sums of outputs whose K range is shared
+ *                by several SMs, and their arrival counters). Zero-fill it before its
  *                first use; every call that completes leaves its counters zero again, so one workspace
  *                serves any sequence of calls, of this and of the three entry points below, whose
  *                queries ask for no more, on one stream. Calls that may run
  *                concurrently need separate workspaces. After a call whose kernel recorded an error
  *                in the device status, zero-fill it again.
  *   M <= 16: the weights enter as exact integers and group scales and zero points are applied in
- *   fp32 (about 1e-6 relative before the one rounding to bf16). M > 16: tcgen05 MMAs on weights
+ *   fp32 (about 1e-5 relative before the one rounding to bf16; an infinity in a row may make that
+ *   row's outputs NaN). M > 16: tcgen05 MMAs on weights
  *   dequantized to fp16 with one rounding (relative 2^-11 per weight; |w| up to 65504) and fp32
  *   accumulation; X enters as fp16 after each row is divided by a power of two, exact for values
  *   within 2^-31 of the row's largest.

@@ -93,6 +93,9 @@ SHAPES = [
     (17, 64, 128, 128, "asym"), (17, 3, 32, 32, "asym"), (33, 100, 96, 32, "sym"), (64, 65, 256, 64, "asym"),
     (100, 333, 576, 64, "sym"), (129, 127, 1024, 256, "asym"), (255, 64, 160, 32, "asym"), (257, 193, 1088, 64, "asym"),
     (300, 1000, 2048, 128, "asym"), (520, 96, 8192, 256, "sym"), (1, 2049, 2048, 128, "asym"), (3, 515, 14336, 128, "asym"),
+    # one and two rows of layers from 2^25 weights a matrix (their own kernel), and three beside them
+    (1, 8200, 4096, 128, "asym"), (2, 4097, 8192, 32, "sym"), (2, 16391, 2048, 64, "asym"), (1, 2056, 16384, 256, "asym"),
+    (1, 65536, 544, 32, "asym"), (3, 8192, 4096, 64, "sym"),
 ]
 
 
@@ -110,6 +113,21 @@ def test_gated_zero_points_outside_the_codes(M, shift):
     wg, wu = weights(72, 256, 64, "asym", 5, shift)
     assert int(wg[2].abs().max()) > 60
     check_gated(R.rows(M, 256, 7, DEV), wg, wu, 64, "asym", "silu")
+
+
+def test_gated_two_large_rows_are_independent():
+    """As below, for the kernel of one and two rows: rows of very different sizes, a NaN in one, and
+    slices of zeros and of tiny values."""
+    H, K = 4096, 8192
+    wg, wu = weights(H, K, 128, "asym", 3)
+    x = R.rows(2, K, 4, DEV)
+    x[0, 256:512], x[0, 512:640], x[1] = 0.0, 2.0 ** -130, x[1] * 2.0 ** 20
+    check_gated(x, wg, wu, 128, "asym", "gelu_tanh")
+    base = run_gated(x, wg, wu, 128, "asym", "silu")
+    x[1, 700] = float("nan")
+    y = run_gated(x, wg, wu, 128, "asym", "silu")
+    status_ok()
+    assert torch.equal(y[0], base[0]) and bool(torch.isnan(y[1]).all())
 
 
 @pytest.mark.parametrize("M", [6, 50])
@@ -215,7 +233,7 @@ def test_dgrad(M, N, K, group, mode):
 
 def test_results_do_not_change_from_run_to_run_and_workspaces_serve_again():
     """One workspace of the largest need over several shapes, each twice: the same bits."""
-    shapes = [(40, 64, 4096, 128), (300, 64, 2048, 128), (17, 200, 8192, 128)]
+    shapes = [(40, 64, 4096, 128), (300, 64, 2048, 128), (1, 8192, 4096, 128), (17, 200, 8192, 128)]
     n = max(w4.w4a16_gated_workspace_bytes(*s) for s in shapes)
     ws = torch.zeros(max(n, 16), dtype=torch.uint8, device=DEV)
     for M, H, K, g in shapes + shapes[::-1]:
@@ -230,7 +248,7 @@ def test_results_do_not_change_from_run_to_run_and_workspaces_serve_again():
 def test_another_stream_and_a_replayed_graph():
     """Calls on a side stream and in a captured graph, replayed on new inputs."""
     g, act = 64, "silu"
-    for M, H, K in [(4, 200, 512), (70, 72, 4096)]:
+    for M, H, K in [(4, 200, 512), (2, 8192, 4096), (70, 72, 4096)]:
         wg, wu = weights(H, K, g, "asym", 2)
         x = [R.rows(M, K, s, DEV) for s in (1, 2, 3)]
         want = [run_gated(v, wg, wu, g, "asym", act) for v in x]
