@@ -183,5 +183,5 @@ W4_API w4_status fp8_ckpt_wgrad(const void *dY_bf16, const uint8_t *X_e4m3, cons
     a.K = K;
     a.cols = N;
     a.out_fp32 = fp32 ? 1 : 0;
-    return xg::launch<xg::WGRAD, false>(p, tm, a, workspace, sms, stream);
+    return xg::launch<xg::WGRAD, false, false>(p, tm, a, workspace, sms, stream);
 }

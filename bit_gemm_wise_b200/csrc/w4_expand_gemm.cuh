@@ -112,7 +112,7 @@ struct Args {
     int NT;                   // columns per tile, a multiple of 16
     int stages, raws;         // of the expanded operands and of the codes
     uint32_t stage_bytes;
-    int gshift, asym, act, out_fp32;
+    int gshift, asym, out_fp32;
 };
 
 // tensor maps: B (DGRAD: of one or two sources) and the codes of A (FWD: gate, up)
@@ -300,8 +300,7 @@ __device__ __forceinline__ bool elect_one() {
 struct Act {
     float value, slope;
 };
-__device__ __forceinline__ Act act_of(float g, int act) {
-    const bool gelu = act == W4_ACT_GELU_TANH;
+__device__ __forceinline__ Act act_of(float g, bool gelu) {
     const float g2 = 0.07135481282f * g * g;                     // 2 sqrt(2/pi) 0.044715 g^2
     const float p = gelu ? g * (1.5957691216f + g2) : g;
     const float dp = gelu ? 1.5957691216f + 3.0f * g2 : 1.0f;     // p'
@@ -367,7 +366,9 @@ struct Walk {
 // on a loaded value may stand between the two, or each stage costs a memory latency.
 template <int KIND> struct Scales {
     uint16_t s[2], z[2];      // fp16 scales and zero points; WGRAD: scale bytes in s
-    bool there[2];
+    bool there[2];            // FWD: the row, the columns; else each chunk
+    const uint16_t *ps[2], *pz[2];  // FWD: of the tile's rows (for symmetric weights pz is ps)
+    uint32_t tile = ~0u;            // FWD: whose rows they are
 
     __device__ __forceinline__ void fetch(const Args &a, const Walk &w, int tt) {
         const int K = (int)a.K, rows = (int)a.rows;  // at most 2^24
@@ -382,15 +383,36 @@ template <int KIND> struct Scales {
             return;
         }
         const int J = K >> a.gshift;
-        const int src = KIND == DGRAD && w.kb >= a.KB0 ? 1 : 0;
-        const int row = KIND == FWD ? (int)w.un.tw * 64 + (tt >> 1) : (w.kb - (src ? a.KB0 : 0)) * BK + (tt >> 2);
-        const int k = KIND == FWD ? w.kb * BK + 32 * (tt & 1) : (int)w.un.tw * 128 + 32 * (tt & 3);
+        if (KIND == FWD) {
+            if (w.un.tw != tile) {
+                tile = w.un.tw;
+                const int row = (int)tile * 64 + (tt >> 1);
+                there[0] = row < rows;
+                const int64_t at = there[0] ? (int64_t)row * J : 0;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    ps[j] = a.w[j].scales + at;
+                    pz[j] = (a.asym ? reinterpret_cast<const uint16_t *>(a.w[j].zeros) : a.w[j].scales) + at;
+                }
+            }
+            const int k = w.kb * BK + 32 * (tt & 1);
+            there[1] = k < K;
+            const int i = there[1] ? k >> a.gshift : 0;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                s[j] = __ldg(ps[j] + i);
+                z[j] = __ldg(pz[j] + i);
+            }
+            return;
+        }
+        const int src = w.kb >= a.KB0 ? 1 : 0;
+        const int row = (w.kb - (src ? a.KB0 : 0)) * BK + (tt >> 2), k = (int)w.un.tw * 128 + 32 * (tt & 3);
         const int64_t at = (int64_t)row * J + (k >> a.gshift);
+        const Weight &m = a.w[src];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const Weight &m = a.w[KIND == FWD ? j : src];
-            there[j] = k < K && row + (KIND == FWD ? 0 : 32 * j) < rows;
-            const int64_t i = there[j] ? at + (KIND == FWD ? 0 : 32 * j * J) : 0;
+            there[j] = k < K && row + 32 * j < rows;
+            const int64_t i = there[j] ? at + 32 * j * J : 0;
             s[j] = __ldg(m.scales + i);
             // symmetric weights: the scale again, for the sake of one instruction stream
             z[j] = __ldg((a.asym ? reinterpret_cast<const uint16_t *>(m.zeros) : m.scales) + i);
@@ -400,7 +422,7 @@ template <int KIND> struct Scales {
     // scale 0 (its codes read as zero)
     __device__ __forceinline__ uint32_t word(const Args &a, int j) const {
         if (KIND == WGRAD) return there[j] ? (uint32_t)s[j] : 127u;
-        return there[j] ? (uint32_t)s[j] | ((a.asym ? (uint32_t)z[j] : 8u) << 16) : 8u << 16;
+        return (KIND == FWD ? there[0] && there[1] : there[j]) ? (uint32_t)s[j] | ((a.asym ? (uint32_t)z[j] : 8u) << 16) : 8u << 16;
     }
 };
 
@@ -489,7 +511,7 @@ __host__ __device__ __forceinline__ constexpr int value_at8(int place) { return 
 __host__ __device__ __forceinline__ constexpr int value_at4(int place) { return (place >> 1) | ((place & 1) << 1); }
 
 // Results of columns [c, c + 16) of a tile, of which n exist, for this thread's lane.
-template <int KIND, bool GRADS>
+template <int KIND, bool GRADS, bool GELU>
 __device__ __forceinline__ void emit(const Args &a, const float *row_pow, const Unit &un, int q4, int lane, int c, int n,
                                      const float (&v)[16], bool add) {
     const int64_t col = (int64_t)un.tn * a.NT + c;
@@ -505,26 +527,27 @@ __device__ __forceinline__ void emit(const Args &a, const float *row_pow, const 
         const int64_t h = (int64_t)un.tw * 64 + 16 * q4 + (lane & 15);
         const int64_t at = (col + up) * a.rows + h, step = 2 * a.rows;
         const int m = h < a.rows ? n - up : 0;  // this lane's tokens are those with 2 i < m
+        const bool whole = __all_sync(FULL, m >= 15);  // no test a value where all are wanted
         float d[8];
         if (GRADS) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) d[i] = 2 * i < m ? __bfloat162float(a.dh[at + i * step]) : 0.0f;
+            for (int i = 0; i < 8; ++i) d[i] = whole || 2 * i < m ? __bfloat162float(a.dh[at + i * step]) : 0.0f;
         }
-        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.out) + at;
+        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.out) + at, *o2 = a.out2 + at;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float got = __shfl_xor_sync(FULL, up ? v[2 * i] : v[2 * i + 1], 16);
             const float4 p4 = pw[KIND == WGRAD ? 0 : i >> 1];
             const float f = i & 1 ? (up ? p4.w : p4.z) : (up ? p4.y : p4.x);
             const float g = f * (up ? got : v[2 * i]), u = f * (up ? v[2 * i + 1] : got);
-            const Act t = act_of(g, a.act);
-            if (2 * i < m) {
-                if (GRADS) {
-                    o[i * step] = __float2bfloat16_rn(d[i] * u * t.slope);
-                    a.out2[at + i * step] = __float2bfloat16_rn(d[i] * t.value);
-                } else {
-                    o[i * step] = __float2bfloat16_rn(t.value * u);
-                }
+            const Act t = act_of(g, GELU);
+            const __nv_bfloat16 first = __float2bfloat16_rn(GRADS ? d[i] * u * t.slope : t.value * u);
+            if (whole) {
+                o[i * step] = first;
+                if (GRADS) o2[i * step] = __float2bfloat16_rn(d[i] * t.value);
+            } else if (2 * i < m) {
+                o[i * step] = first;
+                if (GRADS) o2[i * step] = __float2bfloat16_rn(d[i] * t.value);
             }
         }
     } else {
@@ -549,7 +572,7 @@ __device__ __forceinline__ void emit(const Args &a, const float *row_pow, const 
     }
 }
 
-template <int KIND, bool GRADS>
+template <int KIND, bool GRADS, bool GELU>
 __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_constant__ Maps tm,
                                                                  const __grid_constant__ Args a) {
     extern __shared__ uint8_t smem_raw[];
@@ -785,7 +808,7 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
                             *p = f;
                         }
                     } else {
-                        emit<KIND, GRADS>(a, row_pow, un, q4, lane, c, ncols - c, v, s0 > un.b0);
+                        emit<KIND, GRADS, GELU>(a, row_pow, un, q4, lane, c, ncols - c, v, s0 > un.b0);
                     }
                 }
                 tc_fence_before();
@@ -833,7 +856,7 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
                         }
                     }
                 }
-                emit<KIND, GRADS>(a, row_pow, un, q4, lane, c, ncols - c, v, false);
+                emit<KIND, GRADS, GELU>(a, row_pow, un, q4, lane, c, ncols - c, v, false);
             }
             if (!helper && lane == 0) *cnt = 0u;  // ready for the next call
         }
@@ -1087,7 +1110,7 @@ w4_status launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads, s
     return launch_status();
 }
 
-template <int KIND, bool GRADS>
+template <int KIND, bool GRADS, bool GELU>
 w4_status launch(const Plan &p, Maps &tm, Args a, void *workspace, int sms, cudaStream_t stream) {
     if (p.units > (1 << 30)) return W4_ERR_SHAPE;  // more than the kernel counts
     bool maps = true;
@@ -1118,13 +1141,13 @@ w4_status launch(const Plan &p, Maps &tm, Args a, void *workspace, int sms, cuda
     if (!a.status) return W4_ERR_CUDA;
     const int smem = (int)(p.stages * p.stage_bytes + p.raws * Raw<KIND>::BYTES + CONTROL) + 1024;
     static std::atomic<uint64_t> attr_done{0};
-    if (!allow_smem(expand_gemm_kernel<KIND, GRADS>, (int)SMEM_MAX, attr_done)) return W4_ERR_CUDA;
+    if (!allow_smem(expand_gemm_kernel<KIND, GRADS, GELU>, (int)SMEM_MAX, attr_done)) return W4_ERR_CUDA;
     const unsigned grid = (unsigned)(p.units < sms ? p.units : sms);
     // FWD and DGRAD follow row_prep_kernel: they may start, and read weights, while it finishes.
     // Whatever came before on the stream was complete when it began.
     if (KIND != WGRAD)
-        return launch_behind(expand_gemm_kernel<KIND, GRADS>, grid, THREADS, (size_t)smem, stream, tm, a);
-    expand_gemm_kernel<KIND, GRADS><<<grid, THREADS, smem, stream>>>(tm, a);
+        return launch_behind(expand_gemm_kernel<KIND, GRADS, GELU>, grid, THREADS, (size_t)smem, stream, tm, a);
+    expand_gemm_kernel<KIND, GRADS, GELU><<<grid, THREADS, smem, stream>>>(tm, a);
     return launch_status();
 }
 

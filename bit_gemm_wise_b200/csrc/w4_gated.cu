@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(WARPS * 32) gated_few_kernel(const FewArgs a) 
             u += sums[w][n][16 + f][c];
         }
         if (h0 + f < a.H && 8 * n + c < a.M)
-            a.y[(int64_t)(8 * n + c) * a.H + h0 + f] = __float2bfloat16_rn(act_of(g, a.act).value * u);
+            a.y[(int64_t)(8 * n + c) * a.H + h0 + f] = __float2bfloat16_rn(act_of(g, a.act == W4_ACT_GELU_TANH).value * u);
     }
 }
 
@@ -455,7 +455,7 @@ template <int GB> __global__ void __launch_bounds__(B_WARPS * 32, 8) gated_bytes
                 g += sums[w][f][c + k];
                 u += sums[w][16 + f][c + k];
             }
-        if (h0 + f < a.H) a.y[(int64_t)(i >> 4) * a.H + h0 + f] = __float2bfloat16_rn(act_of(g, a.act).value * u);
+        if (h0 + f < a.H) a.y[(int64_t)(i >> 4) * a.H + h0 + f] = __float2bfloat16_rn(act_of(g, a.act == W4_ACT_GELU_TANH).value * u);
     }
 }
 
@@ -594,8 +594,8 @@ W4_API w4_status w4a16_gated(const void *X_bf16, int64_t M, const uint8_t *codes
     a.K = K;
     a.cols = M;
     a.gshift = group_shift(group);
-    a.act = act;
-    return xg::launch<xg::FWD, false>(p, tm, a, workspace, sms, stream);
+    return act == W4_ACT_SILU ? xg::launch<xg::FWD, false, false>(p, tm, a, workspace, sms, stream)
+                              : xg::launch<xg::FWD, false, true>(p, tm, a, workspace, sms, stream);
 }
 
 namespace {
@@ -664,14 +664,14 @@ W4_API w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const 
     a.K = K;
     a.cols = M;
     a.gshift = group_shift(group);
-    a.act = act;
     a.dh = static_cast<const __nv_bfloat16 *>(dH_bf16);
     a.out = dG_bf16;
     a.out2 = static_cast<__nv_bfloat16 *>(dU_bf16);
     a.row_pow = prep.row_pow;
     if (!xg::make_map(&tm.b[0], prep.y[0], M, K, l.grads.NT)) return W4_ERR_CUDA;
     tm.b[1] = tm.b[0];
-    st = xg::launch<xg::FWD, true>(l.grads, tm, a, workspace, sms, stream);
+    st = act == W4_ACT_SILU ? xg::launch<xg::FWD, true, false>(l.grads, tm, a, workspace, sms, stream)
+                            : xg::launch<xg::FWD, true, true>(l.grads, tm, a, workspace, sms, stream);
     if (st != W4_OK || !dX_bf16) return st;
     prep.x[0] = static_cast<const __nv_bfloat16 *>(dG_bf16);
     prep.x[1] = static_cast<const __nv_bfloat16 *>(dU_bf16);
@@ -687,7 +687,7 @@ W4_API w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const 
     a.dh = nullptr;
     a.out = dX_bf16;
     a.out2 = nullptr;
-    return xg::launch<xg::DGRAD, false>(l.dx, tm, a, workspace, sms, stream);
+    return xg::launch<xg::DGRAD, false, false>(l.dx, tm, a, workspace, sms, stream);
 }
 
 W4_API size_t w4a16_dgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int group) {
@@ -730,5 +730,5 @@ W4_API w4_status w4a16_dgrad(const void *dY_bf16, int64_t M, const uint8_t *code
     a.K = K;
     a.cols = M;
     a.gshift = group_shift(group);
-    return xg::launch<xg::DGRAD, false>(p, tm, a, workspace, sms, stream);
+    return xg::launch<xg::DGRAD, false, false>(p, tm, a, workspace, sms, stream);
 }
