@@ -1016,17 +1016,19 @@ inline Plan make_plan(int kind, int64_t lanes, int64_t cols, int64_t red, int so
     p.raws = GROUPS;
     while (p.stages < MAX_STAGES && (p.stages + 1) * p.stage_bytes + p.raws * rb <= room) ++p.stages;
     while (p.raws + GROUPS <= MAX_RAW && p.stages * p.stage_bytes + (p.raws + GROUPS) * rb <= room) p.raws += GROUPS;
-    // Parts of the reduction: the count with the least estimated time. In cycles: a stage takes
-    // its MMAs (2 per column) or its expansion (about 300), a unit about 2500 to start and end,
-    // and the last part of a tile reads S partial sums at about 60 bytes per cycle.
+    // Parts of the reduction: the count with the least estimated time, in cycles as measured: a stage
+    // takes its MMAs (2.1 a column) or the hand-over between the warps (470), a unit 7000 to start and
+    // end; the last part of a tile reads two partial sums of 16 columns in 1300 cycles, five groups of
+    // columns at a time, after 1500 for the count.
     const int64_t tiles = p.Tw * p.Tn;
     double best = 0;
     p.S = 1;
     for (int S = 1; S <= 32 && (S == 1 || S * 4 <= p.KB); ++S) {
         if (S > 1 && (tiles * S > 8 * (int64_t)sms || tiles > MAX_SPLIT_TILES)) break;
-        const double waves = (double)((tiles * S + sms - 1) / sms);
-        const double stage = p.NT * 2 > 300 ? p.NT * 2 : 300;
-        const double t = waves * ((double)((p.KB + S - 1) / S) * stage + 2500) + (S > 1 ? 2000 + S * p.NT * 512.0 / 60 : 0);
+        const int64_t waves = (tiles * S + sms - 1) / sms;
+        const double stage = p.NT * 2.1 > 470 ? p.NT * 2.1 : 470;
+        const double join = S > 1 ? 1500.0 + 1300.0 * ((p.NT + 79) / 80) * ((S + 1) / 2) : 0.0;
+        const double t = (double)waves * ((double)((p.KB + S - 1) / S) * stage + 7000) + join;
         if (S == 1 || t < best) {
             best = t;
             p.S = S;
