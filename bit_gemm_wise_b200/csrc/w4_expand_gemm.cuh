@@ -510,10 +510,24 @@ __device__ __forceinline__ void expand_store(uint32_t raw, uint32_t base, const 
 __host__ __device__ __forceinline__ constexpr int value_at8(int place) { return (place >> 1) | ((place & 1) << 2); }
 __host__ __device__ __forceinline__ constexpr int value_at4(int place) { return (place >> 1) | ((place & 1) << 1); }
 
+// dH at the tokens and the feature that this lane finishes of columns [c, c + 16), n of which exist
+// (see emit). Only loads: nothing waits for them before emit() uses them.
+struct Incoming {
+    uint16_t v[8];
+    __device__ __forceinline__ void fetch(const Args &a, const Unit &un, int q4, int lane, int c, int n) {
+        const int up = lane >> 4;
+        const int64_t h = (int64_t)un.tw * 64 + 16 * q4 + (lane & 15);
+        const int m = h < a.rows ? n - up : 0;
+        const uint16_t *p = reinterpret_cast<const uint16_t *>(a.dh) + ((int64_t)un.tn * a.NT + c + up) * a.rows + h;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 2 * i < m ? __ldg(p + 2 * i * a.rows) : (uint16_t)0;
+    }
+};
+
 // Results of columns [c, c + 16) of a tile, of which n exist, for this thread's lane.
 template <int KIND, bool GRADS, bool GELU>
 __device__ __forceinline__ void emit(const Args &a, const float *row_pow, const Unit &un, int q4, int lane, int c, int n,
-                                     const float (&v)[16], bool add) {
+                                     const float (&v)[16], const Incoming &dh, bool add) {
     const int64_t col = (int64_t)un.tn * a.NT + c;
     float4 pw[KIND == WGRAD ? 1 : 4];
     if (KIND != WGRAD) {
@@ -528,11 +542,6 @@ __device__ __forceinline__ void emit(const Args &a, const float *row_pow, const 
         const int64_t at = (col + up) * a.rows + h, step = 2 * a.rows;
         const int m = h < a.rows ? n - up : 0;  // this lane's tokens are those with 2 i < m
         const bool whole = __all_sync(FULL, m >= 15);  // no test a value where all are wanted
-        float d[8];
-        if (GRADS) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) d[i] = whole || 2 * i < m ? __bfloat162float(a.dh[at + i * step]) : 0.0f;
-        }
         __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.out) + at, *o2 = a.out2 + at;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -541,13 +550,14 @@ __device__ __forceinline__ void emit(const Args &a, const float *row_pow, const 
             const float f = i & 1 ? (up ? p4.w : p4.z) : (up ? p4.y : p4.x);
             const float g = f * (up ? got : v[2 * i]), u = f * (up ? v[2 * i + 1] : got);
             const Act t = act_of(g, GELU);
-            const __nv_bfloat16 first = __float2bfloat16_rn(GRADS ? d[i] * u * t.slope : t.value * u);
+            const float d = GRADS ? bf16_lo(dh.v[i]) : 0.0f;
+            const __nv_bfloat16 first = __float2bfloat16_rn(GRADS ? d * u * t.slope : t.value * u);
             if (whole) {
                 o[i * step] = first;
-                if (GRADS) o2[i * step] = __float2bfloat16_rn(d[i] * t.value);
+                if (GRADS) o2[i * step] = __float2bfloat16_rn(d * t.value);
             } else if (2 * i < m) {
                 o[i * step] = first;
-                if (GRADS) o2[i * step] = __float2bfloat16_rn(d[i] * t.value);
+                if (GRADS) o2[i * step] = __float2bfloat16_rn(d * t.value);
             }
         }
     } else {
@@ -784,6 +794,8 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
                 if (last) named_bar_sync(1 + q4, W_B / 4 * 32);
                 __syncwarp();
             }
+            Incoming ahead;  // dH of the next columns, on its way while the present ones are finished
+            if (GRADS) ahead.fetch(a, un, q4, lane, c0, ncols - c0);
             for (int s0 = un.b0; s0 < un.b1 && ok; s0 += a.seg, ++n) {
                 const int buf = n & 1;
                 if (!warp_wait(&sm->accf[buf], (uint32_t)(n >> 1) & 1u, sm, a.status)) { ok = false; break; }
@@ -808,7 +820,9 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
                             *p = f;
                         }
                     } else {
-                        emit<KIND, GRADS, GELU>(a, row_pow, un, q4, lane, c, ncols - c, v, s0 > un.b0);
+                        const Incoming now = ahead;
+                        if (GRADS) ahead.fetch(a, un, q4, lane, c + cstep, ncols - c - cstep);
+                        emit<KIND, GRADS, GELU>(a, row_pow, un, q4, lane, c, ncols - c, v, now, s0 > un.b0);
                     }
                 }
                 tc_fence_before();
@@ -856,7 +870,9 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
                         }
                     }
                 }
-                emit<KIND, GRADS, GELU>(a, row_pow, un, q4, lane, c, ncols - c, v, false);
+                const Incoming now = ahead;
+                if (GRADS) ahead.fetch(a, un, q4, lane, c + cstep, ncols - c - cstep);
+                emit<KIND, GRADS, GELU>(a, row_pow, un, q4, lane, c, ncols - c, v, now, false);
             }
             if (!helper && lane == 0) *cnt = 0u;  // ready for the next call
         }
