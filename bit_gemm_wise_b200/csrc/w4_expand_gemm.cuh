@@ -923,7 +923,7 @@ template <bool CKPT> __device__ __forceinline__ void prep_read(const Prep &p, in
             v[4 * j + 3] = bf16_hi(o[1]);
         }
     } else {
-        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p.x[t] + m * p.K) + i);
+        const uint4 w = __ldcg(reinterpret_cast<const uint4 *>((t ? p.x[1] : p.x[0]) + m * p.K) + i);
         const uint32_t o[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -935,6 +935,7 @@ template <bool CKPT> __device__ __forceinline__ void prep_read(const Prep &p, in
 
 template <bool CKPT> __global__ void __launch_bounds__(256) row_prep_kernel(const Prep p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // of the kernel before, where this one may start early
     __shared__ float top[8];
     const int64_t chunks = p.K >> 3;
     for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
@@ -967,7 +968,7 @@ template <bool CKPT> __global__ void __launch_bounds__(256) row_prep_kernel(cons
                     const __half2 h = __floats2half2_rn(lo * f, hi * f);
                     o[j] = *reinterpret_cast<const uint32_t *>(&h);
                 }
-                reinterpret_cast<uint4 *>(p.y[t] + m * p.K)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+                reinterpret_cast<uint4 *>((t ? p.y[1] : p.y[0]) + m * p.K)[i] = make_uint4(o[0], o[1], o[2], o[3]);
             }
     }
 }
@@ -983,15 +984,6 @@ inline PrepPlace place_prep(size_t at, int64_t values, int64_t M) {
     q.row_pow = (q.y + (size_t)values * 2 + 255) / 256 * 256;
     q.end = (q.row_pow + ((size_t)M + 16) * sizeof(float) + 255) / 256 * 256;
     return q;
-}
-
-inline w4_status launch_prep(const Prep &p, cudaStream_t stream) {
-    const unsigned grid = (unsigned)(p.M < (1 << 20) ? p.M : (1 << 20));
-    if (p.x8)
-        row_prep_kernel<true><<<grid, 256, 0, stream>>>(p);
-    else
-        row_prep_kernel<false><<<grid, 256, 0, stream>>>(p);
-    return launch_status();
 }
 
 // ------------------------------------------------------------------ host side
@@ -1125,6 +1117,21 @@ w4_status launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads, s
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kernel, P(args)...) != cudaSuccess) return W4_ERR_CUDA;
+    return launch_status();
+}
+
+// behind: the kernel before it on the stream is this call's own, so it may start while that one is
+// finishing. Else whatever came before is complete when it starts, and with that the weights that the
+// product behind it reads before it has waited for this kernel.
+inline w4_status launch_prep(const Prep &p, bool behind, cudaStream_t stream) {
+    const unsigned grid = (unsigned)(p.M < (1 << 20) ? p.M : (1 << 20));
+    if (behind)
+        return p.x8 ? launch_behind(row_prep_kernel<true>, grid, 256, 0, stream, p)
+                    : launch_behind(row_prep_kernel<false>, grid, 256, 0, stream, p);
+    if (p.x8)
+        row_prep_kernel<true><<<grid, 256, 0, stream>>>(p);
+    else
+        row_prep_kernel<false><<<grid, 256, 0, stream>>>(p);
     return launch_status();
 }
 

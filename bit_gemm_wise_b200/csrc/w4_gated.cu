@@ -583,7 +583,7 @@ W4_API w4_status w4a16_gated(const void *X_bf16, int64_t M, const uint8_t *codes
     prep.K = K;
     prep.tensors = 1;
     prep.pairs = 1;
-    st = xg::launch_prep(prep, stream);
+    st = xg::launch_prep(prep, false, stream);
     if (st != W4_OK) return st;
     xg::Args a = {};
     a.row_pow = prep.row_pow;
@@ -654,7 +654,7 @@ W4_API w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const 
     prep.K = K;
     prep.tensors = 1;
     prep.pairs = 1;
-    st = xg::launch_prep(prep, stream);
+    st = xg::launch_prep(prep, false, stream);
     if (st != W4_OK) return st;
     xg::Maps tm;
     xg::Args a = {};
@@ -680,7 +680,7 @@ W4_API w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const 
     prep.K = H;
     prep.tensors = 2;
     prep.pairs = 0;
-    st = xg::launch_prep(prep, stream);
+    st = xg::launch_prep(prep, true, stream);
     if (st != W4_OK) return st;
     if (!xg::make_map(&tm.b[0], prep.y[0], M, H, l.dx.NT) || !xg::make_map(&tm.b[1], prep.y[1], M, H, l.dx.NT))
         return W4_ERR_CUDA;
@@ -720,7 +720,7 @@ W4_API w4_status w4a16_dgrad(const void *dY_bf16, int64_t M, const uint8_t *code
     prep.M = M;
     prep.K = N;
     prep.tensors = 1;
-    st = xg::launch_prep(prep, stream);
+    st = xg::launch_prep(prep, false, stream);
     if (st != W4_OK) return st;
     xg::Args a = {};
     a.row_pow = prep.row_pow;
