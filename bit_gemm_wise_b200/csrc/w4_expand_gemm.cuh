@@ -14,16 +14,15 @@
 // (MN-major, which the MMA reads as it stands), so the expansion writes the same bytes either way:
 // 16-byte chunks of eight k, at the place that the 128-byte swizzle gives them.
 //
-// One persistent CTA per SM takes units (tile, part of the reduction), stages of 64 along it:
-//   warps 0-15   expand A, in four groups that take the stages in turn (a wait costs a warp some
-//                200 cycles even when it is over, so a group alone cannot keep up). A thread takes
-//                two chunks of 32 consecutive values (half of a row's 64 columns, or a quarter of a
-//                row of 128), so that a chunk has a single group scale, which it loads itself a turn
-//                ahead;
-//   warps 16-19  read the fp32 accumulators (two buffers in TMEM, so that a tile's results leave while
+// One persistent CTA per SM takes units (tile, part of the reduction), stages of 64 along it. Its warps:
+//   0-15 or 0-7  expand A, in four groups that take the stages in turn, so that one group's waits and
+//                fences overlap the others' arithmetic. A thread takes two or four chunks of 32
+//                consecutive values (half of a row's 64 columns, or a quarter of a row of 128), so that
+//                a chunk has a single group scale, which it loads itself a turn ahead;
+//   then 4 or 8  read the fp32 accumulators (two buffers in TMEM, so that a tile's results leave while
 //                the next one is multiplied) and finish them;
-//   warp 20      loads B by TMA; warp 21 issues the MMAs (M = 128, N = the token tile, K = 16);
-//   warp 22      loads the codes by TMA, into a ring of their own.
+//   one each     loads B by TMA; issues the MMAs (M = 128, N = the token tile, K = 16); loads the codes
+//                by TMA, into a ring of their own.
 // Lanes are weights and columns are tokens: a small batch takes a small N and the MMAs shrink with
 // it, while the expansion is shared by all tokens of a tile. What bounds a stage is the instructions
 // that the SM issues for it (about 1900 at first: 1.0 us a stage, twice its MMAs): the codes' pairs
@@ -46,13 +45,25 @@ namespace xg {
 
 enum Kind { FWD = 0, DGRAD = 1, WGRAD = 2 };
 
-constexpr int EXPAND_WARPS = 16;
 constexpr int GROUPS = 4;                     // of expansion warps; stage i is group i % GROUPS's
-constexpr int WPG = EXPAND_WARPS / GROUPS;    // warps per group
-constexpr int TPG = WPG * 32;                 // threads per group: two chunks of 32 values each
-constexpr int OUT_WARPS = 4;                  // one for each quarter of the lanes
-constexpr int W_OUT = EXPAND_WARPS, W_B = W_OUT + OUT_WARPS, W_MMA = W_B + 1, W_Q = W_B + 2;
-constexpr int THREADS = (W_Q + 1) * 32;
+
+// How a CTA's warps are divided. Sixteen expansion warps and four for the results leave a thread 80
+// registers; where the results take long (two gradients and dH for each pair of accumulators; tiles of
+// few stages), eight and eight do better. Measured with the two ways in turn, us: prefill 4096 x 15360 x
+// 3840 822 and 853, dgrad 4096 x 4096 x 14336 407 and 429; the gradients of 2048 x 14336 x 4096 with
+// their dX 1126 and 1065, wgrad 2048 x 4096 x 4096 91 and 87.
+template <bool LONG_RESULTS> struct Roles {
+    static constexpr int EXPAND = LONG_RESULTS ? 8 : 16, OUT = LONG_RESULTS ? 8 : 4;
+    static constexpr int WPG = EXPAND / GROUPS;     // expansion warps per group
+    static constexpr int TPG = WPG * 32;            // threads per group
+    static constexpr int CPT = 256 / TPG;           // chunks of 32 values each, per thread and stage
+    static constexpr int W_OUT = EXPAND, W_B = W_OUT + OUT, W_MMA = W_B + 1, W_Q = W_B + 2;
+    static constexpr int THREADS = (W_Q + 1) * 32;
+    static constexpr int RANKS = W_B / 4, HELPERS = EXPAND / 4;  // warps of a quarter of the lanes; of them, expansion
+    static_assert(EXPAND % 4 == 0 && OUT % 4 == 0 && TPG >= 64 && TPG <= 128, "warp roles");
+};
+template <int KIND, bool GRADS> using RolesOf = Roles<KIND == 2 || GRADS>;
+
 constexpr int BK = 64;                        // reduction per stage
 constexpr uint32_t A_BYTES = 128 * BK * 2;    // an expanded stage
 constexpr int MAX_STAGES = 8;
@@ -70,8 +81,8 @@ struct Smem {
     uint64_t acce[2];             // its columns were read (one arrival per warp)
     uint32_t tmem_base;
     int abort;
-    uint32_t arrived[OUT_WARPS];  // parts of the tile's lanes that came before
-    alignas(16) float row_pow[OUT_WARPS][256];  // of the current tile's tokens, a copy for each quarter
+    uint32_t arrived[4];  // parts of the tile's lanes that came before
+    alignas(16) float row_pow[4][256];  // of the current tile's tokens, a copy for each quarter
 };
 constexpr uint32_t CONTROL = 5 * 1024;
 static_assert(sizeof(Smem) <= CONTROL, "control block");
@@ -80,7 +91,7 @@ static_assert(sizeof(Smem) <= CONTROL, "control block");
 template <int KIND> struct Raw {
     static constexpr uint32_t BYTES = KIND == WGRAD ? 8192 : 4096;
 };
-static_assert(TPG == 128 && MIN_STAGES >= GROUPS, "warp roles");
+static_assert(MIN_STAGES >= GROUPS, "every group has a stage");
 static_assert(MIN_STAGES * (A_BYTES + 256 * 128 + Raw<FWD>::BYTES) <= SMEM_MAX - CONTROL - 1024 &&
                   MIN_STAGES * (A_BYTES + 192 * 128 + Raw<WGRAD>::BYTES) <= SMEM_MAX - CONTROL - 1024,
               "four stages of each ring");
@@ -361,34 +372,40 @@ struct Walk {
     }
 };
 
-// The scales of the two chunks that a thread expands in a stage. fetch() only issues loads, from
+// The scales of the chunks that a thread expands in a stage. fetch() only issues loads, from
 // addresses that always exist, and nothing waits for them before word(): no branch and no arithmetic
 // on a loaded value may stand between the two, or each stage costs a memory latency.
-template <int KIND> struct Scales {
-    uint16_t s[2], z[2];      // fp16 scales and zero points; WGRAD: scale bytes in s
-    bool there[2];            // FWD: the row, the columns; else each chunk
-    const uint16_t *ps[2], *pz[2];  // FWD: of the tile's rows (for symmetric weights pz is ps)
-    uint32_t tile = ~0u;            // FWD: whose rows they are
+template <int KIND, int TPG> struct Scales {
+    static constexpr int CPT = 256 / TPG;
+    uint16_t s[CPT], z[CPT];  // fp16 scales and zero points; WGRAD: scale bytes in s
+    uint32_t there;           // bit j: chunk j exists
+    const uint16_t *ps[2], *pz[2];  // FWD: of the tile's first row (for symmetric weights pz is ps)
+    uint32_t tile = ~0u, rows;      // FWD: whose row it is, and which of the thread's rows exist
 
     __device__ __forceinline__ void fetch(const Args &a, const Walk &w, int tt) {
-        const int K = (int)a.K, rows = (int)a.rows;  // at most 2^24
+        const int K = (int)a.K, n = (int)a.rows;  // at most 2^24
+        there = 0u;
         if (KIND == WGRAD) {
             const int m = w.kb * BK + (tt >> 2), k = (int)w.un.tw * 128 + 32 * (tt & 3);
             const int64_t at = (int64_t)m * (K >> 5) + (k >> 5);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                there[j] = k < K && m + 32 * j < rows;
-                s[j] = __ldg(a.xs + (there[j] ? at + j * K : 0));  // 32 rows of K / 32 further
+            for (int j = 0; j < CPT; ++j) {
+                const bool ok = k < K && m + TPG / 4 * j < n;
+                there |= ok ? 1u << j : 0u;
+                s[j] = __ldg(a.xs + (ok ? at + (int64_t)(TPG / 4 * j) * (K >> 5) : 0));
             }
             return;
         }
         const int J = K >> a.gshift;
         if (KIND == FWD) {
+            // raw rows TPG / 2 apart: those of the gate, then those of up
             if (w.un.tw != tile) {
                 tile = w.un.tw;
                 const int row = (int)tile * 64 + (tt >> 1);
-                there[0] = row < rows;
-                const int64_t at = there[0] ? (int64_t)row * J : 0;
+                rows = 0u;
+#pragma unroll
+                for (int j = 0; j < CPT; ++j) rows |= row + (TPG / 2 * j & 63) < n ? 1u << j : 0u;
+                const int64_t at = row < n ? (int64_t)row * J : 0;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     ps[j] = a.w[j].scales + at;
@@ -396,12 +413,13 @@ template <int KIND> struct Scales {
                 }
             }
             const int k = w.kb * BK + 32 * (tt & 1);
-            there[1] = k < K;
-            const int i = there[1] ? k >> a.gshift : 0;
+            there = k < K ? rows : 0u;
+            const int i = k < K ? k >> a.gshift : 0;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                s[j] = __ldg(ps[j] + i);
-                z[j] = __ldg(pz[j] + i);
+            for (int j = 0; j < CPT; ++j) {
+                const int d = TPG / 2 * j, x = (d & 63) && ((rows >> j) & 1u) ? i + (d & 63) * J : i;
+                s[j] = __ldg(ps[d >> 6] + x);
+                z[j] = __ldg(pz[d >> 6] + x);
             }
             return;
         }
@@ -409,20 +427,23 @@ template <int KIND> struct Scales {
         const int row = (w.kb - (src ? a.KB0 : 0)) * BK + (tt >> 2), k = (int)w.un.tw * 128 + 32 * (tt & 3);
         const int64_t at = (int64_t)row * J + (k >> a.gshift);
         const Weight &m = a.w[src];
+        // symmetric weights: the scale again, for the sake of one instruction stream
+        const uint16_t *mz = a.asym ? reinterpret_cast<const uint16_t *>(m.zeros) : m.scales;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            there[j] = k < K && row + 32 * j < rows;
-            const int64_t i = there[j] ? at + 32 * j * J : 0;
+        for (int j = 0; j < CPT; ++j) {
+            const bool ok = k < K && row + TPG / 4 * j < n;
+            there |= ok ? 1u << j : 0u;
+            const int64_t i = ok ? at + (int64_t)(TPG / 4 * j) * J : 0;
             s[j] = __ldg(m.scales + i);
-            // symmetric weights: the scale again, for the sake of one instruction stream
-            z[j] = __ldg((a.asym ? reinterpret_cast<const uint16_t *>(m.zeros) : m.scales) + i);
+            z[j] = __ldg(mz + i);
         }
     }
     // fp16 scale with the zero point above it, or the scale byte; a chunk that does not exist has
     // scale 0 (its codes read as zero)
     __device__ __forceinline__ uint32_t word(const Args &a, int j) const {
-        if (KIND == WGRAD) return there[j] ? (uint32_t)s[j] : 127u;
-        return (KIND == FWD ? there[0] && there[1] : there[j]) ? (uint32_t)s[j] | ((a.asym ? (uint32_t)z[j] : 8u) << 16) : 8u << 16;
+        const bool ok = (there >> j) & 1u;
+        if (KIND == WGRAD) return ok ? (uint32_t)s[j] : 127u;
+        return ok ? (uint32_t)s[j] | ((a.asym ? (uint32_t)z[j] : 8u) << 16) : 8u << 16;
     }
 };
 
@@ -430,9 +451,8 @@ template <int KIND> struct Scales {
 // c % 2; else row c / 4, columns 32 (c % 4). In FWD the rows go to the lanes 16 of the gate, 16 of
 // up, 16 of the gate, ..., so that a warp of the results has both of a feature. Its codes are at
 // c * 16 (WGRAD: c * 32) of the stage's codes.
-// A thread's place in that: chunks tt and tt + 128, whose rows in the A tile are 16 (FWD) or 32 apart.
-template <int KIND> struct Place {
-    static constexpr uint32_t NEXT = KIND == FWD ? 16 * 128 : 32 * 128;
+// A thread's place in that: chunks tt, tt + TPG, ...
+template <int KIND, int TPG> struct Place {
     uint32_t codes;           // of the first chunk, from the start of the stage's codes
     uint32_t swap;            // DGRAD, WGRAD: which half of the codes comes first
     uint32_t out[4];          // of its four 16-byte pieces, from the start of the A tile
@@ -448,62 +468,65 @@ template <int KIND> struct Place {
         codes = (uint32_t)tt * (KIND == WGRAD ? 32u : 16u);
         swap = flip ? (KIND == WGRAD ? 16u : 8u) : 0u;
     }
+    // from the first chunk's row of the A tile to chunk j's, in bytes (FWD: the up rows are 16 lanes
+    // behind their features' gate rows); whole groups of eight rows
+    static __device__ __forceinline__ constexpr uint32_t next(int j) {
+        return KIND == FWD ? (TPG / 2 * j & 63) * 2 * 128 + (TPG / 2 * j >> 6) * 16 * 128 : j * (TPG / 4) * 128;
+    }
 };
 
-template <int KIND>
-__device__ __forceinline__ void expand_store(uint32_t raw, uint32_t base, const Place<KIND> &p, uint32_t s0, uint32_t s1) {
-    const uint32_t sz[2] = {s0, s1};
+// chunk j of a thread; ANY: with any scale and zero point
+template <int KIND, int TPG, bool ANY>
+__device__ __forceinline__ void expand_chunk(uint32_t raw, uint32_t base, const Place<KIND, TPG> &p, int j, uint32_t sz) {
+    uint32_t q[KIND == WGRAD ? 8 : 4];
+    const uint32_t at = raw + p.codes + (uint32_t)(TPG * j) * (KIND == WGRAD ? 32u : 16u);
+    if (KIND == FWD) {
+        const uint4 v = lds128(at);
+        q[0] = v.x; q[1] = v.y; q[2] = v.z; q[3] = v.w;
+    } else if (KIND == DGRAD) {
+        const uint2 v = lds64(at + p.swap), u = lds64(at + (p.swap ^ 8u));
+        q[0] = v.x; q[1] = v.y; q[2] = u.x; q[3] = u.y;
+    } else {
+        const uint4 v = lds128(at + p.swap), u = lds128(at + (p.swap ^ 16u));
+        q[0] = v.x; q[1] = v.y; q[2] = v.z; q[3] = v.w;
+        q[KIND == WGRAD ? 4 : 0] = u.x; q[KIND == WGRAD ? 5 : 1] = u.y;
+        q[KIND == WGRAD ? 6 : 2] = u.z; q[KIND == WGRAD ? 7 : 3] = u.w;
+    }
+    const uint2 k = KIND == WGRAD ? make_uint2(pow2_one(sz), 0u) : near_words(sz);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t o[4];
+        if (KIND == WGRAD) {
+            if (ANY) {
+                expand4_any(q[KIND == WGRAD ? 2 * i : 0], sz, o[0], o[1]);
+                expand4_any(q[KIND == WGRAD ? 2 * i + 1 : 0], sz, o[2], o[3]);
+            } else {
+                expand4(q[KIND == WGRAD ? 2 * i : 0], k.x, o[0], o[1]);
+                expand4(q[KIND == WGRAD ? 2 * i + 1 : 0], k.x, o[2], o[3]);
+            }
+        } else if (ANY) {
+            expand8_any(q[i], sz, o);
+        } else {
+            expand8(q[i], k.x, k.y, o);
+        }
+        sts128(base + p.out[i] + Place<KIND, TPG>::next(j), o[0], o[1], o[2], o[3]);
+    }
+}
+template <int KIND, int TPG>
+__device__ __forceinline__ void expand_store(uint32_t raw, uint32_t base, const Place<KIND, TPG> &p,
+                                             const uint32_t (&sz)[256 / TPG]) {
+    constexpr int CPT = 256 / TPG;
     // One branch for the whole warp: scales outside the usual range are rare, and their arithmetic
     // beside the other in one instruction stream cost a third of the expansion's rate.
-    const bool any = __any_sync(FULL, KIND == WGRAD ? s0 > 134u || s1 > 134u : !is_near(s0) || !is_near(s1));
-    uint32_t q[2][KIND == WGRAD ? 8 : 4];
+    bool any = false;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const uint32_t at = raw + p.codes + (KIND == WGRAD ? 128u * 32u : 128u * 16u) * j;
-        if (KIND == FWD) {
-            const uint4 v = lds128(at);
-            q[j][0] = v.x; q[j][1] = v.y; q[j][2] = v.z; q[j][3] = v.w;
-        } else if (KIND == DGRAD) {
-            const uint2 v = lds64(at + p.swap), u = lds64(at + (p.swap ^ 8u));
-            q[j][0] = v.x; q[j][1] = v.y; q[j][2] = u.x; q[j][3] = u.y;
-        } else {
-            const uint4 v = lds128(at + p.swap), u = lds128(at + (p.swap ^ 16u));
-            q[j][0] = v.x; q[j][1] = v.y; q[j][2] = v.z; q[j][3] = v.w;
-            q[j][KIND == WGRAD ? 4 : 0] = u.x; q[j][KIND == WGRAD ? 5 : 1] = u.y;
-            q[j][KIND == WGRAD ? 6 : 2] = u.z; q[j][KIND == WGRAD ? 7 : 3] = u.w;
-        }
-    }
-    if (!any) {
+    for (int j = 0; j < CPT; ++j) any = any || (KIND == WGRAD ? sz[j] > 134u : !is_near(sz[j]));
+    if (!__any_sync(FULL, any)) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint2 k = KIND == WGRAD ? make_uint2(pow2_one(sz[j]), 0u) : near_words(sz[j]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t o[4];
-                if (KIND == WGRAD) {
-                    expand4(q[j][KIND == WGRAD ? 2 * i : 0], k.x, o[0], o[1]);
-                    expand4(q[j][KIND == WGRAD ? 2 * i + 1 : 0], k.x, o[2], o[3]);
-                } else {
-                    expand8(q[j][i], k.x, k.y, o);
-                }
-                sts128(base + p.out[i] + Place<KIND>::NEXT * j, o[0], o[1], o[2], o[3]);
-            }
-        }
+        for (int j = 0; j < CPT; ++j) expand_chunk<KIND, TPG, false>(raw, base, p, j, sz[j]);
     } else {
-        // rare, and kept small
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t o[4];
-                if (KIND == WGRAD) {
-                    expand4_any(q[j][KIND == WGRAD ? 2 * i : 0], sz[j], o[0], o[1]);
-                    expand4_any(q[j][KIND == WGRAD ? 2 * i + 1 : 0], sz[j], o[2], o[3]);
-                } else {
-                    expand8_any(q[j][i], sz[j], o);
-                }
-                sts128(base + p.out[i] + Place<KIND>::NEXT * j, o[0], o[1], o[2], o[3]);
-            }
+        for (int j = 0; j < CPT; ++j) expand_chunk<KIND, TPG, true>(raw, base, p, j, sz[j]);
     }
 }
 // The place of value i of eight (FWD, DGRAD) or of four (WGRAD) in what expand8 and expand4 write
@@ -583,8 +606,9 @@ __device__ __forceinline__ void emit(const Args &a, const float *row_pow, const 
 }
 
 template <int KIND, bool GRADS, bool GELU>
-__global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_constant__ Maps tm,
-                                                                 const __grid_constant__ Args a) {
+__global__ void __launch_bounds__((RolesOf<KIND, GRADS>::THREADS), 1) expand_gemm_kernel(const __grid_constant__ Maps tm,
+                                                                                       const __grid_constant__ Args a) {
+    using R = RolesOf<KIND, GRADS>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *raw = base + (size_t)a.stages * a.stage_bytes;
@@ -595,29 +619,29 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
     // the expansion's first scales, on their way while the CTA sets up
     Walk w;
     bool more = false;
-    Scales<KIND> next;
-    if (warp < EXPAND_WARPS) {
+    Scales<KIND, R::TPG> next;
+    if (warp < R::EXPAND) {
         w.start(a);
-        more = w.skip(a, warp / WPG);
-        if (more) next.fetch(a, w, threadIdx.x % TPG);
+        more = w.skip(a, warp / R::WPG);
+        if (more) next.fetch(a, w, threadIdx.x % R::TPG);
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
-            mbar_init(&sm->full[s], 1 + WPG);
+            mbar_init(&sm->full[s], 1 + R::WPG);
             mbar_init(&sm->empty[s], 1);
         }
         for (int s = 0; s < NR; ++s) {
             mbar_init(&sm->rawf[s], 1);
-            mbar_init(&sm->rawe[s], WPG);
+            mbar_init(&sm->rawe[s], R::WPG);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sm->accf[b], 1);
-            mbar_init(&sm->acce[b], OUT_WARPS);
+            mbar_init(&sm->acce[b], R::OUT);
         }
         sm->abort = 0;
         fence_mbar_init();
     }
-    if (warp == W_MMA) {
+    if (warp == R::W_MMA) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sm->tmem_base)),
                      "r"(512u)
                      : "memory");
@@ -628,20 +652,22 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
     tc_fence_after();
     const uint32_t tmem = sm->tmem_base;
 
-    if (warp < EXPAND_WARPS) {
+    if (warp < R::EXPAND) {
         // ------------------------------------------------ expansion of A
-        const int grp = warp / WPG, tt = threadIdx.x % TPG;
-        const Place<KIND> place(tt);
+        const int grp = warp / R::WPG, tt = threadIdx.x % R::TPG;
+        const Place<KIND, R::TPG> place(tt);
         int slot = grp, rs = grp;
         uint32_t phase = 0, rphase = 0;
         while (more) {
-            const uint32_t s0 = next.word(a, 0), s1 = next.word(a, 1);
+            uint32_t sz[R::CPT];
+#pragma unroll
+            for (int j = 0; j < R::CPT; ++j) sz[j] = next.word(a, j);
             more = w.skip(a, GROUPS);
             if (more) next.fetch(a, w, tt);
             if (!warp_wait(&sm->rawf[rs], rphase, sm, a.status)) break;
             if (!warp_wait(&sm->empty[slot], phase ^ 1u, sm, a.status)) break;
-            expand_store<KIND>(smem_addr(raw + (size_t)rs * Raw<KIND>::BYTES), smem_addr(base + (size_t)slot * a.stage_bytes),
-                               place, s0, s1);
+            expand_store<KIND, R::TPG>(smem_addr(raw + (size_t)rs * Raw<KIND>::BYTES), smem_addr(base + (size_t)slot * a.stage_bytes),
+                               place, sz);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMA reads them
             __syncwarp();
             if (lane == 0) {
@@ -653,7 +679,7 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
             rs += GROUPS;
             if (rs >= NR) { rs -= NR; rphase ^= 1u; }
         }
-    } else if (warp == W_B) {
+    } else if (warp == R::W_B) {
         // ------------------------------------------------ B by TMA
         if (KIND != WGRAD) asm volatile("griddepcontrol.wait;" ::: "memory");  // B is row_prep_kernel's
         if (elect_one()) {
@@ -685,7 +711,7 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
                 (void)mbar_wait_bounded(&sm->full[i % NS], (uint32_t)(i / NS) & 1u, a.status);
         }
         __syncwarp();
-    } else if (warp == W_Q) {
+    } else if (warp == R::W_Q) {
         // ------------------------------------------------ codes by TMA
         if (elect_one()) {
             int rs = 0, issued = 0;
@@ -715,7 +741,7 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
                 (void)mbar_wait_bounded(&sm->rawf[i % NR], (uint32_t)(i / NR) & 1u, a.status);
         }
         __syncwarp();
-    } else if (warp == W_MMA) {
+    } else if (warp == R::W_MMA) {
         // ------------------------------------------------ MMA issue
         // D fp32, A and B fp16 (0) or bf16 (1), M = 128, N = NT; A (and B in WGRAD) contiguous
         // along M (N)
@@ -760,14 +786,15 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
         __syncwarp();
     }
 
-    if (warp < W_B) {
+    if (warp < R::W_B) {
         // ------------------------------------------------ results (lane 32 q4 + lane of the tile), 16
-        // columns at a time. The CTA's last tile has nothing behind it to overlap with: there the
-        // expansion warps, whose work is done, share the columns (ranks 0-3, the result warps are
-        // rank 4). Where a tile is summed up in several accumulators, they do not.
+        // columns at a time, in turn by the warps of a quarter: the two result warps; and, in the CTA's
+        // last tile, which has nothing behind it to overlap with, the expansion warps too, whose work is
+        // done. Where a tile is summed up in several accumulators, they do not.
+        constexpr int RANKS = R::RANKS, HELPERS = R::HELPERS;
         const int q4 = warp & 3, r = q4 * 32 + lane, rank = warp >> 2;
         const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
-        const bool helper = warp < EXPAND_WARPS, shared = a.seg >= a.KB;
+        const bool helper = warp < R::EXPAND, shared = a.seg >= a.KB;
         const uint32_t before = ((uint32_t)a.units - 1u - blockIdx.x) / gridDim.x;  // this CTA's units but the last
         float *row_pow = sm->row_pow[q4];
         if (KIND != WGRAD) asm volatile("griddepcontrol.wait;" ::: "memory");  // row_pow too
@@ -775,24 +802,23 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
         if (helper && !shared) u = (uint32_t)a.units;
         int n = helper ? (int)before : 0;
         bool ok = true;
-        // A wait that ran out ends this warp's work, but not its way to the last tile: the ranks of
-        // a quarter meet there at barriers that have no time limit of their own.
+        // A wait that ran out ends this warp's work, but not its way through the tiles: the warps of a
+        // quarter meet at barriers that have no time limit of their own.
         for (; u < (uint32_t)a.units; u += gridDim.x) {
             const bool last = shared && (uint32_t)a.units - u <= gridDim.x;
-            if (!ok && !last) continue;
             const Unit un = unit_of(a, u);
             const int64_t left = a.cols - (int64_t)un.tn * a.NT;
             const int ncols = left < a.NT ? (int)left : a.NT;
-            const int c0 = last ? 16 * rank : 0, cstep = last ? 16 * (W_B / 4) : 16;
+            const int c0 = 16 * (last ? rank : rank - HELPERS), cstep = 16 * (last ? RANKS : RANKS - HELPERS);
+            // the warps of this quarter that take part meet at a barrier of their own
+            auto meet = [&] { named_bar_sync(last ? 1 + q4 : 5 + q4, 32 * (last ? RANKS : RANKS - HELPERS)); };
             // partial sums: [column / 4][lane][4 columns]
             float4 *part = reinterpret_cast<float4 *>(a.part) + ((size_t)un.tile * a.S + un.s) * (a.NT * 32) + r;
             if (KIND != WGRAD) {
-                if (last) named_bar_sync(1 + q4, W_B / 4 * 32);  // readers of the previous tile's
-                __syncwarp();
-                if (!helper)
+                meet();  // readers of the previous tile's
+                if (rank == HELPERS)
                     for (int c = lane; c < ncols; c += 32) row_pow[c] = a.row_pow[(int64_t)un.tn * a.NT + c];
-                if (last) named_bar_sync(1 + q4, W_B / 4 * 32);
-                __syncwarp();
+                meet();
             }
             Incoming ahead;  // dH of the next columns, on its way while the present ones are finished
             if (GRADS) ahead.fetch(a, un, q4, lane, c0, ncols - c0);
@@ -831,13 +857,11 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
             }
             if (a.S == 1) continue;
             // the last part of a tile's 32 lanes to arrive adds all parts in order
-            uint32_t *cnt = a.cnt + (size_t)un.tile * OUT_WARPS + q4;
+            uint32_t *cnt = a.cnt + (size_t)un.tile * 4 + q4;
             __threadfence();
-            if (last) named_bar_sync(1 + q4, W_B / 4 * 32);
-            __syncwarp();
-            if (!helper && lane == 0) sm->arrived[q4] = atomicAdd(cnt, 1u);
-            if (last) named_bar_sync(1 + q4, W_B / 4 * 32);
-            __syncwarp();
+            meet();
+            if (rank == HELPERS && lane == 0) sm->arrived[q4] = atomicAdd(cnt, 1u);
+            meet();
             if (sm->arrived[q4] != (uint32_t)(a.S - 1) || !ok) continue;
             __threadfence();
             const float4 *p0 = reinterpret_cast<const float4 *>(a.part) + (size_t)un.tile * a.S * (a.NT * 32) + r;
@@ -874,14 +898,14 @@ __global__ void __launch_bounds__(THREADS, 1) expand_gemm_kernel(const __grid_co
                 if (GRADS) ahead.fetch(a, un, q4, lane, c + cstep, ncols - c - cstep);
                 emit<KIND, GRADS, GELU>(a, row_pow, un, q4, lane, c, ncols - c, v, now, false);
             }
-            if (!helper && lane == 0) *cnt = 0u;  // ready for the next call
+            if (rank == HELPERS && lane == 0) *cnt = 0u;  // ready for the next call
         }
     }
 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == W_MMA)
+    if (warp == R::W_MMA)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
@@ -998,7 +1022,7 @@ struct Plan {
 // The workspace starts with the arrival counters, in a region of one size for all shapes (what
 // one call leaves as partial sums is never another's counter), then holds the partial sums.
 constexpr int64_t MAX_SPLIT_TILES = 4096;
-constexpr size_t CNT_BYTES = MAX_SPLIT_TILES * OUT_WARPS * sizeof(uint32_t);
+constexpr size_t CNT_BYTES = MAX_SPLIT_TILES * 4 * sizeof(uint32_t);
 
 // lanes: weight rows per projection (FWD) or columns K; cols: the other side; red: length of the
 // reduction (per source), sources 1 or 2; max_rows: reduction that one accumulator may sum.
@@ -1171,8 +1195,8 @@ w4_status launch(const Plan &p, Maps &tm, Args a, void *workspace, int sms, cuda
     // FWD and DGRAD follow row_prep_kernel: they may start, and read weights, while it finishes.
     // Whatever came before on the stream was complete when it began.
     if (KIND != WGRAD)
-        return launch_behind(expand_gemm_kernel<KIND, GRADS, GELU>, grid, THREADS, (size_t)smem, stream, tm, a);
-    expand_gemm_kernel<KIND, GRADS, GELU><<<grid, THREADS, smem, stream>>>(tm, a);
+        return launch_behind(expand_gemm_kernel<KIND, GRADS, GELU>, grid, RolesOf<KIND, GRADS>::THREADS, (size_t)smem, stream, tm, a);
+    expand_gemm_kernel<KIND, GRADS, GELU><<<grid, RolesOf<KIND, GRADS>::THREADS, smem, stream>>>(tm, a);
     return launch_status();
 }
 
