@@ -475,39 +475,45 @@ template <int KIND, int TPG> struct Place {
     }
 };
 
-// chunk j of a thread; ANY: with any scale and zero point
-template <int KIND, int TPG, bool ANY>
-__device__ __forceinline__ void expand_chunk(uint32_t raw, uint32_t base, const Place<KIND, TPG> &p, int j, uint32_t sz) {
+template <int KIND> struct Values {
     uint32_t q[KIND == WGRAD ? 8 : 4];
+};
+// the codes of chunk j of a thread, in the order in which it expands them
+template <int KIND, int TPG>
+__device__ __forceinline__ void chunk_load(Values<KIND> &c, uint32_t raw, const Place<KIND, TPG> &p, int j) {
     const uint32_t at = raw + p.codes + (uint32_t)(TPG * j) * (KIND == WGRAD ? 32u : 16u);
     if (KIND == FWD) {
         const uint4 v = lds128(at);
-        q[0] = v.x; q[1] = v.y; q[2] = v.z; q[3] = v.w;
+        c.q[0] = v.x; c.q[1] = v.y; c.q[2] = v.z; c.q[3] = v.w;
     } else if (KIND == DGRAD) {
         const uint2 v = lds64(at + p.swap), u = lds64(at + (p.swap ^ 8u));
-        q[0] = v.x; q[1] = v.y; q[2] = u.x; q[3] = u.y;
+        c.q[0] = v.x; c.q[1] = v.y; c.q[2] = u.x; c.q[3] = u.y;
     } else {
         const uint4 v = lds128(at + p.swap), u = lds128(at + (p.swap ^ 16u));
-        q[0] = v.x; q[1] = v.y; q[2] = v.z; q[3] = v.w;
-        q[KIND == WGRAD ? 4 : 0] = u.x; q[KIND == WGRAD ? 5 : 1] = u.y;
-        q[KIND == WGRAD ? 6 : 2] = u.z; q[KIND == WGRAD ? 7 : 3] = u.w;
+        c.q[0] = v.x; c.q[1] = v.y; c.q[2] = v.z; c.q[3] = v.w;
+        c.q[KIND == WGRAD ? 4 : 0] = u.x; c.q[KIND == WGRAD ? 5 : 1] = u.y;
+        c.q[KIND == WGRAD ? 6 : 2] = u.z; c.q[KIND == WGRAD ? 7 : 3] = u.w;
     }
+}
+// their values into the A tile; ANY: with any scale and zero point
+template <int KIND, int TPG, bool ANY>
+__device__ __forceinline__ void chunk_store(const Values<KIND> &c, uint32_t base, const Place<KIND, TPG> &p, int j, uint32_t sz) {
     const uint2 k = KIND == WGRAD ? make_uint2(pow2_one(sz), 0u) : near_words(sz);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint32_t o[4];
         if (KIND == WGRAD) {
             if (ANY) {
-                expand4_any(q[KIND == WGRAD ? 2 * i : 0], sz, o[0], o[1]);
-                expand4_any(q[KIND == WGRAD ? 2 * i + 1 : 0], sz, o[2], o[3]);
+                expand4_any(c.q[KIND == WGRAD ? 2 * i : 0], sz, o[0], o[1]);
+                expand4_any(c.q[KIND == WGRAD ? 2 * i + 1 : 0], sz, o[2], o[3]);
             } else {
-                expand4(q[KIND == WGRAD ? 2 * i : 0], k.x, o[0], o[1]);
-                expand4(q[KIND == WGRAD ? 2 * i + 1 : 0], k.x, o[2], o[3]);
+                expand4(c.q[KIND == WGRAD ? 2 * i : 0], k.x, o[0], o[1]);
+                expand4(c.q[KIND == WGRAD ? 2 * i + 1 : 0], k.x, o[2], o[3]);
             }
         } else if (ANY) {
-            expand8_any(q[i], sz, o);
+            expand8_any(c.q[i], sz, o);
         } else {
-            expand8(q[i], k.x, k.y, o);
+            expand8(c.q[i], k.x, k.y, o);
         }
         sts128(base + p.out[i] + Place<KIND, TPG>::next(j), o[0], o[1], o[2], o[3]);
     }
@@ -521,12 +527,19 @@ __device__ __forceinline__ void expand_store(uint32_t raw, uint32_t base, const 
     bool any = false;
 #pragma unroll
     for (int j = 0; j < CPT; ++j) any = any || (KIND == WGRAD ? sz[j] > 134u : !is_near(sz[j]));
-    if (!__any_sync(FULL, any)) {
+    any = __any_sync(FULL, any);
 #pragma unroll
-        for (int j = 0; j < CPT; ++j) expand_chunk<KIND, TPG, false>(raw, base, p, j, sz[j]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < CPT; ++j) expand_chunk<KIND, TPG, true>(raw, base, p, j, sz[j]);
+    for (int j = 0; j < CPT; j += 2) {
+        Values<KIND> c[2];  // two chunks' loads in flight
+        chunk_load<KIND, TPG>(c[0], raw, p, j);
+        chunk_load<KIND, TPG>(c[1], raw, p, j + 1);
+        if (!any) {
+            chunk_store<KIND, TPG, false>(c[0], base, p, j, sz[j]);
+            chunk_store<KIND, TPG, false>(c[1], base, p, j + 1, sz[j + 1]);
+        } else {
+            chunk_store<KIND, TPG, true>(c[0], base, p, j, sz[j]);
+            chunk_store<KIND, TPG, true>(c[1], base, p, j + 1, sz[j + 1]);
+        }
     }
 }
 // The place of value i of eight (FWD, DGRAD) or of four (WGRAD) in what expand8 and expand4 write
