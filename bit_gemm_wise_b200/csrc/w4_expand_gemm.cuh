@@ -827,8 +827,11 @@ __global__ void __launch_bounds__((RolesOf<KIND, GRADS>::THREADS), 1) expand_gem
             auto meet = [&] { named_bar_sync(last ? 1 + q4 : 5 + q4, 32 * (last ? RANKS : RANKS - HELPERS)); };
             // partial sums: [column / 4][lane][4 columns]
             float4 *part = reinterpret_cast<float4 *>(a.part) + ((size_t)un.tile * a.S + un.s) * (a.NT * 32) + r;
+            // Also what keeps the helpers from the last tile's accumulator until the result warps have
+            // finished the tile before it: a helper sees only the parity of that accumulator's phase, which
+            // two tiles back had the same.
+            if (KIND != WGRAD || last) meet();  // and the readers of the previous tile's powers
             if (KIND != WGRAD) {
-                meet();  // readers of the previous tile's
                 if (rank == HELPERS)
                     for (int c = lane; c < ncols; c += 32) row_pow[c] = a.row_pow[(int64_t)un.tn * a.NT + c];
                 meet();

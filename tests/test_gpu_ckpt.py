@@ -94,6 +94,24 @@ def test_wgrad(M, N, K, fp32):
         assert R.rel(dw, ref) <= (1e-5 if fp32 else 2.6e-3), R.rel(dw, ref)
 
 
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("M,N,K", [(40, 4096, 8192), (8, 2056, 16384), (100, 8, 131072)])
+def test_wgrad_of_few_rows_and_many_tiles(M, N, K, fp32):
+    """Several tiles an SM, each of one or two stages: the results of the last tile must wait for its
+    own products, not for those of a tile before. Tolerances as above (100 rows and fewer)."""
+    x8, xs = save(R.rows(M, K, 3, DEV))
+    dy = R.rows(M, N, 4, DEV, std=0.01)
+    dw = torch.full((N, K), float("nan"), dtype=torch.float32 if fp32 else R.BF16, device=DEV)
+    ws = w4.alloc_ckpt_wgrad_workspace(M, N, K)
+    ref = dy.double().t() @ R.restored(x8, xs)
+    for _ in range(3):
+        dw.fill_(float("nan"))
+        w4.fp8_ckpt_wgrad(dy, x8, xs, M, N, K, dw, w4.W4_OUT_FP32 if fp32 else 0, ws)
+        status_ok()
+        assert bool(torch.isfinite(dw).all())
+        assert R.rel(dw, ref) <= (1e-5 if fp32 else 2.6e-3), R.rel(dw, ref)
+
+
 def test_wgrad_large_and_tiny_scales_and_nan_blocks():
     """Rows of magnitude 2^100 and 2^-100 in one checkpoint, and a block that was not finite."""
     M, N, K = 80, 16, 96

@@ -231,6 +231,26 @@ def test_dgrad(M, N, K, group, mode):
     near(dx, ref, bound, 2.6e-3)
 
 
+@pytest.mark.parametrize("M,H,K,group", [(20, 50000, 32, 32), (300, 20000, 96, 32), (40, 40008, 128, 64)])
+def test_many_tiles_of_a_short_reduction(M, H, K, group):
+    """Several tiles an SM, each of one or two stages, in every product."""
+    wg, wu = weights(H, K, group, "asym", 3)
+    x = R.rows(M, K, 1, DEV)
+    check_gated(x, wg, wu, group, "asym", "silu")
+    dh = R.rows(M, H, 2, DEV, std=0.01)
+    got = run_bwd(dh, wg, wu, group, "asym", "gelu_tanh", X=x)
+    status_ok()
+    check_bwd(got, x, dh, wg, wu, group, "gelu_tanh")
+    N, K = K, H // group * group  # a wide layer of few rows
+    w = R.weight(N, K, group, "asym", 4, DEV)
+    dy = R.rows(M, N, 5, DEV, std=0.01)
+    dx = run_dgrad(dy, w, group, "asym")
+    status_ok()
+    a = R.dequant(w, group)
+    ref = dy.double() @ a
+    near(dx, ref, (2.0 ** -11 + 2.0 ** -12) * (dy.double().abs() @ a.abs()) + R.HALF * ref.abs() + 1e-30, 2.6e-3)
+
+
 def test_results_do_not_change_from_run_to_run_and_workspaces_serve_again():
     """One workspace of the largest need over several shapes, each twice: the same bits."""
     shapes = [(40, 64, 4096, 128), (300, 64, 2048, 128), (1, 8192, 4096, 128), (17, 200, 8192, 128)]
