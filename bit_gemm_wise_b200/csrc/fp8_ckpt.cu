@@ -108,16 +108,9 @@ using namespace w4;
 
 namespace {
 
-constexpr int64_t kMaxRows = (int64_t)1 << 24;
-
-bool ckpt_shape_ok(int64_t M, int64_t K) {
-    return M >= 1 && M <= kMaxRows && K >= 32 && K <= kMaxRows && K % 32 == 0;
-}
-
-// blocks of THREADS threads with PIECES pieces each; 0 where the grid would be too large
+// blocks of THREADS threads with PIECES pieces each (of 2^37 at most: shape_ok)
 unsigned blocks_for(int64_t pieces) {
-    const int64_t b = (pieces + ckpt::THREADS * ckpt::PIECES - 1) / (ckpt::THREADS * ckpt::PIECES);
-    return b <= 0x7fffffff ? (unsigned)b : 0u;
+    return (unsigned)((pieces + ckpt::THREADS * ckpt::PIECES - 1) / (ckpt::THREADS * ckpt::PIECES));
 }
 
 }  // namespace
@@ -125,11 +118,10 @@ unsigned blocks_for(int64_t pieces) {
 W4_API w4_status fp8_ckpt_save(const void *X_bf16, int64_t M, int64_t K, uint8_t *X_e4m3, uint8_t *X_scale,
                                cudaStream_t stream) {
     if (!X_bf16 || !X_e4m3 || !X_scale) return W4_ERR_NULL;
-    if (!ckpt_shape_ok(M, K)) return W4_ERR_SHAPE;
+    if (!xg::shape_ok(M, 1, K)) return W4_ERR_SHAPE;
     if (!aligned16(X_bf16) || !aligned16(X_e4m3) || !aligned16(X_scale)) return W4_ERR_ALIGN;
     const int64_t n = M * (K / 32);
     const unsigned grid = blocks_for(4 * n);
-    if (!grid) return W4_ERR_SHAPE;
     ckpt::save_kernel<<<grid, ckpt::THREADS, 0, stream>>>(static_cast<const uint4 *>(X_bf16), n,
                                                           reinterpret_cast<uint2 *>(X_e4m3), X_scale);
     return launch_status();
@@ -138,11 +130,10 @@ W4_API w4_status fp8_ckpt_save(const void *X_bf16, int64_t M, int64_t K, uint8_t
 W4_API w4_status fp8_ckpt_load(const uint8_t *X_e4m3, const uint8_t *X_scale, int64_t M, int64_t K, void *X_bf16,
                                cudaStream_t stream) {
     if (!X_bf16 || !X_e4m3 || !X_scale) return W4_ERR_NULL;
-    if (!ckpt_shape_ok(M, K)) return W4_ERR_SHAPE;
+    if (!xg::shape_ok(M, 1, K)) return W4_ERR_SHAPE;
     if (!aligned16(X_bf16) || !aligned16(X_e4m3) || !aligned16(X_scale)) return W4_ERR_ALIGN;
     const int64_t n = M * (K / 16);
     const unsigned grid = blocks_for(n);
-    if (!grid) return W4_ERR_SHAPE;
     ckpt::load_kernel<<<grid, ckpt::THREADS, 0, stream>>>(reinterpret_cast<const uint4 *>(X_e4m3), X_scale, n,
                                                           static_cast<uint4 *>(X_bf16));
     return launch_status();
@@ -156,7 +147,7 @@ static xg::Plan wgrad_plan(int64_t M, int64_t N, int64_t K, bool fp32, int sms) 
 }
 
 W4_API size_t fp8_ckpt_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-    if (!ckpt_shape_ok(M, K) || N < 1 || N > kMaxRows || N % 8 != 0) return 0;
+    if (!xg::shape_ok(M, N, K) || N % 8 != 0) return 0;
     return wgrad_plan(M, N, K, false, num_sms()).bytes;
 }
 
@@ -164,7 +155,7 @@ W4_API w4_status fp8_ckpt_wgrad(const void *dY_bf16, const uint8_t *X_e4m3, cons
                                 int64_t K, void *dW, int flags, void *workspace, size_t workspace_bytes,
                                 cudaStream_t stream) {
     if (!dY_bf16 || !X_e4m3 || !X_scale || !dW) return W4_ERR_NULL;
-    if (!ckpt_shape_ok(M, K) || N < 1 || N > kMaxRows || N % 8 != 0) return W4_ERR_SHAPE;
+    if (!xg::shape_ok(M, N, K) || N % 8 != 0) return W4_ERR_SHAPE;
     if ((flags & ~W4_OUT_FP32) != 0) return W4_ERR_ARG;
     for (const void *p : {dY_bf16, (const void *)X_e4m3, (const void *)X_scale, (const void *)dW, (const void *)workspace})
         if (p && !aligned16(p)) return W4_ERR_ALIGN;

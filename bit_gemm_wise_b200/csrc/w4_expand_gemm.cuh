@@ -312,8 +312,9 @@ struct Act {
     float value, slope;
 };
 __device__ __forceinline__ Act act_of(float g, bool gelu) {
-    const float g2 = 0.07135481282f * g * g;                     // 2 sqrt(2/pi) 0.044715 g^2
-    const float p = gelu ? g * (1.5957691216f + g2) : g;
+    const float h = fminf(fmaxf(g, -64.0f), 64.0f);              // exp is 0 or inf there; h^3 stays finite
+    const float g2 = 0.07135481282f * h * h;                     // 2 sqrt(2/pi) 0.044715 g^2
+    const float p = gelu ? h * (1.5957691216f + g2) : g;
     const float dp = gelu ? 1.5957691216f + 3.0f * g2 : 1.0f;     // p'
     const float s = __fdividef(1.0f, 1.0f + __expf(-p));
     Act r;
@@ -323,7 +324,7 @@ __device__ __forceinline__ Act act_of(float g, bool gelu) {
 }
 
 // A unit: its tile, its part of the reduction (stages [b0, b1)) and its place in the partial sums.
-// 32 bits throughout: the plan has fewer than 2^31 units, and a 64-bit division costs hundreds of
+// 32 bits throughout: shape_ok's limits leave fewer than 2^28 units, and a 64-bit division costs hundreds of
 // instructions (six of them at a kernel's start took 4 us).
 struct Unit {
     uint32_t tile, tw, tn, s;
@@ -1013,20 +1014,33 @@ template <bool CKPT> __global__ void __launch_bounds__(256) row_prep_kernel(cons
     }
 }
 
-// Place of the fp16 copy (of `values` in all) and of its powers (M of them, and room for the rest
-// of a column group, which the epilogue may read beside them) behind the first `at` bytes.
+// The workspace starts with the arrival counters, in a region of one size for all shapes (what
+// one call leaves as partial sums or rows is never another's counter), then holds the partial sums.
+constexpr int64_t MAX_SPLIT_TILES = 4096;
+constexpr size_t CNT_BYTES = MAX_SPLIT_TILES * 4 * sizeof(uint32_t);
+
+// Place of the fp16 copy (of `values` in all) and of its powers (M of them) behind the counters and
+// the partial sums, of `sums` bytes together, or 0 where the call has neither.
 struct PrepPlace {
     size_t y, row_pow, end;
 };
-inline PrepPlace place_prep(size_t at, int64_t values, int64_t M) {
+inline PrepPlace place_prep(size_t sums, int64_t values, int64_t M) {
     PrepPlace q;
-    q.y = (at + 255) / 256 * 256;
+    q.y = ((sums > CNT_BYTES ? sums : CNT_BYTES) + 255) / 256 * 256;
     q.row_pow = (q.y + (size_t)values * 2 + 255) / 256 * 256;
-    q.end = (q.row_pow + ((size_t)M + 16) * sizeof(float) + 255) / 256 * 256;
+    q.end = (q.row_pow + (size_t)M * sizeof(float) + 255) / 256 * 256;
     return q;
 }
 
 // ------------------------------------------------------------------ host side
+
+// Limits of M tokens, N rows and K columns of a weight: each dimension fits the kernels' 32-bit
+// arithmetic, and any two of them (an operand's or a result's size) their count of tiles.
+inline bool shape_ok(int64_t M, int64_t N, int64_t K) {
+    constexpr int64_t most = (int64_t)1 << 24, area = (int64_t)1 << 40;
+    return M >= 1 && M <= most && N >= 1 && N <= most && K >= 32 && K <= most && K % 32 == 0 && M * N <= area &&
+           M * K <= area && N * K <= area;
+}
 
 struct Plan {
     int64_t Tw, Tn, units;
@@ -1034,11 +1048,6 @@ struct Plan {
     uint32_t stage_bytes;
     size_t bytes;                   // of the workspace, 0 where S is 1
 };
-
-// The workspace starts with the arrival counters, in a region of one size for all shapes (what
-// one call leaves as partial sums is never another's counter), then holds the partial sums.
-constexpr int64_t MAX_SPLIT_TILES = 4096;
-constexpr size_t CNT_BYTES = MAX_SPLIT_TILES * 4 * sizeof(uint32_t);
 
 // lanes: weight rows per projection (FWD) or columns K; cols: the other side; red: length of the
 // reduction (per source), sources 1 or 2; max_rows: reduction that one accumulator may sum.
@@ -1177,7 +1186,6 @@ inline w4_status launch_prep(const Prep &p, bool behind, cudaStream_t stream) {
 
 template <int KIND, bool GRADS, bool GELU>
 w4_status launch(const Plan &p, Maps &tm, Args a, void *workspace, int sms, cudaStream_t stream) {
-    if (p.units > (1 << 30)) return W4_ERR_SHAPE;  // more than the kernel counts
     bool maps = true;
     if (KIND == WGRAD) {
         maps = make_raw_map(&tm.q[0], a.x8, a.rows, a.K, 128, BK);

@@ -509,11 +509,6 @@ using namespace w4;
 namespace {
 
 constexpr int64_t kFewRows = 16;  // up to here w4a16_gated reads the weights as a decode step does
-constexpr int64_t kMaxRows = (int64_t)1 << 24;
-
-bool gated_shape_ok(int64_t M, int64_t N, int64_t K) {
-    return M >= 1 && M <= kMaxRows && N >= 1 && N <= kMaxRows && K >= 32 && K <= kMaxRows && K % 32 == 0;
-}
 
 int group_shift(int g) { return g == 32 ? 5 : g == 64 ? 6 : g == 128 ? 7 : 8; }
 
@@ -529,7 +524,7 @@ w4_status weight_ok(const uint8_t *codes, const uint16_t *scales, const int16_t 
 }  // namespace
 
 W4_API size_t w4a16_gated_workspace_bytes(int64_t M, int64_t H, int64_t K, int group) {
-    if (!gated_shape_ok(M, H, K) || !valid_group(group) || K % group != 0) return 0;
+    if (!xg::shape_ok(M, H, K) || !valid_group(group) || K % group != 0) return 0;
     if (M <= kFewRows) return gated::by_bytes(M, H, K) ? gated::bytes_place(M, K, group).end : 0;
     return xg::place_prep(xg::make_plan(xg::FWD, H, M, K, 1, 0, num_sms()).bytes, M * K, M).end;
 }
@@ -539,7 +534,7 @@ W4_API w4_status w4a16_gated(const void *X_bf16, int64_t M, const uint8_t *codes
                              const int16_t *zeros_up, int64_t H, int64_t K, int group, int mode, int act, void *Y_bf16,
                              void *workspace, size_t workspace_bytes, cudaStream_t stream) {
     if (!X_bf16 || !Y_bf16) return W4_ERR_NULL;
-    if (!gated_shape_ok(M, H, K)) return W4_ERR_SHAPE;
+    if (!xg::shape_ok(M, H, K)) return W4_ERR_SHAPE;
     if (!valid_group(group) || K % group != 0) return W4_ERR_GROUP;
     if (!valid_mode(mode) || (act != W4_ACT_SILU && act != W4_ACT_GELU_TANH)) return W4_ERR_ARG;
     w4_status st = weight_ok(codes_gate, scales_gate, zeros_gate, mode);
@@ -617,7 +612,7 @@ BwdLayout bwd_layout(int64_t M, int64_t H, int64_t K, int sms) {
 }  // namespace
 
 W4_API size_t w4a16_gated_bwd_workspace_bytes(int64_t M, int64_t H, int64_t K, int group, int from_ckpt) {
-    if (!gated_shape_ok(M, H, K) || H % 8 != 0 || !valid_group(group) || K % group != 0) return 0;
+    if (!xg::shape_ok(M, H, K) || H % 8 != 0 || !valid_group(group) || K % group != 0) return 0;
     (void)from_ckpt;  // both sources become the same fp16 rows
     return bwd_layout(M, H, K, num_sms()).q.end;
 }
@@ -631,7 +626,7 @@ W4_API w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const 
     const bool ckpt = X_bf16 == nullptr;
     if (!dH_bf16 || !dG_bf16 || !dU_bf16 || (ckpt && (!X_e4m3 || !X_scale))) return W4_ERR_NULL;
     if (!ckpt && (X_e4m3 || X_scale)) return W4_ERR_ARG;
-    if (!gated_shape_ok(M, H, K) || H % 8 != 0) return W4_ERR_SHAPE;
+    if (!xg::shape_ok(M, H, K) || H % 8 != 0) return W4_ERR_SHAPE;
     if (!valid_group(group) || K % group != 0) return W4_ERR_GROUP;
     if (!valid_mode(mode) || (act != W4_ACT_SILU && act != W4_ACT_GELU_TANH)) return W4_ERR_ARG;
     w4_status st = weight_ok(codes_gate, scales_gate, zeros_gate, mode);
@@ -691,7 +686,7 @@ W4_API w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const 
 }
 
 W4_API size_t w4a16_dgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int group) {
-    if (!gated_shape_ok(M, N, K) || N % 8 != 0 || !valid_group(group) || K % group != 0) return 0;
+    if (!xg::shape_ok(M, N, K) || N % 8 != 0 || !valid_group(group) || K % group != 0) return 0;
     return xg::place_prep(xg::make_plan(xg::DGRAD, K, M, N, 1, 0, num_sms()).bytes, M * N, M).end;
 }
 
@@ -699,7 +694,7 @@ W4_API w4_status w4a16_dgrad(const void *dY_bf16, int64_t M, const uint8_t *code
                              const int16_t *zeros, int64_t N, int64_t K, int group, int mode, void *dX_bf16,
                              void *workspace, size_t workspace_bytes, cudaStream_t stream) {
     if (!dY_bf16 || !dX_bf16) return W4_ERR_NULL;
-    if (!gated_shape_ok(M, N, K) || N % 8 != 0) return W4_ERR_SHAPE;
+    if (!xg::shape_ok(M, N, K) || N % 8 != 0) return W4_ERR_SHAPE;
     if (!valid_group(group) || K % group != 0) return W4_ERR_GROUP;
     if (!valid_mode(mode)) return W4_ERR_ARG;
     w4_status st = weight_ok(codes, scales, zeros, mode);

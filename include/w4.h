@@ -563,8 +563,10 @@ w4_status w4_nf4_gemv(const void *x_bf16, int64_t M, const uint8_t *codes, const
  *   accumulation; X enters as fp16 after each row is divided by a power of two, exact for values
  *   within 2^-31 of the row's largest.
  *   Outputs must not overlap inputs. Results are bit-identical run to run on a given GPU.
- *   M, H <= 2^24; 32 <= K <= 2^24, K % 32 == 0. Errors: NULL / SHAPE / GROUP / ALIGN / ARG (mode,
- *   act, zeros given for W4_SYM) / WORKSPACE / CUDA.
+ *   Over a reduction of R terms the tensor cores' fp32 sums are off by R / 16 * 2^-23 of the largest
+ *   partial sum at most (they truncate): within bf16's own rounding up to R = 2^18.
+ *   M, H <= 2^24; 32 <= K <= 2^24, K % 32 == 0; M * H, M * K and H * K <= 2^40. Errors: NULL / SHAPE /
+ *   GROUP / ALIGN / ARG (mode, act, zeros given for W4_SYM) / WORKSPACE / CUDA.
  */
 size_t w4a16_gated_workspace_bytes(int64_t M, int64_t H, int64_t K, int group);
 w4_status w4a16_gated(const void *X_bf16, int64_t M, const uint8_t *codes_gate, const uint16_t *scales_gate,
@@ -602,7 +604,7 @@ w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const uint8_t
  *   dY_bf16 [M, N], dX_bf16 [M, K] bf16; codes, scales, zeros as w4_quantize writes them for W[N, K].
  *   workspace as w4a16_gated's, of w4a16_dgrad_workspace_bytes(M, N, K, group) bytes, always needed.
  *   Weights and dY enter the product as w4a16_gated's do at M > 16.
- *   M <= 2^24; N <= 2^24, N % 8 == 0; K as w4a16_gated. Errors as w4a16_gated.
+ *   N % 8 == 0; other limits (with H for N) and errors as w4a16_gated.
  */
 size_t w4a16_dgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int group);
 w4_status w4a16_dgrad(const void *dY_bf16, int64_t M, const uint8_t *codes, const uint16_t *scales,
@@ -619,7 +621,7 @@ w4_status w4a16_dgrad(const void *dY_bf16, int64_t M, const uint8_t *codes, cons
  *   X_bf16 [M, K] bf16; X_e4m3 uint8 [M, K]; X_scale uint8 [M, K/32], the byte e + 127. A block of 32
  *   with an infinity or a NaN gets scale byte 255 and values 0x7F, and restores as NaN.
  *   fp8_ckpt_load writes value * 2^e to bf16, exactly; a scale byte of 255 makes its block NaN.
- *   M >= 1; K >= 32, K % 32 == 0. Errors: NULL / SHAPE / ALIGN / CUDA.
+ *   1 <= M <= 2^24; 32 <= K <= 2^24, K % 32 == 0; M * K <= 2^40. Errors: NULL / SHAPE / ALIGN / CUDA.
  */
 w4_status fp8_ckpt_save(const void *X_bf16, int64_t M, int64_t K, uint8_t *X_e4m3, uint8_t *X_scale,
                         cudaStream_t stream);
@@ -630,9 +632,10 @@ w4_status fp8_ckpt_load(const uint8_t *X_e4m3, const uint8_t *X_scale, int64_t M
  * fp8_ckpt_wgrad -- the gradient of a linear layer y = x W^T by its weight (an adapter's, or a full
  *   one's) from the 8-bit checkpoint of x: dW[n, k] = sum_m dY[m, n] x8[m, k] 2^e[m, k/32].
  *   dY_bf16 [M, N] bf16; X_e4m3, X_scale as fp8_ckpt_save writes them for x [M, K]; dW [N, K] bf16, or
- *   fp32 with W4_OUT_FP32 in flags. The products are exact, accumulation is fp32.
+ *   fp32 with W4_OUT_FP32 in flags. The products are exact; accumulation is fp32, for fp32 results
+ *   outside the tensor cores from 2048 rows to the next.
  *   workspace as w4a16_gated's, of fp8_ckpt_wgrad_workspace_bytes(M, N, K) bytes.
- *   M, N <= 2^24, N % 8 == 0; 32 <= K <= 2^24, K % 32 == 0. Errors: NULL / SHAPE / ALIGN / ARG / WORKSPACE / CUDA.
+ *   N % 8 == 0; other limits as w4a16_gated (with N for H). Errors: NULL / SHAPE / ALIGN / ARG / WORKSPACE / CUDA.
  */
 size_t fp8_ckpt_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K);
 w4_status fp8_ckpt_wgrad(const void *dY_bf16, const uint8_t *X_e4m3, const uint8_t *X_scale, int64_t M, int64_t N,

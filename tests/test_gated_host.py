@@ -41,6 +41,17 @@ def test_shapes_groups_and_modes(fn, kw, code):
     assert fn(**kw) == code
 
 
+def test_products_of_two_dimensions_are_limited():
+    """2^40 elements an operand or result: refused before anything is launched."""
+    big = 1 << 24
+    for fn, kw in [(gated, dict(M=big, H=1 << 17)), (bwd, dict(M=big, H=1 << 17)), (dgrad, dict(M=big, N=1 << 17)),
+                   (wgrad, dict(M=big, N=1 << 17)), (gated, dict(M=big, K=1 << 17)), (gated, dict(H=big, K=1 << 17))]:
+        assert fn(**kw) == SHAPE
+    assert w4.lib().fp8_ckpt_save(FAKE, big, 1 << 17, FAKE, FAKE, None) == SHAPE
+    assert w4.lib().fp8_ckpt_load(FAKE, FAKE, big, 1 << 17, FAKE, None) == SHAPE
+    assert w4.w4a16_gated_workspace_bytes(big, 1 << 17, 128, 128) == 0
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(X=None), NULL), (dict(Y=None), NULL), (dict(wg=(None, FAKE, FAKE)), NULL), (dict(wu=(FAKE, None, FAKE)), NULL),
     (dict(wu=(FAKE, FAKE, None)), NULL), (dict(mode=0), ARG), (dict(mode=0, wg=(FAKE, FAKE, None)), ARG),

@@ -112,6 +112,23 @@ def test_wgrad_of_few_rows_and_many_tiles(M, N, K, fp32):
         assert R.rel(dw, ref) <= (1e-5 if fp32 else 2.6e-3), R.rel(dw, ref)
 
 
+@pytest.mark.parametrize("M,N,K", [(5000, 24, 160), (4100, 1544, 4128), (2049, 8, 32), (9000, 264, 1056)])
+def test_wgrad_of_many_rows(M, N, K):
+    """fp32 results are added up from 2048 rows to the next: 2048 / 16 * 2^-23 = 1.53e-5 of a partial sum
+    at most, and a rounding of 2^-24 for each of the five partial sums at most: 1.6e-5. bf16 sums
+    truncate at M / 16 steps: 9000 / 16 * 2^-23 = 6.7e-5, with 2^-8 / sqrt(3) = 2.26e-3 below 2.6e-3."""
+    x8, xs = save(R.rows(M, K, 3, DEV))
+    dy = R.rows(M, N, 4, DEV, std=0.01)
+    ref = dy.double().t() @ R.restored(x8, xs)
+    ws = w4.alloc_ckpt_wgrad_workspace(M, N, K)
+    for fp32 in (True, False, True):
+        dw = torch.full((N, K), float("nan"), dtype=torch.float32 if fp32 else R.BF16, device=DEV)
+        w4.fp8_ckpt_wgrad(dy, x8, xs, M, N, K, dw, w4.W4_OUT_FP32 if fp32 else 0, ws)
+        status_ok()
+        assert bool(torch.isfinite(dw).all())
+        assert R.rel(dw, ref) <= (1.6e-5 if fp32 else 2.6e-3), R.rel(dw, ref)
+
+
 def test_wgrad_large_and_tiny_scales_and_nan_blocks():
     """Rows of magnitude 2^100 and 2^-100 in one checkpoint, and a block that was not finite."""
     M, N, K = 80, 16, 96
@@ -164,3 +181,54 @@ def test_training_step_of_an_adapter():
     rg, ru, rx = R.gated_grads(xr, dh, wg, wu, g, "silu")
     assert R.rel(dg, rg) <= 2.6e-3 and R.rel(du, ru) <= 2.6e-3 and R.rel(dx, rx) <= 3.5e-3
     assert R.rel(da, t.double().t() @ xr) <= 1e-5
+
+
+@pytest.mark.parametrize("M,H,K", [(24, 264, 512), (300, 1032, 768)])
+def test_a_captured_step_with_one_workspace(M, H, K):
+    """Forward, checkpoint, backward and both kinds of weight product on a side stream and in a
+    captured graph, all through one workspace, replayed on new inputs: bit for bit the separate
+    calls' results."""
+    g = 64
+    wg, wu, wd = (R.weight(*s, g, "asym", i, DEV) for i, s in enumerate([(H, K), (H, K), (K, H // g * g)]))
+    ins = [(R.rows(M, K, s, DEV), R.rows(M, H, s + 10, DEV, std=0.01), R.rows(M, K, s + 20, DEV, std=0.01)) for s in (1, 2, 3)]
+    need = max(w4.w4a16_gated_workspace_bytes(M, H, K, g), w4.w4a16_gated_bwd_workspace_bytes(M, H, K, g, 1),
+               w4.w4a16_dgrad_workspace_bytes(M, K, H // g * g, g), w4.fp8_ckpt_wgrad_workspace_bytes(M, H, K))
+
+    def outputs():
+        f = lambda *s, t=R.BF16: torch.full(s, float("nan"), dtype=t, device=DEV)
+        return [f(M, H), f(M, H), f(M, H), f(M, K), f(M, H // g * g), f(H, K, t=torch.float32)]
+
+    def step(x, dh, dy, o, ck, ws, **kw):
+        x8, xs = ck
+        w = (lambda n: ws) if ws is not None else (lambda n: torch.zeros(max(n, 16), dtype=torch.uint8, device=DEV))
+        w4.w4a16_gated(x, M, wg, wu, H, K, g, "asym", "silu", o[0], w(w4.w4a16_gated_workspace_bytes(M, H, K, g)), **kw)
+        w4.fp8_ckpt_save(x, M, K, x8, xs, **kw)
+        w4.w4a16_dgrad(dy, M, wd, K, H // g * g, g, "asym", o[4], w(w4.w4a16_dgrad_workspace_bytes(M, K, H // g * g, g)), **kw)
+        w4.w4a16_gated_bwd(dh, M, wg, wu, H, K, g, "asym", "silu", o[1], o[2], o[3],
+                           w(w4.w4a16_gated_bwd_workspace_bytes(M, H, K, g, 1)), X8=x8, x_scale=xs, **kw)
+        w4.fp8_ckpt_wgrad(o[1], x8, xs, M, H, K, o[5], w4.W4_OUT_FP32, w(w4.fp8_ckpt_wgrad_workspace_bytes(M, H, K)), **kw)
+
+    want = []
+    for i in ins:
+        want.append(outputs())
+        step(*i, want[-1], w4.alloc_ckpt(M, K), None)
+    ws, o, ck = torch.zeros(need, dtype=torch.uint8, device=DEV), outputs(), w4.alloc_ckpt(M, K)
+    buf = [t.clone() for t in ins[0]]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(2):  # what the first round leaves in the workspace, too
+        step(*buf, o, ck, ws, stream=s)
+        s.synchronize()
+        assert [torch.equal(a, b) for a, b in zip(o, want[0])] == [True] * 6
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        step(*buf, o, ck, ws)
+    for i in (1, 2, 0):
+        for b, v in zip(buf, ins[i]):
+            b.copy_(v)
+        for t in o:
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(o, want[i]))
+    status_ok()

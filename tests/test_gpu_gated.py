@@ -95,7 +95,7 @@ SHAPES = [
     (300, 1000, 2048, 128, "asym"), (520, 96, 8192, 256, "sym"), (1, 2049, 2048, 128, "asym"), (3, 515, 14336, 128, "asym"),
     # one and two rows of layers from 2^25 weights a matrix (their own kernel), and three beside them
     (1, 8200, 4096, 128, "asym"), (2, 4097, 8192, 32, "sym"), (2, 16391, 2048, 64, "asym"), (1, 2056, 16384, 256, "asym"),
-    (1, 65536, 544, 32, "asym"), (3, 8192, 4096, 64, "sym"),
+    (1, 65536, 544, 32, "asym"), (3, 8192, 4096, 64, "sym"), (2, 1048577, 32, 32, "asym"), (1, 524289, 64, 64, "sym"),
 ]
 
 
@@ -249,6 +249,31 @@ def test_many_tiles_of_a_short_reduction(M, H, K, group):
     a = R.dequant(w, group)
     ref = dy.double() @ a
     near(dx, ref, (2.0 ** -11 + 2.0 ** -12) * (dy.double().abs() @ a.abs()) + R.HALF * ref.abs() + 1e-30, 2.6e-3)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("M", [2, 40])
+def test_activations_far_outside_their_bend(act, M):
+    """|G| around 1e20, whose square is not a float: act(g) is g or 0 there, its slope 1 or 0."""
+    H, K, g = 200, 256, 64
+    wg, wu = weights(H, K, g, "asym", 9)
+    x, dh = (R.rows(M, K, 1, DEV).double() * 2.0 ** 68).to(R.BF16), (R.rows(M, H, 2, DEV).double() * 2.0 ** -90).to(R.BF16)
+    G, U, d = x.double() @ R.dequant(wg, g).t(), x.double() @ R.dequant(wu, g).t(), dh.double()
+    y = run_gated(x, wg, wu, g, "asym", act)
+    dg, du, _ = run_bwd(dh, wg, wu, g, "asym", act, X=x, want_dx=False)
+    status_ok()
+    # the weights' and the sums' roundings, then the result's
+    e = 2.0 ** -11 + 2.0 ** -12
+    eg, eu = e * magnitudes(x, wg, g), e * magnitudes(x, wu, g)
+    sure, on = G.abs() > eg, (G > 0).double()
+    assert float(sure.double().mean()) > 0.95
+    for got, ref, off in ((y, G * U * on, eg * (U.abs() + eu) + G.abs() * eu), (dg, d * U * on, d.abs() * eu), (du, d * G * on, d.abs() * eg)):
+        got, bound = got.double(), off * on + (1 + R.HALF) * R.HALF * (ref.abs() + off * on)
+        assert not bool(torch.isnan(got).any())
+        # y is up to 1e40: past bf16's largest value, 3.39e38, it is infinite
+        inside = sure & (ref.abs() + bound < 3.38e38)
+        assert bool(inside.any()) and not bool((inside & ((got - ref).abs() > bound)).any())
+        assert bool((got.abs() >= 3.38e38)[sure & (ref.abs() - bound > 3.4e38)].all())
 
 
 def test_results_do_not_change_from_run_to_run_and_workspaces_serve_again():
