@@ -232,3 +232,33 @@ def test_a_captured_step_with_one_workspace(M, H, K):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(o, want[i]))
     status_ok()
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 values in the checkpoint, and in dW: the last rows."""
+    M, K = 66000, 32768
+    x = torch.randn(M, K, device=DEV, dtype=R.BF16, generator=torch.Generator(device=DEV).manual_seed(1))
+    x8, xs = save(x)
+    back = load(x8, xs)
+    status_ok()
+    for sl in (slice(0, 64), slice(M - 64, M)):
+        rs, rv = R.save(x[sl].cpu())
+        assert torch.equal(xs[sl].cpu(), rs) and torch.equal(x8[sl].cpu().view(torch.float8_e4m3fn).double(), rv)
+        assert torch.equal(back[sl].double(), R.restored(x8[sl], xs[sl]))
+    del x, back
+    dy = R.rows(M, 8, 2, DEV, std=0.01)
+    dw = torch.full((8, K), float("nan"), dtype=R.BF16, device=DEV)
+    w4.fp8_ckpt_wgrad(dy, x8, xs, M, 8, K, dw, 0, w4.alloc_ckpt_wgrad_workspace(M, 8, K))
+    status_ok()
+    cols = slice(K - 96, K)
+    ref = dy.double().t() @ R.restored(x8[:, cols].contiguous(), xs[:, K // 32 - 3:].contiguous())
+    # truncation at 66000 / 16 steps, 2^-23 each: 4.9e-4, beside the output's 2.26e-3
+    assert R.rel(dw[:, cols], ref) <= 2.9e-3
+    n, m = 66000, 20
+    x8, xs = x8[:m].contiguous(), xs[:m].contiguous()
+    dy = R.rows(m, n, 3, DEV)
+    dw = torch.full((n, K), float("nan"), dtype=torch.float32, device=DEV)
+    w4.fp8_ckpt_wgrad(dy, x8, xs, m, n, K, dw, w4.W4_OUT_FP32, w4.alloc_ckpt_wgrad_workspace(m, n, K))
+    status_ok()
+    for sl in (slice(0, 100), slice(n - 200, n)):
+        assert R.rel(dw[sl], dy[:, sl].double().t() @ R.restored(x8, xs)) <= 1e-5

@@ -276,6 +276,54 @@ def test_activations_far_outside_their_bend(act, M):
         assert bool((got.abs() >= 3.38e38)[sure & (ref.abs() - bound > 3.4e38)].all())
 
 
+def test_two_calls_at_once():
+    """Two streams, each with its own workspace, many rows and few, none waiting for the other."""
+    g = 64
+    calls = []
+    for M, H, K in [(300, 1024, 2048), (40, 4096, 1024), (2, 8192, 4096), (9, 4096, 1024)]:
+        wg, wu = weights(H, K, g, "asym", M)
+        x = R.rows(M, K, M, DEV)
+        calls.append((x, wg, wu, w4.alloc_gated_workspace(M, H, K, g), nan_like(M, H), run_gated(x, wg, wu, g, "asym", "silu")))
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, (x, wg, wu, ws, y, _) in zip(streams, calls):
+            w4.w4a16_gated(x, x.shape[0], wg, wu, y.shape[1], x.shape[1], g, "asym", "silu", y, ws, stream=s)
+    status_ok()
+    for x, wg, wu, ws, y, want in calls:
+        assert torch.equal(y, want)
+
+
+def big_weight(N, K, group, seed):
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    codes = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device=DEV, generator=gen)
+    s = (torch.rand(N, K // group, device=DEV, generator=gen) * 0.01 + 0.001).half()
+    return codes, s, torch.randint(0, 16, (N, K // group), dtype=torch.int16, device=DEV, generator=gen)
+
+
+def test_offsets_past_32_bits():
+    """Codes of more than 2^32 bytes and results of more than 2^31 values: the last features and rows."""
+    g, H, K = 128, 1 << 21, 4160 // 128 * 128 + 128
+    wg, wu = big_weight(H, K, g, 1), big_weight(H, K, g, 2)
+    assert wg[0].numel() > 1 << 32
+    cut = lambda w, sl: tuple(t[sl].contiguous() for t in w)
+    for M in (1, 3, 20):
+        x = R.rows(M, K, M, DEV)
+        y = run_gated(x, wg, wu, g, "asym", "silu")
+        status_ok()
+        for sl in (slice(0, 64), slice(H - 200, H)):
+            want = R.gated(x, cut(wg, sl), cut(wu, sl), g, "silu")
+            assert R.rel(y[:, sl], want) <= 2.6e-3
+    del wg, wu, y
+    M, N, K = 70000, 8, 32768
+    w = R.weight(N, K, g, "asym", 3, DEV)
+    dy = R.rows(M, N, 4, DEV)
+    dx = run_dgrad(dy, w, g, "asym")
+    status_ok()
+    for sl in (slice(0, 128), slice(M - 300, M)):
+        assert R.rel(dx[sl], dy[sl].double() @ R.dequant(w, g)) <= 2.6e-3
+
+
 def test_results_do_not_change_from_run_to_run_and_workspaces_serve_again():
     """One workspace of the largest need over several shapes, each twice: the same bits."""
     shapes = [(40, 64, 4096, 128), (300, 64, 2048, 128), (1, 8192, 4096, 128), (17, 200, 8192, 128)]
