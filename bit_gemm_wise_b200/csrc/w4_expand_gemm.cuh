@@ -131,17 +131,58 @@ struct Maps {
     CUtensorMap b[2], q[2];
 };
 
+template <bool PAIR>
 __device__ __forceinline__ void mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
     // descriptor high word: 1024 bytes between groups of eight rows, version 1, 128-byte swizzle
     constexpr uint32_t hi = 64u | (1u << 14) | (2u << 29);
-    asm volatile(
-        "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
-        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(hi));
+    if (PAIR)
+        asm volatile(
+            "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+            " tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
+            "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(hi));
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
+            "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(hi));
 }
-__device__ __forceinline__ void mma_commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-                 : "memory");
+// PAIR: arrives at the barrier of either CTA
+template <bool PAIR> __device__ __forceinline__ void mma_commit(uint64_t *bar) {
+    if (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                smem_addr(bar)),
+            "h"((uint16_t)3)
+            : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                     : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// all threads of both CTAs
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// arrives at the first CTA's barrier of that place
+__device__ __forceinline__ void arrive_first(uint64_t *bar) {
+    asm volatile(
+        "{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %0, 0;\n mbarrier.arrive.shared::cluster.b64 _, [r];\n}\n" ::"r"(
+            smem_addr(bar))
+        : "memory");
+}
+// a wait whose arrivals come from both CTAs
+__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -286,9 +327,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, Smem *
     return slow_wait(bar, parity, &sm->abort, status);
 }
 // The same by the one thread that runs a producer's or the MMA issuer's loop.
+template <bool PAIR>
 static __device__ __noinline__ bool slow_wait1(uint64_t *bar, uint32_t parity, int *abort, int *status) {
     const long long t0 = clock64();
-    while (!mbar_try_wait_short(bar, parity)) {
+    while (!(PAIR ? try_wait_cluster(bar, parity) : mbar_try_wait_short(bar, parity))) {
         if (*(volatile int *)abort) return false;
         if (clock64() - t0 > kWaitCycles) {
             *(volatile int *)abort = 1;
@@ -298,8 +340,9 @@ static __device__ __noinline__ bool slow_wait1(uint64_t *bar, uint32_t parity, i
     }
     return true;
 }
-__device__ __forceinline__ bool wait1(uint64_t *bar, uint32_t parity, Smem *sm, int *status) {
-    return mbar_try_wait_short(bar, parity) || slow_wait1(bar, parity, &sm->abort, status);
+template <bool PAIR = false> __device__ __forceinline__ bool wait1(uint64_t *bar, uint32_t parity, Smem *sm, int *status) {
+    return (PAIR ? try_wait_cluster(bar, parity) : mbar_try_wait_short(bar, parity)) ||
+           slow_wait1<PAIR>(bar, parity, &sm->abort, status);
 }
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
@@ -330,7 +373,10 @@ struct Unit {
     uint32_t tile, tw, tn, s;
     int b0, b1;
 };
-__device__ __forceinline__ Unit unit_of(const Args &a, uint32_t u) {
+// A pair's tile is two tiles of lanes, one for each CTA; a CTA's place is among the tiles of one.
+template <bool PAIR> __device__ __forceinline__ uint32_t first_unit() { return PAIR ? blockIdx.x >> 1 : blockIdx.x; }
+template <bool PAIR> __device__ __forceinline__ uint32_t unit_step() { return PAIR ? gridDim.x >> 1 : gridDim.x; }
+template <bool PAIR> __device__ __forceinline__ Unit unit_of(const Args &a, uint32_t u) {
     Unit t;
     const uint32_t r = u / (uint32_t)a.Tw;
     t.tw = u - r * (uint32_t)a.Tw;
@@ -347,26 +393,30 @@ __device__ __forceinline__ Unit unit_of(const Args &a, uint32_t u) {
         t.b1 = t.b0 + a.part_kb + (t.s < (uint32_t)a.part_more ? 1 : 0);
     }
     t.tile = t.tn * (uint32_t)a.Tw + t.tw;
+    if (PAIR) {
+        t.tw = 2 * t.tw + cluster_rank();
+        t.tile = 2 * t.tile + cluster_rank();
+    }
     return t;
 }
 
 // The stages of this CTA's units, one after the other.
-struct Walk {
+template <bool PAIR> struct Walk {
     uint32_t u;
     Unit un;
     int kb;
     __device__ __forceinline__ void start(const Args &a) {  // the grid has a unit for every CTA
-        u = blockIdx.x;
-        un = unit_of(a, u);
+        u = first_unit<PAIR>();
+        un = unit_of<PAIR>(a, u);
         kb = un.b0;
     }
     __device__ __forceinline__ bool skip(const Args &a, int n) {  // false: there are no more
         kb += n;
         while (kb >= un.b1) {
             const int over = kb - un.b1;
-            u += gridDim.x;
+            u += unit_step<PAIR>();
             if (u >= (uint32_t)a.units) return false;
-            un = unit_of(a, u);
+            un = unit_of<PAIR>(a, u);
             kb = un.b0 + over;
         }
         return true;
@@ -383,7 +433,7 @@ template <int KIND, int TPG> struct Scales {
     const uint16_t *ps[2], *pz[2];  // FWD: of the tile's first row (for symmetric weights pz is ps)
     uint32_t tile = ~0u, rows;      // FWD: whose row it is, and which of the thread's rows exist
 
-    __device__ __forceinline__ void fetch(const Args &a, const Walk &w, int tt) {
+    template <bool PAIR> __device__ __forceinline__ void fetch(const Args &a, const Walk<PAIR> &w, int tt) {
         const int K = (int)a.K, n = (int)a.rows;  // at most 2^24
         there = 0u;
         if (KIND == WGRAD) {
@@ -460,9 +510,10 @@ template <int KIND, int TPG> struct Place {
     __device__ __forceinline__ explicit Place(int tt) {
         const int r = tt >> 1;
         const int row = KIND == FWD ? 32 * (r >> 4) + (r & 15) : tt >> 2;
-        // DGRAD, WGRAD: the threads of the second 64 columns write their pieces in the order
-        // 2, 3, 0, 1: the eight threads of a quarter warp then write eight different 16-byte banks
-        const uint32_t flip = KIND != FWD && (tt & 2) ? 32u : 0u;
+        // DGRAD, WGRAD: every other thread (by the parity of three bits of its number) takes its pieces in
+        // the order 2, 3, 0, 1: the eight threads of a quarter warp then write eight different 16-byte
+        // banks, and threads whose codes are 128 bytes apart read different banks
+        const uint32_t flip = KIND != FWD && (((tt >> 1) ^ (tt >> 2) ^ (tt >> 3)) & 1) ? 32u : 0u;
         const uint32_t at = (KIND == FWD ? 0u : (uint32_t)((tt >> 1) & 1) * 8192u) + (uint32_t)row * 128u;
 #pragma unroll
         for (int i = 0; i < 4; ++i) out[i] = at + ((((uint32_t)(tt & 1) << 6) + 16u * i) ^ flip ^ ((uint32_t)(row & 7) << 4));
@@ -619,7 +670,7 @@ __device__ __forceinline__ void emit(const Args &a, const float *row_pow, const 
     }
 }
 
-template <int KIND, bool GRADS, bool GELU>
+template <int KIND, bool GRADS, bool GELU, bool PAIR>
 __global__ void __launch_bounds__((RolesOf<KIND, GRADS>::THREADS), 1) expand_gemm_kernel(const __grid_constant__ Maps tm,
                                                                                        const __grid_constant__ Args a) {
     using R = RolesOf<KIND, GRADS>;
@@ -631,7 +682,7 @@ __global__ void __launch_bounds__((RolesOf<KIND, GRADS>::THREADS), 1) expand_gem
     const int NS = a.stages, NR = a.raws;
 
     // the expansion's first scales, on their way while the CTA sets up
-    Walk w;
+    Walk<PAIR> w;
     bool more = false;
     Scales<KIND, R::TPG> next;
     if (warp < R::EXPAND) {
@@ -641,7 +692,7 @@ __global__ void __launch_bounds__((RolesOf<KIND, GRADS>::THREADS), 1) expand_gem
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
-            mbar_init(&sm->full[s], 1 + R::WPG);
+            mbar_init(&sm->full[s], 1 + R::WPG + (PAIR && cluster_rank() == 0 ? 1 : 0));
             mbar_init(&sm->empty[s], 1);
         }
         for (int s = 0; s < NR; ++s) {
@@ -650,19 +701,27 @@ __global__ void __launch_bounds__((RolesOf<KIND, GRADS>::THREADS), 1) expand_gem
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sm->accf[b], 1);
-            mbar_init(&sm->acce[b], R::OUT);
+            mbar_init(&sm->acce[b], PAIR ? 2 * R::OUT : R::OUT);
         }
         sm->abort = 0;
         fence_mbar_init();
     }
     if (warp == R::W_MMA) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sm->tmem_base)),
-                     "r"(512u)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        if (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sm->tmem_base)),
+                         "r"(512u)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sm->tmem_base)),
+                         "r"(512u)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
     }
     tc_fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();  // the other CTA's barriers are ready
     tc_fence_after();
     const uint32_t tmem = sm->tmem_base;
 
@@ -701,9 +760,9 @@ __global__ void __launch_bounds__((RolesOf<KIND, GRADS>::THREADS), 1) expand_gem
             uint32_t phase = 0;
             bool ok = true;
             const uint32_t bytes = a.stage_bytes - A_BYTES;
-            for (uint32_t u = blockIdx.x; u < (uint32_t)a.units && ok; u += gridDim.x) {
-                const Unit un = unit_of(a, u);
-                const int c0 = (int)(un.tn * a.NT);
+            for (uint32_t u = first_unit<PAIR>(); u < (uint32_t)a.units && ok; u += unit_step<PAIR>()) {
+                const Unit un = unit_of<PAIR>(a, u);
+                const int c0 = (int)(un.tn * a.NT) + (PAIR ? (int)cluster_rank() * (a.NT >> 1) : 0);  // a half each
                 for (int kb = un.b0; kb < un.b1; ++kb) {
                     if (!wait1(&sm->empty[slot], phase ^ 1u, sm, a.status)) { ok = false; break; }
                     uint8_t *dst = base + (size_t)slot * a.stage_bytes + A_BYTES;
@@ -731,8 +790,8 @@ __global__ void __launch_bounds__((RolesOf<KIND, GRADS>::THREADS), 1) expand_gem
             int rs = 0, issued = 0;
             uint32_t rphase = 0;
             bool ok = true;
-            for (uint32_t u = blockIdx.x; u < (uint32_t)a.units && ok; u += gridDim.x) {
-                const Unit un = unit_of(a, u);
+            for (uint32_t u = first_unit<PAIR>(); u < (uint32_t)a.units && ok; u += unit_step<PAIR>()) {
+                const Unit un = unit_of<PAIR>(a, u);
                 const int tw = (int)un.tw;
                 for (int kb = un.b0; kb < un.b1; ++kb) {
                     if (!wait1(&sm->rawe[rs], rphase ^ 1u, sm, a.status)) { ok = false; break; }
@@ -757,37 +816,57 @@ __global__ void __launch_bounds__((RolesOf<KIND, GRADS>::THREADS), 1) expand_gem
         __syncwarp();
     } else if (warp == R::W_MMA) {
         // ------------------------------------------------ MMA issue
-        // D fp32, A and B fp16 (0) or bf16 (1), M = 128, N = NT; A (and B in WGRAD) contiguous
-        // along M (N)
+        // D fp32, A and B fp16 (0) or bf16 (1), M = 128 (a pair: 256), N = NT; A (and B in WGRAD)
+        // contiguous along M (N)
         const uint32_t idesc = (1u << 4) | (KIND == WGRAD ? (1u << 7) | (1u << 10) : 0u) | (KIND != FWD ? 1u << 15 : 0u) |
-                               (KIND == WGRAD ? 1u << 16 : 0u) | ((uint32_t)(a.NT >> 3) << 17) | (8u << 24);
+                               (KIND == WGRAD ? 1u << 16 : 0u) | ((uint32_t)(a.NT >> 3) << 17) | ((PAIR ? 16u : 8u) << 24);
         // low word: address / 16 | leading offset / 16 (K-major: unused; MN-major: 8192 bytes
         // between the 64-element atoms); a K step of 16 is 32 bytes, or 16 rows of 128
         constexpr uint32_t alead = KIND == FWD ? 1u << 16 : 512u << 16, astep = KIND == FWD ? 2u : 128u;
         constexpr uint32_t blead = KIND == WGRAD ? 512u << 16 : 1u << 16, bstep = KIND == WGRAD ? 128u : 2u;
         const uint32_t sbase = smem_addr(base);
-        if (elect_one()) {
+        if (PAIR && cluster_rank() != 0) {
+            // The second CTA of a pair: the first one's MMAs read its stages too, so it passes on that a
+            // stage is full.
+            if (elect_one()) {
+                int slot = 0, done = 0;
+                uint32_t phase = 0;
+                bool ok = true;
+                for (uint32_t u = first_unit<PAIR>(); u < (uint32_t)a.units && ok; u += unit_step<PAIR>()) {
+                    const Unit un = unit_of<PAIR>(a, u);
+                    for (int kb = un.b0; kb < un.b1; ++kb) {
+                        if (!wait1(&sm->full[slot], phase, sm, a.status)) { ok = false; break; }
+                        arrive_first(&sm->full[slot]);
+                        ++done;
+                        if (++slot == NS) { slot = 0; phase ^= 1u; }
+                    }
+                }
+                // no commit may arrive after the CTA exits
+                for (int i = done > NS ? done - NS : 0; i < done; ++i)
+                    (void)mbar_wait_bounded(&sm->empty[i % NS], (uint32_t)(i / NS) & 1u, a.status);
+            }
+        } else if (elect_one()) {
             int slot = 0, done = 0, n = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (uint32_t u = blockIdx.x; u < (uint32_t)a.units && ok; u += gridDim.x) {
-                const Unit un = unit_of(a, u);
+            for (uint32_t u = first_unit<PAIR>(); u < (uint32_t)a.units && ok; u += unit_step<PAIR>()) {
+                const Unit un = unit_of<PAIR>(a, u);
                 for (int s0 = un.b0; s0 < un.b1 && ok; s0 += a.seg, ++n) {
                     const int s1 = un.b1 - s0 < a.seg ? un.b1 : s0 + a.seg;
                     const int buf = n & 1;
-                    if (!wait1(&sm->acce[buf], ((uint32_t)(n >> 1) & 1u) ^ 1u, sm, a.status)) { ok = false; break; }
+                    if (!wait1<PAIR>(&sm->acce[buf], ((uint32_t)(n >> 1) & 1u) ^ 1u, sm, a.status)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t d = tmem + (uint32_t)(buf * 256);
                     for (int kb = s0; kb < s1; ++kb) {
-                        if (!wait1(&sm->full[slot], phase, sm, a.status)) { ok = false; break; }
+                        if (!wait1<PAIR>(&sm->full[slot], phase, sm, a.status)) { ok = false; break; }
                         tc_fence_after();
                         const uint32_t sa = sbase + (uint32_t)slot * a.stage_bytes;
                         const uint32_t alo = (sa >> 4) | alead, blo = ((sa + A_BYTES) >> 4) | blead;
 #pragma unroll
                         for (int kk = 0; kk < BK / 16; ++kk)
-                            mma(d, alo + kk * astep, blo + kk * bstep, idesc, kb > s0 || kk > 0 ? 1u : 0u);
-                        mma_commit(&sm->empty[slot]);
-                        if (kb + 1 == s1) mma_commit(&sm->accf[buf]);
+                            mma<PAIR>(d, alo + kk * astep, blo + kk * bstep, idesc, kb > s0 || kk > 0 ? 1u : 0u);
+                        mma_commit<PAIR>(&sm->empty[slot]);
+                        if (kb + 1 == s1) mma_commit<PAIR>(&sm->accf[buf]);
                         ++done;
                         if (++slot == NS) { slot = 0; phase ^= 1u; }
                     }
@@ -809,18 +888,19 @@ __global__ void __launch_bounds__((RolesOf<KIND, GRADS>::THREADS), 1) expand_gem
         const int q4 = warp & 3, r = q4 * 32 + lane, rank = warp >> 2;
         const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
         const bool helper = warp < R::EXPAND, shared = a.seg >= a.KB;
-        const uint32_t before = ((uint32_t)a.units - 1u - blockIdx.x) / gridDim.x;  // this CTA's units but the last
+        const uint32_t u0 = first_unit<PAIR>(), step = unit_step<PAIR>();
+        const uint32_t before = ((uint32_t)a.units - 1u - u0) / step;  // this CTA's units but the last
         float *row_pow = sm->row_pow[q4];
         if (KIND != WGRAD) asm volatile("griddepcontrol.wait;" ::: "memory");  // row_pow too
-        uint32_t u = helper ? blockIdx.x + before * gridDim.x : blockIdx.x;
+        uint32_t u = helper ? u0 + before * step : u0;
         if (helper && !shared) u = (uint32_t)a.units;
         int n = helper ? (int)before : 0;
         bool ok = true;
         // A wait that ran out ends this warp's work, but not its way through the tiles: the warps of a
         // quarter meet at barriers that have no time limit of their own.
-        for (; u < (uint32_t)a.units; u += gridDim.x) {
-            const bool last = shared && (uint32_t)a.units - u <= gridDim.x;
-            const Unit un = unit_of(a, u);
+        for (; u < (uint32_t)a.units; u += step) {
+            const bool last = shared && (uint32_t)a.units - u <= step;
+            const Unit un = unit_of<PAIR>(a, u);
             const int64_t left = a.cols - (int64_t)un.tn * a.NT;
             const int ncols = left < a.NT ? (int)left : a.NT;
             const int c0 = 16 * (last ? rank : rank - HELPERS), cstep = 16 * (last ? RANKS : RANKS - HELPERS);
@@ -870,7 +950,12 @@ __global__ void __launch_bounds__((RolesOf<KIND, GRADS>::THREADS), 1) expand_gem
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0 && !helper) mbar_arrive(&sm->acce[buf]);
+                if (lane == 0 && !helper) {
+                    if (PAIR)
+                        arrive_first(&sm->acce[buf]);
+                    else
+                        mbar_arrive(&sm->acce[buf]);
+                }
             }
             if (a.S == 1) continue;
             // the last part of a tile's 32 lanes to arrive adds all parts in order
@@ -921,9 +1006,14 @@ __global__ void __launch_bounds__((RolesOf<KIND, GRADS>::THREADS), 1) expand_gem
 
     tc_fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();  // neither CTA leaves while the other may arrive at its barriers or read its stages
     tc_fence_after();
-    if (warp == R::W_MMA)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    if (warp == R::W_MMA) {
+        if (PAIR)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    }
 }
 
 // ------------------------------------------------------------------ activations as fp16 rows
@@ -1043,8 +1133,9 @@ inline bool shape_ok(int64_t M, int64_t N, int64_t K) {
 }
 
 struct Plan {
-    int64_t Tw, Tn, units;
-    int NT, S, KB, KB0, seg, stages, raws;
+    int64_t Tw, Tn, units;          // pair: Tw counts pairs of tiles
+    bool pair;                      // two CTAs share a tile of columns
+    int NT, box, S, KB, KB0, seg, stages, raws;  // box: columns of B that a CTA holds
     uint32_t stage_bytes;
     size_t bytes;                   // of the workspace, 0 where S is 1
 };
@@ -1052,48 +1143,56 @@ struct Plan {
 // lanes: weight rows per projection (FWD) or columns K; cols: the other side; red: length of the
 // reduction (per source), sources 1 or 2; max_rows: reduction that one accumulator may sum.
 inline Plan make_plan(int kind, int64_t lanes, int64_t cols, int64_t red, int sources, int64_t max_rows, int sms) {
-    Plan p;
-    p.Tw = kind == FWD ? (lanes + 63) / 64 : (lanes + 127) / 128;
-    // WGRAD: 192 columns at most, so that four stages of operands and four of codes fit
-    const int64_t widest = kind == WGRAD ? 192 : 256;
-    p.Tn = (cols + widest - 1) / widest;
-    p.NT = (int)(((cols + p.Tn - 1) / p.Tn + 15) / 16 * 16);
-    p.KB0 = (int)((red + BK - 1) / BK);
-    p.KB = p.KB0 * sources;
-    p.seg = max_rows > 0 && max_rows / BK < p.KB ? (int)(max_rows / BK) : p.KB;
-    const uint32_t bb = kind == WGRAD ? (uint32_t)((p.NT + 63) / 64) * 8192u : (uint32_t)p.NT * 128u;
-    p.stage_bytes = A_BYTES + bb;
-    // A wait tells only neighbouring laps of a ring apart, so each slot's previous lap must be known
-    // to be over when a warp waits for the next one. The codes' ring has a multiple of GROUPS
-    // slots: a slot then belongs to one group, which sees its laps in order. The
-    // operands' ring has GROUPS slots at least: a group that filled stage i - GROUPS waited for
-    // the MMAs of the lap before it, which complete in order.
-    const uint32_t rb = kind == WGRAD ? Raw<WGRAD>::BYTES : Raw<FWD>::BYTES, room = SMEM_MAX - CONTROL - 1024;
-    p.stages = MIN_STAGES;
-    p.raws = GROUPS;
-    while (p.stages < MAX_STAGES && (p.stages + 1) * p.stage_bytes + p.raws * rb <= room) ++p.stages;
-    while (p.raws + GROUPS <= MAX_RAW && p.stages * p.stage_bytes + (p.raws + GROUPS) * rb <= room) p.raws += GROUPS;
-    // Parts of the reduction: the count with the least estimated time, in cycles as measured: a stage
-    // takes its MMAs (2.1 a column) or the hand-over between the warps (470), a unit 7000 to start and
-    // end; the last part of a tile reads two partial sums of 16 columns in 1300 cycles, five groups of
-    // columns at a time, after 1500 for the count.
-    const int64_t tiles = p.Tw * p.Tn;
-    double best = 0;
-    p.S = 1;
-    for (int S = 1; S <= 32 && (S == 1 || S * 4 <= p.KB); ++S) {
-        if (S > 1 && (tiles * S > 8 * (int64_t)sms || tiles > MAX_SPLIT_TILES)) break;
-        const int64_t waves = (tiles * S + sms - 1) / sms;
-        const double stage = p.NT * 2.1 > 470 ? p.NT * 2.1 : 470;
-        const double join = S > 1 ? 1500.0 + 1300.0 * ((p.NT + 79) / 80) * ((S + 1) / 2) : 0.0;
-        const double t = (double)waves * ((double)((p.KB + S - 1) / S) * stage + 7000) + join;
-        if (S == 1 || t < best) {
-            best = t;
-            p.S = S;
+    const int64_t Tw = kind == FWD ? (lanes + 63) / 64 : (lanes + 127) / 128;
+    Plan best = {};
+    double least = 0;
+    for (int pair = 0; pair < 2; ++pair) {
+        if (pair && (Tw < 2 || cols <= 64 || sms < 2)) continue;
+        Plan p;
+        p.pair = pair != 0;
+        p.Tw = pair ? (Tw + 1) / 2 : Tw;
+        // a CTA of WGRAD holds 192 columns at most, so that four stages of operands and four of codes fit
+        const int64_t widest = kind == WGRAD && !pair ? 192 : 256, unit = pair ? 32 : 16;
+        p.Tn = (cols + widest - 1) / widest;
+        p.NT = (int)(((cols + p.Tn - 1) / p.Tn + unit - 1) / unit * unit);
+        p.KB0 = (int)((red + BK - 1) / BK);
+        p.KB = p.KB0 * sources;
+        p.seg = max_rows > 0 && max_rows / BK < p.KB ? (int)(max_rows / BK) : p.KB;
+        p.box = pair ? p.NT / 2 : p.NT;
+        const uint32_t bb = kind == WGRAD ? (uint32_t)((p.box + 63) / 64) * 8192u : (uint32_t)p.box * 128u;
+        p.stage_bytes = A_BYTES + bb;
+        // A wait tells only neighbouring laps of a ring apart, so each slot's previous lap must be known
+        // to be over when a warp waits for the next one. The codes' ring has a multiple of GROUPS
+        // slots: a slot then belongs to one group, which sees its laps in order. The
+        // operands' ring has GROUPS slots at least: a group that filled stage i - GROUPS waited for
+        // the MMAs of the lap before it, which complete in order.
+        const uint32_t rb = kind == WGRAD ? Raw<WGRAD>::BYTES : Raw<FWD>::BYTES, room = SMEM_MAX - CONTROL - 1024;
+        p.stages = MIN_STAGES;
+        p.raws = GROUPS;
+        while (p.stages < MAX_STAGES && (p.stages + 1) * p.stage_bytes + p.raws * rb <= room) ++p.stages;
+        while (p.raws + GROUPS <= MAX_RAW && p.stages * p.stage_bytes + (p.raws + GROUPS) * rb <= room) p.raws += GROUPS;
+        // One CTA or two, and parts of the reduction: what has the least estimated time, in cycles as
+        // measured. A stage takes the shared memory's traffic (the codes, A and the scales, and two passes
+        // of B, which a pair divides) or its MMAs; a unit takes 7000 to start and end; the last part of a
+        // tile reads two partial sums of 16 columns in 1300 cycles, five groups of columns at a time,
+        // after 1500 for the count.
+        const int64_t tiles = p.Tw * p.Tn, workers = pair ? sms / 2 : sms;
+        const double mem = 430 + 1.9 * p.box, mma = 2.1 * p.NT, stage = mem > mma ? mem : mma;
+        for (int S = 1; S <= 32 && (S == 1 || S * 4 <= p.KB); ++S) {
+            if (S > 1 && (tiles * S > 8 * workers || tiles * (pair + 1) > MAX_SPLIT_TILES)) break;
+            const int64_t waves = (tiles * S + workers - 1) / workers;
+            const double join = S > 1 ? 1500.0 + 1300.0 * ((p.NT + 79) / 80) * ((S + 1) / 2) : 0.0;
+            const double t = (double)waves * ((double)((p.KB + S - 1) / S) * stage + 7000) + join;
+            if (least == 0 || t < least) {
+                least = t;
+                p.S = S;
+                p.units = tiles * S;
+                p.bytes = S > 1 ? CNT_BYTES + (size_t)p.units * (pair + 1) * p.NT * 512 : 0;
+                best = p;
+            }
         }
     }
-    p.units = tiles * p.S;
-    p.bytes = p.S > 1 ? CNT_BYTES + (size_t)p.units * p.NT * 512 : 0;
-    return p;
+    return best;
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -1154,17 +1253,21 @@ template <typename F> bool allow_smem(F *kernel, int bytes, std::atomic<uint64_t
 // Launch that may start while the kernel before it on the stream is finishing (programmatic
 // dependent launch).
 template <typename... P, typename... A>
-w4_status launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream, A &&...args) {
+w4_status launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream, int behind,
+                        int cluster, A &&...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[0].val.programmaticStreamSerializationAllowed = behind;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, kernel, P(args)...) != cudaSuccess) return W4_ERR_CUDA;
     return launch_status();
 }
@@ -1175,8 +1278,8 @@ w4_status launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads, s
 inline w4_status launch_prep(const Prep &p, bool behind, cudaStream_t stream) {
     const unsigned grid = (unsigned)(p.M < (1 << 20) ? p.M : (1 << 20));
     if (behind)
-        return p.x8 ? launch_behind(row_prep_kernel<true>, grid, 256, 0, stream, p)
-                    : launch_behind(row_prep_kernel<false>, grid, 256, 0, stream, p);
+        return p.x8 ? launch_behind(row_prep_kernel<true>, grid, 256, 0, stream, 1, 1, p)
+                    : launch_behind(row_prep_kernel<false>, grid, 256, 0, stream, 1, 1, p);
     if (p.x8)
         row_prep_kernel<true><<<grid, 256, 0, stream>>>(p);
     else
@@ -1213,15 +1316,19 @@ w4_status launch(const Plan &p, Maps &tm, Args a, void *workspace, int sms, cuda
     a.status = device_status_ptr();
     if (!a.status) return W4_ERR_CUDA;
     const int smem = (int)(p.stages * p.stage_bytes + p.raws * Raw<KIND>::BYTES + CONTROL) + 1024;
-    static std::atomic<uint64_t> attr_done{0};
-    if (!allow_smem(expand_gemm_kernel<KIND, GRADS, GELU>, (int)SMEM_MAX, attr_done)) return W4_ERR_CUDA;
-    const unsigned grid = (unsigned)(p.units < sms ? p.units : sms);
+    static std::atomic<uint64_t> attr_done{0}, pair_done{0};
+    const int cluster = p.pair ? 2 : 1;
+    const int64_t most = sms / cluster;
+    const unsigned grid = (unsigned)((p.units < most ? p.units : most) * cluster), threads = RolesOf<KIND, GRADS>::THREADS;
     // FWD and DGRAD follow row_prep_kernel: they may start, and read weights, while it finishes.
     // Whatever came before on the stream was complete when it began.
-    if (KIND != WGRAD)
-        return launch_behind(expand_gemm_kernel<KIND, GRADS, GELU>, grid, RolesOf<KIND, GRADS>::THREADS, (size_t)smem, stream, tm, a);
-    expand_gemm_kernel<KIND, GRADS, GELU><<<grid, RolesOf<KIND, GRADS>::THREADS, smem, stream>>>(tm, a);
-    return launch_status();
+    const int behind = KIND != WGRAD;
+    if (p.pair) {
+        if (!allow_smem(expand_gemm_kernel<KIND, GRADS, GELU, true>, (int)SMEM_MAX, pair_done)) return W4_ERR_CUDA;
+        return launch_behind(expand_gemm_kernel<KIND, GRADS, GELU, true>, grid, threads, (size_t)smem, stream, behind, 2, tm, a);
+    }
+    if (!allow_smem(expand_gemm_kernel<KIND, GRADS, GELU, false>, (int)SMEM_MAX, attr_done)) return W4_ERR_CUDA;
+    return launch_behind(expand_gemm_kernel<KIND, GRADS, GELU, false>, grid, threads, (size_t)smem, stream, behind, 1, tm, a);
 }
 
 }  // namespace xg

@@ -484,7 +484,7 @@ template <int GB> w4_status launch_few(const FewArgs &a, cudaStream_t stream) {
         bytes_prep_kernel<GB><<<(unsigned)((warps + 3) / 4), 128, 0, stream>>>(a);
         const w4_status st = launch_status();
         return st != W4_OK ? st : xg::launch_behind(gated_bytes_kernel<GB>, grid, B_WARPS * 32,
-                                                    (size_t)(B_WARPS * AHEAD * BLOCK_BYTES) + scales, stream, a);
+                                                    (size_t)(B_WARPS * AHEAD * BLOCK_BYTES) + scales, stream, 1, 1, a);
     }
     if (a.M <= 8)
         gated_few_kernel<GB, 1><<<grid, WARPS * 32, scales, stream>>>(a);
@@ -568,7 +568,7 @@ W4_API w4_status w4a16_gated(const void *X_bf16, int64_t M, const uint8_t *codes
     if (!workspace || workspace_bytes < q.end) return W4_ERR_WORKSPACE;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     xg::Maps tm;
-    if (!xg::make_map(&tm.b[0], ws + q.y, M, K, p.NT)) return W4_ERR_CUDA;
+    if (!xg::make_map(&tm.b[0], ws + q.y, M, K, p.box)) return W4_ERR_CUDA;
     tm.b[1] = tm.b[0];
     xg::Prep prep = {};
     prep.x[0] = static_cast<const __nv_bfloat16 *>(X_bf16);
@@ -663,7 +663,7 @@ W4_API w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const 
     a.out = dG_bf16;
     a.out2 = static_cast<__nv_bfloat16 *>(dU_bf16);
     a.row_pow = prep.row_pow;
-    if (!xg::make_map(&tm.b[0], prep.y[0], M, K, l.grads.NT)) return W4_ERR_CUDA;
+    if (!xg::make_map(&tm.b[0], prep.y[0], M, K, l.grads.box)) return W4_ERR_CUDA;
     tm.b[1] = tm.b[0];
     st = act == W4_ACT_SILU ? xg::launch<xg::FWD, true, false>(l.grads, tm, a, workspace, sms, stream)
                             : xg::launch<xg::FWD, true, true>(l.grads, tm, a, workspace, sms, stream);
@@ -677,7 +677,7 @@ W4_API w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const 
     prep.pairs = 0;
     st = xg::launch_prep(prep, true, stream);
     if (st != W4_OK) return st;
-    if (!xg::make_map(&tm.b[0], prep.y[0], M, H, l.dx.NT) || !xg::make_map(&tm.b[1], prep.y[1], M, H, l.dx.NT))
+    if (!xg::make_map(&tm.b[0], prep.y[0], M, H, l.dx.box) || !xg::make_map(&tm.b[1], prep.y[1], M, H, l.dx.box))
         return W4_ERR_CUDA;
     a.dh = nullptr;
     a.out = dX_bf16;
@@ -706,7 +706,7 @@ W4_API w4_status w4a16_dgrad(const void *dY_bf16, int64_t M, const uint8_t *code
     if (!workspace || workspace_bytes < q.end) return W4_ERR_WORKSPACE;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     xg::Maps tm;
-    if (!xg::make_map(&tm.b[0], ws + q.y, M, N, p.NT)) return W4_ERR_CUDA;
+    if (!xg::make_map(&tm.b[0], ws + q.y, M, N, p.box)) return W4_ERR_CUDA;
     tm.b[1] = tm.b[0];
     xg::Prep prep = {};
     prep.x[0] = static_cast<const __nv_bfloat16 *>(dY_bf16);
