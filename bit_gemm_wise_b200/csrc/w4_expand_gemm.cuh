@@ -24,10 +24,17 @@
 //   one each     loads B by TMA; issues the MMAs (M = 128, N = the token tile, K = 16); loads the codes
 //                by TMA, into a ring of their own.
 // Lanes are weights and columns are tokens: a small batch takes a small N and the MMAs shrink with
-// it, while the expansion is shared by all tokens of a tile. What bounds a stage is the instructions
-// that the SM issues for it (about 1900 at first: 1.0 us a stage, twice its MMAs): the codes' pairs
-// (i, i + 4) of eight stay in that order, and B's rows (FWD) or the results' lanes (DGRAD, WGRAD)
-// are permuted instead; a thread's scale addresses move by one addition.
+// it, while the expansion is shared by all tokens of a tile. What bounds a stage is the shared memory's
+// data path: codes in and out, A in and out and B twice, 128 bytes a cycle, came to 1060 (FWD), 980
+// (DGRAD) and 900 (WGRAD) cycles of its 990, 900 and 840 at N = 256 (192), against 512 (384) of MMAs.
+// So where there are more than 64 columns, two CTAs make a pair: one MMA of both SMs (M = 256) on
+// 128 lanes of each, every SM holding half of B, which it writes and reads half as often (DGRAD 727
+// cycles a stage). The first CTA of a pair issues the MMAs; the second one passes on that its stages
+// are full. Beyond that, instructions count: the codes' pairs (i, i + 4) of eight stay in that order, and
+// B's rows (FWD) or the results' lanes (DGRAD, WGRAD) are permuted instead; a thread's scale
+// addresses move by one addition. (Not kept: a table of FWD's scales made beforehand, side by side for a
+// stage, which loads them in a tenth of the accesses: no faster, and small calls pay for it; tiles
+// ordered so that neighbours share their codes in L2: no faster.)
 //
 // Where the tiles are too few for the SMs, the reduction is cut into S parts: each part's fp32 sums
 // go to the workspace and the last part to finish adds them in order, so results do not depend on
@@ -49,9 +56,9 @@ constexpr int GROUPS = 4;                     // of expansion warps; stage i is 
 
 // How a CTA's warps are divided. Sixteen expansion warps and four for the results leave a thread 80
 // registers; where the results take long (two gradients and dH for each pair of accumulators; tiles of
-// few stages), eight and eight do better. Measured with the two ways in turn, us: prefill 4096 x 15360 x
-// 3840 822 and 853, dgrad 4096 x 4096 x 14336 407 and 429; the gradients of 2048 x 14336 x 4096 with
-// their dX 1126 and 1065, wgrad 2048 x 4096 x 4096 91 and 87.
+// few stages), eight and eight do better. Measured with the two ways in turn, one CTA a tile, us: prefill
+// 4096 x 15360 x 3840 822 and 853, dgrad 4096 x 4096 x 14336 407 and 429; the gradients of 2048 x 14336 x
+// 4096 with their dX 1126 and 1065, wgrad 2048 x 4096 x 4096 91 and 87.
 template <bool LONG_RESULTS> struct Roles {
     static constexpr int EXPAND = LONG_RESULTS ? 8 : 16, OUT = LONG_RESULTS ? 8 : 4;
     static constexpr int WPG = EXPAND / GROUPS;     // expansion warps per group
@@ -167,7 +174,9 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// arrives at the first CTA's barrier of that place
+// Arrives at the first CTA's barrier of that place. The order is that within this CTA: what the arrival
+// passes on, its own SM reads (the tensor core its shared memory, of which the writers' proxy fences
+// came before) or has read (its TMEM). Release at cluster scope cost 900 cycles a stage.
 __device__ __forceinline__ void arrive_first(uint64_t *bar) {
     asm volatile(
         "{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %0, 0;\n mbarrier.arrive.shared::cluster.b64 _, [r];\n}\n" ::"r"(
@@ -1141,8 +1150,10 @@ struct Plan {
 };
 
 // lanes: weight rows per projection (FWD) or columns K; cols: the other side; red: length of the
-// reduction (per source), sources 1 or 2; max_rows: reduction that one accumulator may sum.
-inline Plan make_plan(int kind, int64_t lanes, int64_t cols, int64_t red, int sources, int64_t max_rows, int sms) {
+// reduction (per source), sources 1 or 2; max_rows: reduction that one accumulator may sum; grads: FWD
+// with the gradients.
+inline Plan make_plan(int kind, int64_t lanes, int64_t cols, int64_t red, int sources, int64_t max_rows, int sms,
+                      bool grads = false) {
     const int64_t Tw = kind == FWD ? (lanes + 63) / 64 : (lanes + 127) / 128;
     Plan best = {};
     double least = 0;
@@ -1169,11 +1180,19 @@ inline Plan make_plan(int kind, int64_t lanes, int64_t cols, int64_t red, int so
         const uint32_t rb = kind == WGRAD ? Raw<WGRAD>::BYTES : Raw<FWD>::BYTES, room = SMEM_MAX - CONTROL - 1024;
         p.stages = MIN_STAGES;
         p.raws = GROUPS;
-        while (p.stages < MAX_STAGES && (p.stages + 1) * p.stage_bytes + p.raws * rb <= room) ++p.stages;
-        while (p.raws + GROUPS <= MAX_RAW && p.stages * p.stage_bytes + (p.raws + GROUPS) * rb <= room) p.raws += GROUPS;
+        const auto grow = [&](int stages, int raws) {  // as far as both fit
+            while (p.raws + GROUPS <= raws && p.stages * p.stage_bytes + (p.raws + GROUPS) * rb <= room) p.raws += GROUPS;
+            while (p.stages < stages && (p.stages + 1) * p.stage_bytes + p.raws * rb <= room) ++p.stages;
+        };
+        // Codes come from HBM or a far L2 slice, and a group has one slot in four. Y's, in rows of 32 bytes,
+        // take longest (us with 16 slots and 4 stages, and with 12 and 5: 1024 x 14336 x 4096 230 and 240;
+        // the gradients of 2048 x 14336 x 4096 with their dX, whose expansion is slower, 980 and 956).
+        if (kind == FWD && !grads) grow(MIN_STAGES, MAX_RAW);
+        grow(MIN_STAGES + 1, 2 * GROUPS);
+        grow(MAX_STAGES, MAX_RAW);
         // One CTA or two, and parts of the reduction: what has the least estimated time, in cycles as
         // measured. A stage takes the shared memory's traffic (the codes, A and the scales, and two passes
-        // of B, which a pair divides) or its MMAs; a unit takes 7000 to start and end; the last part of a
+        // of B, which a pair divides) or its MMAs; a unit takes 7000 to start and end, 8500 in a pair; the last part of a
         // tile reads two partial sums of 16 columns in 1300 cycles, five groups of columns at a time,
         // after 1500 for the count.
         const int64_t tiles = p.Tw * p.Tn, workers = pair ? sms / 2 : sms;
@@ -1182,7 +1201,7 @@ inline Plan make_plan(int kind, int64_t lanes, int64_t cols, int64_t red, int so
             if (S > 1 && (tiles * S > 8 * workers || tiles * (pair + 1) > MAX_SPLIT_TILES)) break;
             const int64_t waves = (tiles * S + workers - 1) / workers;
             const double join = S > 1 ? 1500.0 + 1300.0 * ((p.NT + 79) / 80) * ((S + 1) / 2) : 0.0;
-            const double t = (double)waves * ((double)((p.KB + S - 1) / S) * stage + 7000) + join;
+            const double t = (double)waves * ((double)((p.KB + S - 1) / S) * stage + (pair ? 8500 : 7000)) + join;
             if (least == 0 || t < least) {
                 least = t;
                 p.S = S;

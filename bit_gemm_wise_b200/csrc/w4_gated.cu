@@ -603,7 +603,7 @@ struct BwdLayout {
 };
 BwdLayout bwd_layout(int64_t M, int64_t H, int64_t K, int sms) {
     BwdLayout l;
-    l.grads = xg::make_plan(xg::FWD, H, M, K, 1, 0, sms);
+    l.grads = xg::make_plan(xg::FWD, H, M, K, 1, 0, sms, true);
     l.dx = xg::make_plan(xg::DGRAD, K, M, H, 2, 0, sms);
     l.q = xg::place_prep(l.grads.bytes > l.dx.bytes ? l.grads.bytes : l.dx.bytes, M * (K > 2 * H ? K : 2 * H), M);
     return l;
