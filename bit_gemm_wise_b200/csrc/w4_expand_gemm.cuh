@@ -28,7 +28,7 @@
 // data path: codes in and out, A in and out and B twice, 128 bytes a cycle, came to 1060 (FWD), 980
 // (DGRAD) and 900 (WGRAD) cycles of its 990, 900 and 840 at N = 256 (192), against 512 (384) of MMAs.
 // So where there are more than 64 columns, two CTAs make a pair: one MMA of both SMs (M = 256) on
-// 128 lanes of each, every SM holding half of B, which it writes and reads half as often (DGRAD 727
+// 128 lanes of each, every SM holding half of B, which it writes and reads half as often (DGRAD 714
 // cycles a stage). The first CTA of a pair issues the MMAs; the second one passes on that its stages
 // are full. Beyond that, instructions count: the codes' pairs (i, i + 4) of eight stay in that order, and
 // B's rows (FWD) or the results' lanes (DGRAD, WGRAD) are permuted instead; a thread's scale
@@ -1188,6 +1188,7 @@ inline Plan make_plan(int kind, int64_t lanes, int64_t cols, int64_t red, int so
         // take longest (us with 16 slots and 4 stages, and with 12 and 5: 1024 x 14336 x 4096 230 and 240;
         // the gradients of 2048 x 14336 x 4096 with their dX, whose expansion is slower, 980 and 956).
         if (kind == FWD && !grads) grow(MIN_STAGES, MAX_RAW);
+        grow(MIN_STAGES + 1, GROUPS);
         grow(MIN_STAGES + 1, 2 * GROUPS);
         grow(MAX_STAGES, MAX_RAW);
         // One CTA or two, and parts of the reduction: what has the least estimated time, in cycles as
