@@ -76,7 +76,7 @@ def test_save_blocks_are_independent():
     assert xs[1, 1] == 255 and xs[2, 0] == 255 and xs[3, 2] == 255 and int((xs == 255).sum()) == 3
 
 
-WGRAD = [(1, 8, 32), (5, 16, 96), (64, 8, 160), (130, 72, 320), (257, 264, 1056), (1000, 16, 4096), (1000, 512, 768), (300, 1000, 288)]
+WGRAD = [(1, 8, 32), (5, 16, 96), (64, 8, 160), (130, 72, 320), (257, 264, 1056), (1000, 16, 4096), (1000, 512, 768), (300, 1000, 288), (900, 520, 1056)]
 
 
 @pytest.mark.parametrize("fp32", [False, True])

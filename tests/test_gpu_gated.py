@@ -324,6 +324,27 @@ def test_offsets_past_32_bits():
         assert R.rel(dx[sl], dy[sl].double() @ R.dequant(w, g)) <= 2.6e-3
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("M,H,K,group,mode", [(250, 264, 2112, 64, "asym"), (700, 328, 1088, 32, "sym"), (1100, 72, 4096, 128, "asym")])
+def test_two_ctas_a_tile(M, H, K, group, mode, act):
+    """Columns and reductions long enough for pairs of CTAs, with an odd count of lane tiles, ragged
+    columns and both whole and split reductions, in every product."""
+    wg, wu = weights(H, K, group, mode, M)
+    x, dh = R.rows(M, K, 1, DEV, outliers=4), R.rows(M, H, 2, DEV, std=0.01)
+    check_gated(x, wg, wu, group, mode, act)
+    got = run_bwd(dh, wg, wu, group, mode, act, X=x)
+    status_ok()
+    check_bwd(got, x, dh, wg, wu, group, act)
+    n = K // 8 * 8
+    w = R.weight(n, 3 * group * 11, group, mode, 5, DEV)
+    dy = R.rows(M, n, 5, DEV, std=0.01)
+    dx = run_dgrad(dy, w, group, mode)
+    status_ok()
+    a = R.dequant(w, group)
+    ref = dy.double() @ a
+    near(dx, ref, (2.0 ** -11 + 2.0 ** -12) * (dy.double().abs() @ a.abs()) + R.HALF * ref.abs() + 1e-30, 2.6e-3)
+
+
 def test_results_do_not_change_from_run_to_run_and_workspaces_serve_again():
     """One workspace of the largest need over several shapes, each twice: the same bits."""
     shapes = [(40, 64, 4096, 128), (300, 64, 2048, 128), (1, 8192, 4096, 128), (17, 200, 8192, 128)]
