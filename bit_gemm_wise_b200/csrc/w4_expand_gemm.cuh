@@ -27,7 +27,7 @@
 // it, while the expansion is shared by all tokens of a tile. What bounds a stage is the shared memory's
 // data path: codes in and out, A in and out and B twice, 128 bytes a cycle, came to 1060 (FWD), 980
 // (DGRAD) and 900 (WGRAD) cycles of its 990, 900 and 840 at N = 256 (192), against 512 (384) of MMAs.
-// So where there are more than 64 columns, two CTAs make a pair: one MMA of both SMs (M = 256) on
+// So where there are more than 128 columns, two CTAs make a pair: one MMA of both SMs (M = 256) on
 // 128 lanes of each, every SM holding half of B, which it writes and reads half as often (DGRAD 714
 // cycles a stage). The first CTA of a pair issues the MMAs; the second one passes on that its stages
 // are full. Beyond that, instructions count: the codes' pairs (i, i + 4) of eight stay in that order, and
@@ -58,7 +58,9 @@ constexpr int GROUPS = 4;                     // of expansion warps; stage i is 
 // registers; where the results take long (two gradients and dH for each pair of accumulators; tiles of
 // few stages), eight and eight do better. Measured with the two ways in turn, one CTA a tile, us: prefill
 // 4096 x 15360 x 3840 822 and 853, dgrad 4096 x 4096 x 14336 407 and 429; the gradients of 2048 x 14336 x
-// 4096 with their dX 1126 and 1065, wgrad 2048 x 4096 x 4096 91 and 87.
+// 4096 with their dX 1126 and 1065, wgrad 2048 x 4096 x 4096 91 and 87. In pairs of CTAs, whose stages are
+// shorter, the gelu of prefill counts as long too (911 and 829), silu does not (4096 x 14336 x 4096 879 and
+// 858, but 512 x 4096 x 4096 in groups of 32 43.0 and 45.3).
 template <bool LONG_RESULTS> struct Roles {
     static constexpr int EXPAND = LONG_RESULTS ? 8 : 16, OUT = LONG_RESULTS ? 8 : 4;
     static constexpr int WPG = EXPAND / GROUPS;     // expansion warps per group
@@ -69,7 +71,7 @@ template <bool LONG_RESULTS> struct Roles {
     static constexpr int RANKS = W_B / 4, HELPERS = EXPAND / 4;  // warps of a quarter of the lanes; of them, expansion
     static_assert(EXPAND % 4 == 0 && OUT % 4 == 0 && TPG >= 64 && TPG <= 128, "warp roles");
 };
-template <int KIND, bool GRADS> using RolesOf = Roles<KIND == 2 || GRADS>;
+template <int KIND, bool GRADS, bool GELU, bool PAIR> using RolesOf = Roles<KIND == 2 || GRADS || (GELU && PAIR)>;
 
 constexpr int BK = 64;                        // reduction per stage
 constexpr uint32_t A_BYTES = 128 * BK * 2;    // an expanded stage
@@ -680,9 +682,9 @@ __device__ __forceinline__ void emit(const Args &a, const float *row_pow, const 
 }
 
 template <int KIND, bool GRADS, bool GELU, bool PAIR>
-__global__ void __launch_bounds__((RolesOf<KIND, GRADS>::THREADS), 1) expand_gemm_kernel(const __grid_constant__ Maps tm,
+__global__ void __launch_bounds__((RolesOf<KIND, GRADS, GELU, PAIR>::THREADS), 1) expand_gemm_kernel(const __grid_constant__ Maps tm,
                                                                                        const __grid_constant__ Args a) {
-    using R = RolesOf<KIND, GRADS>;
+    using R = RolesOf<KIND, GRADS, GELU, PAIR>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *raw = base + (size_t)a.stages * a.stage_bytes;
@@ -1158,7 +1160,7 @@ inline Plan make_plan(int kind, int64_t lanes, int64_t cols, int64_t red, int so
     Plan best = {};
     double least = 0;
     for (int pair = 0; pair < 2; ++pair) {
-        if (pair && (Tw < 2 || cols <= 64 || sms < 2)) continue;
+        if (pair && (Tw < 2 || cols <= 128 || sms < 2)) continue;
         Plan p;
         p.pair = pair != 0;
         p.Tw = pair ? (Tw + 1) / 2 : Tw;
@@ -1191,7 +1193,8 @@ inline Plan make_plan(int kind, int64_t lanes, int64_t cols, int64_t red, int so
         grow(MIN_STAGES + 1, GROUPS);
         grow(MIN_STAGES + 1, 2 * GROUPS);
         grow(MAX_STAGES, MAX_RAW);
-        // One CTA or two, and parts of the reduction: what has the least estimated time, in cycles as
+        // One CTA or two (more than 128 columns: 77 x 5632 x 2048 takes 16.6 us in pairs, 16.0 without), and
+        // parts of the reduction: what has the least estimated time, in cycles as
         // measured. A stage takes the shared memory's traffic (the codes, A and the scales, and two passes
         // of B, which a pair divides) or its MMAs; a unit takes 7000 to start and end, 8500 in a pair; the last part of a
         // tile reads two partial sums of 16 columns in 1300 cycles, five groups of columns at a time,
@@ -1339,16 +1342,16 @@ w4_status launch(const Plan &p, Maps &tm, Args a, void *workspace, int sms, cuda
     static std::atomic<uint64_t> attr_done{0}, pair_done{0};
     const int cluster = p.pair ? 2 : 1;
     const int64_t most = sms / cluster;
-    const unsigned grid = (unsigned)((p.units < most ? p.units : most) * cluster), threads = RolesOf<KIND, GRADS>::THREADS;
+    const unsigned grid = (unsigned)((p.units < most ? p.units : most) * cluster);
     // FWD and DGRAD follow row_prep_kernel: they may start, and read weights, while it finishes.
     // Whatever came before on the stream was complete when it began.
     const int behind = KIND != WGRAD;
     if (p.pair) {
         if (!allow_smem(expand_gemm_kernel<KIND, GRADS, GELU, true>, (int)SMEM_MAX, pair_done)) return W4_ERR_CUDA;
-        return launch_behind(expand_gemm_kernel<KIND, GRADS, GELU, true>, grid, threads, (size_t)smem, stream, behind, 2, tm, a);
+        return launch_behind(expand_gemm_kernel<KIND, GRADS, GELU, true>, grid, RolesOf<KIND, GRADS, GELU, true>::THREADS, (size_t)smem, stream, behind, 2, tm, a);
     }
     if (!allow_smem(expand_gemm_kernel<KIND, GRADS, GELU, false>, (int)SMEM_MAX, attr_done)) return W4_ERR_CUDA;
-    return launch_behind(expand_gemm_kernel<KIND, GRADS, GELU, false>, grid, threads, (size_t)smem, stream, behind, 1, tm, a);
+    return launch_behind(expand_gemm_kernel<KIND, GRADS, GELU, false>, grid, RolesOf<KIND, GRADS, GELU, false>::THREADS, (size_t)smem, stream, behind, 1, tm, a);
 }
 
 }  // namespace xg
