@@ -139,16 +139,10 @@ W4_API w4_status fp8_ckpt_load(const uint8_t *X_e4m3, const uint8_t *X_scale, in
     return launch_status();
 }
 
-// fp32 sums of the tensor cores truncate: against a 64-bit product, bf16 operands of N(0, 1) gave a
-// relative error of 4e-7 over 910 rows, 2e-6 over 2048 and 9e-6 over 8192. An fp32 gradient is
-// therefore added up outside them every 2048 rows; a bf16 one rounds far above that.
-static xg::Plan wgrad_plan(int64_t M, int64_t N, int64_t K, bool fp32, int sms) {
-    return xg::make_plan(xg::WGRAD, K, N, M, 1, fp32 ? 2048 : 0, sms);
-}
-
 W4_API size_t fp8_ckpt_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     if (!xg::shape_ok(M, N, K) || N % 8 != 0) return 0;
-    return wgrad_plan(M, N, K, false, num_sms()).bytes;
+    // results in fp32 ask for no more: their plan differs only in where long sums are added up
+    return xg::make_plan(xg::WGRAD, K, N, M, 1, num_sms()).bytes;
 }
 
 W4_API w4_status fp8_ckpt_wgrad(const void *dY_bf16, const uint8_t *X_e4m3, const uint8_t *X_scale, int64_t M, int64_t N,
@@ -161,7 +155,7 @@ W4_API w4_status fp8_ckpt_wgrad(const void *dY_bf16, const uint8_t *X_e4m3, cons
         if (p && !aligned16(p)) return W4_ERR_ALIGN;
     const int sms = num_sms();
     const bool fp32 = (flags & W4_OUT_FP32) != 0;
-    const xg::Plan p = wgrad_plan(M, N, K, fp32, sms);
+    const xg::Plan p = xg::make_plan(xg::WGRAD, K, N, M, 1, sms, false, fp32);
     if (p.bytes && (!workspace || workspace_bytes < p.bytes)) return W4_ERR_WORKSPACE;
     xg::Maps tm;
     if (!xg::make_map(&tm.b[0], dY_bf16, M, N, xg::BK)) return W4_ERR_CUDA;

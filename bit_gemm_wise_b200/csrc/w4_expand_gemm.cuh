@@ -118,7 +118,7 @@ struct Args {
     void *out;                // FWD: Y or dG [cols, rows]; DGRAD: dX [cols, K]; WGRAD: dW [cols, K]
     __nv_bfloat16 *out2;      // FWD with dh: dU
     const float *row_pow;     // FWD, DGRAD: the power of two that each token's row was divided by
-    float *part;              // partial sums [tile][part][column / 4][lane][4]
+    float *part;              // partial sums [tile][part][column / 4][lane][4]; carry: of a CTA's tile, [CTA]
     uint32_t *cnt;            // arrival counters [tile][4], zero between calls
     int *status;
     int64_t rows;             // weight rows (FWD, DGRAD: of one source) or tokens (WGRAD)
@@ -128,11 +128,13 @@ struct Args {
     int Tw, S;                // lane tiles, parts of the reduction
     int KB, KB0;              // stages of the whole reduction, and of the first source
     int part_kb, part_more;   // stages of a part, and how many parts have one more
-    int seg;                  // stages that one fp32 accumulator sums at most
+    int seg;                  // stages that one fp32 accumulator sums at most (KB: a whole unit's)
     int NT;                   // columns per tile, a multiple of 16
     int stages, raws;         // of the expanded operands and of the codes
     uint32_t stage_bytes;
     int gshift, asym, out_fp32;
+    int joined;               // results come from `part`: S > 1, or
+    int carry;                // S is 1, and a tile's several accumulators are added up there
 };
 
 // tensor maps: B (DGRAD: of one or two sources) and the codes of A (FWD: gate, up)
@@ -894,7 +896,7 @@ __global__ void __launch_bounds__((RolesOf<KIND, GRADS, GELU, PAIR>::THREADS), 1
         // ------------------------------------------------ results (lane 32 q4 + lane of the tile), 16
         // columns at a time, in turn by the warps of a quarter: the two result warps; and, in the CTA's
         // last tile, which has nothing behind it to overlap with, the expansion warps too, whose work is
-        // done. Where a tile is summed up in several accumulators, they do not.
+        // done. Where a unit is summed up in several accumulators, they do not.
         constexpr int RANKS = R::RANKS, HELPERS = R::HELPERS;
         const int q4 = warp & 3, r = q4 * 32 + lane, rank = warp >> 2;
         const uint32_t tl = tmem + ((uint32_t)(q4 * 32) << 16);
@@ -918,7 +920,8 @@ __global__ void __launch_bounds__((RolesOf<KIND, GRADS, GELU, PAIR>::THREADS), 1
             // the warps of this quarter that take part meet at a barrier of their own
             auto meet = [&] { named_bar_sync(last ? 1 + q4 : 5 + q4, 32 * (last ? RANKS : RANKS - HELPERS)); };
             // partial sums: [column / 4][lane][4 columns]
-            float4 *part = reinterpret_cast<float4 *>(a.part) + ((size_t)un.tile * a.S + un.s) * (a.NT * 32) + r;
+            const uint32_t place = a.carry ? blockIdx.x : un.tile;
+            float4 *part = reinterpret_cast<float4 *>(a.part) + ((size_t)place * a.S + un.s) * (a.NT * 32) + r;
             // Also what keeps the helpers from the last tile's accumulator until the result warps have
             // finished the tile before it: a helper sees only the parity of that accumulator's phase, which
             // two tiles back had the same.
@@ -942,7 +945,7 @@ __global__ void __launch_bounds__((RolesOf<KIND, GRADS, GELU, PAIR>::THREADS), 1
                     float v[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(raw16[i]);
-                    if (a.S > 1) {
+                    if (a.joined) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             float4 f = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
@@ -968,16 +971,16 @@ __global__ void __launch_bounds__((RolesOf<KIND, GRADS, GELU, PAIR>::THREADS), 1
                         mbar_arrive(&sm->acce[buf]);
                 }
             }
-            if (a.S == 1) continue;
+            if (!a.joined) continue;
             // the last part of a tile's 32 lanes to arrive adds all parts in order
-            uint32_t *cnt = a.cnt + (size_t)un.tile * 4 + q4;
+            uint32_t *cnt = a.cnt + (size_t)place * 4 + q4;
             __threadfence();
             meet();
             if (rank == HELPERS && lane == 0) sm->arrived[q4] = atomicAdd(cnt, 1u);
             meet();
             if (sm->arrived[q4] != (uint32_t)(a.S - 1) || !ok) continue;
             __threadfence();
-            const float4 *p0 = reinterpret_cast<const float4 *>(a.part) + (size_t)un.tile * a.S * (a.NT * 32) + r;
+            const float4 *p0 = reinterpret_cast<const float4 *>(a.part) + (size_t)place * a.S * (a.NT * 32) + r;
 #pragma unroll 1
             for (int c = c0; c < ncols; c += cstep) {
                 float v[16];
@@ -1147,15 +1150,26 @@ struct Plan {
     int64_t Tw, Tn, units;          // pair: Tw counts pairs of tiles
     bool pair;                      // two CTAs share a tile of columns
     int NT, box, S, KB, KB0, seg, stages, raws;  // box: columns of B that a CTA holds
+    bool carry;                     // see Args
     uint32_t stage_bytes;
-    size_t bytes;                   // of the workspace, 0 where S is 1
+    size_t bytes;                   // of the workspace, 0 where there are no partial sums
 };
 
 // lanes: weight rows per projection (FWD) or columns K; cols: the other side; red: length of the
-// reduction (per source), sources 1 or 2; max_rows: reduction that one accumulator may sum; grads: FWD
-// with the gradients.
-inline Plan make_plan(int kind, int64_t lanes, int64_t cols, int64_t red, int sources, int64_t max_rows, int sms,
-                      bool grads = false) {
+// reduction (per source), sources 1 or 2; grads: FWD with the gradients; fp32: WGRAD with results in
+// 32 bits.
+//
+// The tensor cores truncate: each product, towards zero, to a quarter of the last place of the sum that
+// it joins (2^-25 of the sum's power of two), and the sum after each step. So R terms in one
+// accumulator lose up to R * 1.25 * 2^-25 of its largest partial sum, half of that where it grows
+// steadily (2^20 terms of one sign: up to 2e-2, measured 5.5e-3). An accumulator therefore sums 2^15
+// terms at most (6e-4, a sixth of bf16's rounding, measured 1e-4), and for fp32 results 2048 (operands of
+// N(0, 1) against a 64-bit product: 4e-7 over 910 rows, 2e-6 over 2048 and 9e-6 over 8192). Longer
+// units are added up outside, in fp32: in the partial sums of a split reduction, in fp32 results
+// themselves, else in one tile's worth of sums for each CTA.
+inline Plan make_plan(int kind, int64_t lanes, int64_t cols, int64_t red, int sources, int sms, bool grads = false,
+                      bool fp32 = false) {
+    const int most = (fp32 ? 2048 : 1 << 15) / BK;
     const int64_t Tw = kind == FWD ? (lanes + 63) / 64 : (lanes + 127) / 128;
     Plan best = {};
     double least = 0;
@@ -1170,7 +1184,6 @@ inline Plan make_plan(int kind, int64_t lanes, int64_t cols, int64_t red, int so
         p.NT = (int)(((cols + p.Tn - 1) / p.Tn + unit - 1) / unit * unit);
         p.KB0 = (int)((red + BK - 1) / BK);
         p.KB = p.KB0 * sources;
-        p.seg = max_rows > 0 && max_rows / BK < p.KB ? (int)(max_rows / BK) : p.KB;
         p.box = pair ? p.NT / 2 : p.NT;
         const uint32_t bb = kind == WGRAD ? (uint32_t)((p.box + 63) / 64) * 8192u : (uint32_t)p.box * 128u;
         p.stage_bytes = A_BYTES + bb;
@@ -1210,7 +1223,10 @@ inline Plan make_plan(int kind, int64_t lanes, int64_t cols, int64_t red, int so
                 least = t;
                 p.S = S;
                 p.units = tiles * S;
-                p.bytes = S > 1 ? CNT_BYTES + (size_t)p.units * (pair + 1) * p.NT * 512 : 0;
+                p.seg = (p.KB + S - 1) / S > most ? most : p.KB;
+                p.carry = S == 1 && p.seg < p.KB && !fp32;
+                const int64_t ctas = (p.units < workers ? p.units : workers) * (pair + 1);
+                p.bytes = S > 1 || p.carry ? CNT_BYTES + (size_t)(p.carry ? ctas : p.units * (pair + 1)) * p.NT * 512 : 0;
                 best = p;
             }
         }
@@ -1329,6 +1345,8 @@ w4_status launch(const Plan &p, Maps &tm, Args a, void *workspace, int sms, cuda
     a.KB = p.KB;
     a.KB0 = p.KB0;
     a.seg = p.seg;
+    a.carry = p.carry ? 1 : 0;
+    a.joined = p.S > 1 || p.carry ? 1 : 0;
     a.NT = p.NT;
     a.asym = a.w[0].zeros != nullptr ? 1 : 0;
     a.stages = p.stages;

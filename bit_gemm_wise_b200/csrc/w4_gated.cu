@@ -526,7 +526,7 @@ w4_status weight_ok(const uint8_t *codes, const uint16_t *scales, const int16_t 
 W4_API size_t w4a16_gated_workspace_bytes(int64_t M, int64_t H, int64_t K, int group) {
     if (!xg::shape_ok(M, H, K) || !valid_group(group) || K % group != 0) return 0;
     if (M <= kFewRows) return gated::by_bytes(M, H, K) ? gated::bytes_place(M, K, group).end : 0;
-    return xg::place_prep(xg::make_plan(xg::FWD, H, M, K, 1, 0, num_sms()).bytes, M * K, M).end;
+    return xg::place_prep(xg::make_plan(xg::FWD, H, M, K, 1, num_sms()).bytes, M * K, M).end;
 }
 
 W4_API w4_status w4a16_gated(const void *X_bf16, int64_t M, const uint8_t *codes_gate, const uint16_t *scales_gate,
@@ -563,7 +563,7 @@ W4_API w4_status w4a16_gated(const void *X_bf16, int64_t M, const uint8_t *codes
         return gated::gated_few(f, group, stream);
     }
     const int sms = num_sms();
-    const xg::Plan p = xg::make_plan(xg::FWD, H, M, K, 1, 0, sms);
+    const xg::Plan p = xg::make_plan(xg::FWD, H, M, K, 1, sms);
     const xg::PrepPlace q = xg::place_prep(p.bytes, M * K, M);
     if (!workspace || workspace_bytes < q.end) return W4_ERR_WORKSPACE;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
@@ -603,8 +603,8 @@ struct BwdLayout {
 };
 BwdLayout bwd_layout(int64_t M, int64_t H, int64_t K, int sms) {
     BwdLayout l;
-    l.grads = xg::make_plan(xg::FWD, H, M, K, 1, 0, sms, true);
-    l.dx = xg::make_plan(xg::DGRAD, K, M, H, 2, 0, sms);
+    l.grads = xg::make_plan(xg::FWD, H, M, K, 1, sms, true);
+    l.dx = xg::make_plan(xg::DGRAD, K, M, H, 2, sms);
     l.q = xg::place_prep(l.grads.bytes > l.dx.bytes ? l.grads.bytes : l.dx.bytes, M * (K > 2 * H ? K : 2 * H), M);
     return l;
 }
@@ -687,7 +687,7 @@ W4_API w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const 
 
 W4_API size_t w4a16_dgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int group) {
     if (!xg::shape_ok(M, N, K) || N % 8 != 0 || !valid_group(group) || K % group != 0) return 0;
-    return xg::place_prep(xg::make_plan(xg::DGRAD, K, M, N, 1, 0, num_sms()).bytes, M * N, M).end;
+    return xg::place_prep(xg::make_plan(xg::DGRAD, K, M, N, 1, num_sms()).bytes, M * N, M).end;
 }
 
 W4_API w4_status w4a16_dgrad(const void *dY_bf16, int64_t M, const uint8_t *codes, const uint16_t *scales,
@@ -701,7 +701,7 @@ W4_API w4_status w4a16_dgrad(const void *dY_bf16, int64_t M, const uint8_t *code
     if (st != W4_OK) return st;
     if (!aligned16(dY_bf16) || !aligned16(dX_bf16) || (workspace && !aligned16(workspace))) return W4_ERR_ALIGN;
     const int sms = num_sms();
-    const xg::Plan p = xg::make_plan(xg::DGRAD, K, M, N, 1, 0, sms);
+    const xg::Plan p = xg::make_plan(xg::DGRAD, K, M, N, 1, sms);
     const xg::PrepPlace q = xg::place_prep(p.bytes, M * N, M);
     if (!workspace || workspace_bytes < q.end) return W4_ERR_WORKSPACE;
     uint8_t *ws = static_cast<uint8_t *>(workspace);

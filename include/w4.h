@@ -563,8 +563,9 @@ w4_status w4_nf4_gemv(const void *x_bf16, int64_t M, const uint8_t *codes, const
  *   accumulation; X enters as fp16 after each row is divided by a power of two, exact for values
  *   within 2^-31 of the row's largest.
  *   Outputs must not overlap inputs. Results are bit-identical run to run on a given GPU.
- *   Over a reduction of R terms the tensor cores' fp32 sums are off by R / 16 * 2^-23 of the largest
- *   partial sum at most (they truncate): within bf16's own rounding up to R = 2^18.
+ *   M > 16: the tensor cores' fp32 sums truncate each term, by up to 2^-25 of the sum so far. One of them
+ *   takes 2^15 terms at most: off by up to 1.2e-3 of its largest partial sum, 6e-4 where terms of one sign
+ *   make it grow steadily. Longer reductions are added up outside the tensor cores, in fp32.
  *   M, H <= 2^24; 32 <= K <= 2^24, K % 32 == 0; M * H, M * K and H * K <= 2^40. Errors: NULL / SHAPE /
  *   GROUP / ALIGN / ARG (mode, act, zeros given for W4_SYM) / WORKSPACE / CUDA.
  */
@@ -632,8 +633,9 @@ w4_status fp8_ckpt_load(const uint8_t *X_e4m3, const uint8_t *X_scale, int64_t M
  * fp8_ckpt_wgrad -- the gradient of a linear layer y = x W^T by its weight (an adapter's, or a full
  *   one's) from the 8-bit checkpoint of x: dW[n, k] = sum_m dY[m, n] x8[m, k] 2^e[m, k/32].
  *   dY_bf16 [M, N] bf16; X_e4m3, X_scale as fp8_ckpt_save writes them for x [M, K]; dW [N, K] bf16, or
- *   fp32 with W4_OUT_FP32 in flags. The products are exact; accumulation is fp32, for fp32 results
- *   outside the tensor cores from 2048 rows to the next.
+ *   fp32 with W4_OUT_FP32 in flags. The products are exact; accumulation is fp32, outside the tensor
+ *   cores from 2048 rows to the next for fp32 results (whose sums of one sign are thus off by up to 4e-5,
+ *   others by 1e-6), from 2^15 rows to the next for bf16 ones.
  *   workspace as w4a16_gated's, of fp8_ckpt_wgrad_workspace_bytes(M, N, K) bytes.
  *   N % 8 == 0; other limits as w4a16_gated (with N for H). Errors: NULL / SHAPE / ALIGN / ARG / WORKSPACE / CUDA.
  */
