@@ -304,19 +304,20 @@ __device__ __forceinline__ void expand4(uint32_t w, uint32_t f, uint32_t &o0, ui
     o0 = bmul(((w << 4) & 0x07F007F0u) | ((w << 8) & 0x80008000u), f);
     o1 = bmul(((w >> 4) & 0x07F007F0u) | (w & 0x80008000u), f);
 }
-// factors of scale byte b = e + 127 (255 is NaN, 0 is 0): one up to b = 134, else 2^120 and 2^e
-__device__ __forceinline__ uint32_t pow2_one(uint32_t b) {
-    const uint32_t f = b == 0u ? 0u : (120u + b) << 7;
-    return f | (f << 16);
-}
+// E4M3's one NaN, 0x7F of either sign, reads as 480 there. nan_bytes: the top bit of each byte that is one.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+// factors of scale byte b = e + 127 (255 is NaN): one up to b = 134, else 2^120 and 2^e
+__device__ __forceinline__ uint32_t pow2_one(uint32_t b) { return ((120u + b) << 7) * 0x10001u; }
 __device__ __forceinline__ uint32_t pow2_two(uint32_t b) {
-    const uint32_t f = b == 255u ? 0x7FC0u : b << 7;
-    return f | (f << 16);
+    return (b == 255u ? 0x7FC0u : b == 0u ? 0x0040u : b << 7) * 0x10001u;  // 2^-127 is subnormal
 }
 __device__ __forceinline__ void expand4_any(uint32_t w, uint32_t b, uint32_t &o0, uint32_t &o1) {
     expand4(w, 0x7B807B80u, o0, o1);
     o0 = bmul(o0, pow2_two(b));
     o1 = bmul(o1, pow2_two(b));
+    const uint32_t n = nan_bytes(w) >> 7;
+    o0 |= (n & 0x00010001u) * 0x7FC0u;
+    o1 |= ((n >> 8) & 0x00010001u) * 0x7FC0u;
 }
 
 // A wait by all lanes of a warp, with one result for all of them (a vote, so that what follows stays
@@ -560,7 +561,7 @@ __device__ __forceinline__ void chunk_load(Values<KIND> &c, uint32_t raw, const 
         c.q[KIND == WGRAD ? 6 : 2] = u.z; c.q[KIND == WGRAD ? 7 : 3] = u.w;
     }
 }
-// their values into the A tile; ANY: with any scale and zero point
+// their values into the A tile; ANY: with any scale, zero point and NaN
 template <int KIND, int TPG, bool ANY>
 __device__ __forceinline__ void chunk_store(const Values<KIND> &c, uint32_t base, const Place<KIND, TPG> &p, int j, uint32_t sz) {
     const uint2 k = KIND == WGRAD ? make_uint2(pow2_one(sz), 0u) : near_words(sz);
@@ -598,10 +599,18 @@ __device__ __forceinline__ void expand_store(uint32_t raw, uint32_t base, const 
         Values<KIND> c[2];  // two chunks' loads in flight
         chunk_load<KIND, TPG>(c[0], raw, p, j);
         chunk_load<KIND, TPG>(c[1], raw, p, j + 1);
+        bool again = any;
         if (!any) {
             chunk_store<KIND, TPG, false>(c[0], base, p, j, sz[j]);
             chunk_store<KIND, TPG, false>(c[1], base, p, j + 1, sz[j + 1]);
-        } else {
+            if (KIND == WGRAD) {  // NaN among the values: rare, and found beside the rest in 2.5 instructions a word
+                uint32_t nan = 0u;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) nan |= nan_bytes(c[0].q[KIND == WGRAD ? i : 0]) | nan_bytes(c[1].q[KIND == WGRAD ? i : 0]);
+                again = nan != 0u;
+            }
+        }
+        if (again) {
             chunk_store<KIND, TPG, true>(c[0], base, p, j, sz[j]);
             chunk_store<KIND, TPG, true>(c[1], base, p, j + 1, sz[j + 1]);
         }

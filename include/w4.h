@@ -621,7 +621,11 @@ w4_status w4a16_dgrad(const void *dY_bf16, int64_t M, const uint8_t *codes, cons
  *   what the backward pass multiplies is the checkpoint itself, rounded nowhere again.
  *   X_bf16 [M, K] bf16; X_e4m3 uint8 [M, K]; X_scale uint8 [M, K/32], the byte e + 127. A block of 32
  *   with an infinity or a NaN gets scale byte 255 and values 0x7F, and restores as NaN.
- *   fp8_ckpt_load writes value * 2^e to bf16, exactly; a scale byte of 255 makes its block NaN.
+ *   Checkpoints that another program wrote may hold any bytes, here and where w4a16_gated_bwd and
+ *   fp8_ckpt_wgrad read them: E4M3's NaN (0x7F of either sign) is NaN under every scale, a scale byte of 255
+ *   makes its block NaN, and 0 is 2^-127.
+ *   fp8_ckpt_load writes value * 2^e to bf16: exactly, but for what only such bytes can mean, which is
+ *   rounded once (below 2^-126) or infinite (past bf16's range).
  *   1 <= M <= 2^24; 32 <= K <= 2^24, K % 32 == 0; M * K <= 2^40. Errors: NULL / SHAPE / ALIGN / CUDA.
  */
 w4_status fp8_ckpt_save(const void *X_bf16, int64_t M, int64_t K, uint8_t *X_e4m3, uint8_t *X_scale,
