@@ -178,16 +178,18 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Arrives at the first CTA's barrier of that place. The order is that within this CTA: what the arrival
-// passes on, its own SM reads (the tensor core its shared memory, of which the writers' proxy fences
-// came before) or has read (its TMEM). Release at cluster scope cost 900 cycles a stage.
+// Arrives at the first CTA's barrier of that place, and passes on what is ordered before the arrival in
+// this CTA's shared memory (its expanded stage, which the first CTA's MMAs read). The release at
+// cluster scope is a fence for that memory alone: one for all memory (release.cluster) waits for the
+// GPU's and took 900 cycles a stage, 1.9 times the product's time; this one costs nothing.
 __device__ __forceinline__ void arrive_first(uint64_t *bar) {
     asm volatile(
-        "{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %0, 0;\n mbarrier.arrive.shared::cluster.b64 _, [r];\n}\n" ::"r"(
-            smem_addr(bar))
+        "{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %0, 0;\n fence.release.sync_restrict::shared::cta.cluster;\n"
+        " mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [r];\n}\n" ::"r"(smem_addr(bar))
         : "memory");
 }
-// a wait whose arrivals come from both CTAs
+// A wait for what the other CTA does too: for its arrivals, or for the first CTA's MMAs (their commits).
+// It acquires at cluster scope, which costs less than 1% of the product's time.
 __device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -322,11 +324,13 @@ __device__ __forceinline__ void expand4_any(uint32_t w, uint32_t b, uint32_t &o0
 
 // A wait by all lanes of a warp, with one result for all of them (a vote, so that what follows stays
 // uniform). A phase that is over costs some 50 cycles this way; a poll by one lane with the rest
-// reconverging behind it took over 110. Bounded by the SM's clock (4e9 cycles, about 2 s).
+// reconverging behind it took over 110. Bounded by the SM's clock (4e9 cycles, about 2 s). PAIR: the phase
+// is completed by the other CTA too.
+template <bool PAIR>
 static __device__ __noinline__ bool slow_wait(uint64_t *bar, uint32_t parity, int *abort, int *status) {
     const long long t0 = clock64();
     bool r;
-    while (!(r = __all_sync(FULL, mbar_try_wait(bar, parity)))) {
+    while (!(r = __all_sync(FULL, PAIR ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)))) {
         if (__any_sync(FULL, *(volatile int *)abort != 0)) break;
         if (__any_sync(FULL, clock64() - t0 > kWaitCycles)) {
             *(volatile int *)abort = 1;
@@ -336,9 +340,10 @@ static __device__ __noinline__ bool slow_wait(uint64_t *bar, uint32_t parity, in
     }
     return r;
 }
+template <bool PAIR = false>
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, Smem *sm, int *status) {
-    if (__all_sync(FULL, mbar_try_wait_short(bar, parity))) return true;
-    return slow_wait(bar, parity, &sm->abort, status);
+    if (__all_sync(FULL, PAIR ? try_wait_cluster(bar, parity) : mbar_try_wait_short(bar, parity))) return true;
+    return slow_wait<PAIR>(bar, parity, &sm->abort, status);
 }
 // The same by the one thread that runs a producer's or the MMA issuer's loop.
 template <bool PAIR>
@@ -760,7 +765,7 @@ __global__ void __launch_bounds__((RolesOf<KIND, GRADS, GELU, PAIR>::THREADS), 1
             more = w.skip(a, GROUPS);
             if (more) next.fetch(a, w, tt);
             if (!warp_wait(&sm->rawf[rs], rphase, sm, a.status)) break;
-            if (!warp_wait(&sm->empty[slot], phase ^ 1u, sm, a.status)) break;
+            if (!warp_wait<PAIR>(&sm->empty[slot], phase ^ 1u, sm, a.status)) break;
             expand_store<KIND, R::TPG>(smem_addr(raw + (size_t)rs * Raw<KIND>::BYTES), smem_addr(base + (size_t)slot * a.stage_bytes),
                                place, sz);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMA reads them
@@ -786,7 +791,7 @@ __global__ void __launch_bounds__((RolesOf<KIND, GRADS, GELU, PAIR>::THREADS), 1
                 const Unit un = unit_of<PAIR>(a, u);
                 const int c0 = (int)(un.tn * a.NT) + (PAIR ? (int)cluster_rank() * (a.NT >> 1) : 0);  // a half each
                 for (int kb = un.b0; kb < un.b1; ++kb) {
-                    if (!wait1(&sm->empty[slot], phase ^ 1u, sm, a.status)) { ok = false; break; }
+                    if (!wait1<PAIR>(&sm->empty[slot], phase ^ 1u, sm, a.status)) { ok = false; break; }
                     uint8_t *dst = base + (size_t)slot * a.stage_bytes + A_BYTES;
                     mbar_arrive_expect_tx(&sm->full[slot], bytes);
                     if (KIND == WGRAD) {
@@ -944,7 +949,7 @@ __global__ void __launch_bounds__((RolesOf<KIND, GRADS, GELU, PAIR>::THREADS), 1
             if (GRADS) ahead.fetch(a, un, q4, lane, c0, ncols - c0);
             for (int s0 = un.b0; s0 < un.b1 && ok; s0 += a.seg, ++n) {
                 const int buf = n & 1;
-                if (!warp_wait(&sm->accf[buf], (uint32_t)(n >> 1) & 1u, sm, a.status)) { ok = false; break; }
+                if (!warp_wait<PAIR>(&sm->accf[buf], (uint32_t)(n >> 1) & 1u, sm, a.status)) { ok = false; break; }
                 tc_fence_after();
 #pragma unroll 1
                 for (int c = c0; c < ncols; c += cstep) {
