@@ -145,6 +145,14 @@ W4_API size_t fp8_ckpt_wgrad_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     return xg::make_plan(xg::WGRAD, K, N, M, 1, num_sms()).bytes;
 }
 
+W4_API w4_status fp8_ckpt_wgrad_schedule(int64_t M, int64_t N, int64_t K, int flags, int sms, int64_t *out) {
+    if (!out) return W4_ERR_NULL;
+    if (!xg::shape_ok(M, N, K) || N % 8 != 0 || sms < 1 || sms > 4096) return W4_ERR_SHAPE;
+    if ((flags & ~W4_OUT_FP32) != 0) return W4_ERR_ARG;
+    xg::describe(xg::make_plan(xg::WGRAD, K, N, M, 1, sms, false, (flags & W4_OUT_FP32) != 0), sms, out);
+    return W4_OK;
+}
+
 W4_API w4_status fp8_ckpt_wgrad(const void *dY_bf16, const uint8_t *X_e4m3, const uint8_t *X_scale, int64_t M, int64_t N,
                                 int64_t K, void *dW, int flags, void *workspace, size_t workspace_bytes,
                                 cudaStream_t stream) {

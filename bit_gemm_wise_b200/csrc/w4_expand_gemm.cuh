@@ -1248,6 +1248,20 @@ inline Plan make_plan(int kind, int64_t lanes, int64_t cols, int64_t red, int so
     return best;
 }
 
+// A plan as the schedule queries report it (w4.h).
+inline void describe(const Plan &p, int sms, int64_t *out) {
+    const int pair = p.pair ? 2 : 1;
+    const int64_t workers = sms / pair;
+    out[0] = pair;
+    out[1] = p.units;
+    out[2] = p.S;
+    out[3] = p.NT;
+    out[4] = p.KB;
+    out[5] = p.seg;
+    out[6] = (p.units < workers ? p.units : workers) * pair;
+    out[7] = (int64_t)p.bytes;
+}
+
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);

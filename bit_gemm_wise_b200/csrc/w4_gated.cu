@@ -529,6 +529,15 @@ W4_API size_t w4a16_gated_workspace_bytes(int64_t M, int64_t H, int64_t K, int g
     return xg::place_prep(xg::make_plan(xg::FWD, H, M, K, 1, num_sms()).bytes, M * K, M).end;
 }
 
+W4_API w4_status w4a16_gated_schedule(int64_t M, int64_t H, int64_t K, int group, int sms, int64_t *out) {
+    if (!out) return W4_ERR_NULL;
+    if (!xg::shape_ok(M, H, K) || sms < 1 || sms > 4096) return W4_ERR_SHAPE;
+    if (!valid_group(group) || K % group != 0) return W4_ERR_GROUP;
+    for (int i = 0; i < 8; ++i) out[i] = 0;
+    if (M > kFewRows) xg::describe(xg::make_plan(xg::FWD, H, M, K, 1, sms), sms, out);
+    return W4_OK;
+}
+
 W4_API w4_status w4a16_gated(const void *X_bf16, int64_t M, const uint8_t *codes_gate, const uint16_t *scales_gate,
                              const int16_t *zeros_gate, const uint8_t *codes_up, const uint16_t *scales_up,
                              const int16_t *zeros_up, int64_t H, int64_t K, int group, int mode, int act, void *Y_bf16,
@@ -617,6 +626,16 @@ W4_API size_t w4a16_gated_bwd_workspace_bytes(int64_t M, int64_t H, int64_t K, i
     return bwd_layout(M, H, K, num_sms()).q.end;
 }
 
+W4_API w4_status w4a16_gated_bwd_schedule(int64_t M, int64_t H, int64_t K, int group, int sms, int64_t *out) {
+    if (!out) return W4_ERR_NULL;
+    if (!xg::shape_ok(M, H, K) || H % 8 != 0 || sms < 1 || sms > 4096) return W4_ERR_SHAPE;
+    if (!valid_group(group) || K % group != 0) return W4_ERR_GROUP;
+    const BwdLayout l = bwd_layout(M, H, K, sms);
+    xg::describe(l.grads, sms, out);
+    xg::describe(l.dx, sms, out + 8);
+    return W4_OK;
+}
+
 W4_API w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const uint8_t *X_e4m3, const uint8_t *X_scale,
                                  int64_t M, const uint8_t *codes_gate, const uint16_t *scales_gate,
                                  const int16_t *zeros_gate, const uint8_t *codes_up, const uint16_t *scales_up,
@@ -688,6 +707,14 @@ W4_API w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const 
 W4_API size_t w4a16_dgrad_workspace_bytes(int64_t M, int64_t N, int64_t K, int group) {
     if (!xg::shape_ok(M, N, K) || N % 8 != 0 || !valid_group(group) || K % group != 0) return 0;
     return xg::place_prep(xg::make_plan(xg::DGRAD, K, M, N, 1, num_sms()).bytes, M * N, M).end;
+}
+
+W4_API w4_status w4a16_dgrad_schedule(int64_t M, int64_t N, int64_t K, int group, int sms, int64_t *out) {
+    if (!out) return W4_ERR_NULL;
+    if (!xg::shape_ok(M, N, K) || N % 8 != 0 || sms < 1 || sms > 4096) return W4_ERR_SHAPE;
+    if (!valid_group(group) || K % group != 0) return W4_ERR_GROUP;
+    xg::describe(xg::make_plan(xg::DGRAD, K, M, N, 1, sms), sms, out);
+    return W4_OK;
 }
 
 W4_API w4_status w4a16_dgrad(const void *dY_bf16, int64_t M, const uint8_t *codes, const uint16_t *scales,

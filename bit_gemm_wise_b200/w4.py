@@ -76,6 +76,10 @@ SIGNATURES = [
     ("fp8_ckpt_load", _I, [_P, _P, _I64, _I64, _P, _P]),
     ("fp8_ckpt_wgrad_workspace_bytes", _SZ, [_I64, _I64, _I64]),
     ("fp8_ckpt_wgrad", _I, [_P, _P, _P, _I64, _I64, _I64, _P, _I, _P, _SZ, _P]),
+    ("w4a16_gated_schedule", _I, [_I64, _I64, _I64, _I, _I, _P]),
+    ("w4a16_gated_bwd_schedule", _I, [_I64, _I64, _I64, _I, _I, _P]),
+    ("w4a16_dgrad_schedule", _I, [_I64, _I64, _I64, _I, _I, _P]),
+    ("fp8_ckpt_wgrad_schedule", _I, [_I64, _I64, _I64, _I, _I, _P]),
     ("w4_device_status", _I, [_P, ctypes.POINTER(ctypes.c_int)]),
     ("w4_selftest_bounded_wait", _I, [_I64, _P]),
 ]
@@ -480,6 +484,33 @@ def fp8_ckpt_wgrad(dY, X8, x_scale, M, N, K, dW, flags=0, workspace=None, stream
     _call("fp8_ckpt_wgrad", d, stream, _buf("dY", dY, 2 * M * N, d), _buf("X8", X8, M * K, d),
           _buf("x_scale", x_scale, M * (K // 32), d), M, N, K, _buf("dW", dW, (4 if f & W4_OUT_FP32 else 2) * N * K, d),
           f, *_ws(workspace, d))
+
+
+def _product_schedule(name, *args, products=1):
+    keys = ("ctas_per_tile", "units", "parts", "columns", "stages", "stages_per_sum", "ctas", "sums_bytes")
+    out = (ctypes.c_int64 * (8 * products))()
+    _check(name, getattr(lib(), name)(*args, out))
+    return [dict(zip(keys, (int(v) for v in out[8 * i:8 * i + 8]))) for i in range(products)]
+
+
+def w4a16_gated_schedule(M, H, K, group, sms) -> dict:
+    """Host-only: how w4a16_gated divides the problem over `sms` SMs (all zero up to 16 rows)."""
+    return _product_schedule("w4a16_gated_schedule", M, H, K, group, sms)[0]
+
+
+def w4a16_gated_bwd_schedule(M, H, K, group, sms) -> list:
+    """Host-only: how w4a16_gated_bwd divides its two products, of the gradients and of dX."""
+    return _product_schedule("w4a16_gated_bwd_schedule", M, H, K, group, sms, products=2)
+
+
+def w4a16_dgrad_schedule(M, N, K, group, sms) -> dict:
+    """Host-only: how w4a16_dgrad divides the problem over `sms` SMs."""
+    return _product_schedule("w4a16_dgrad_schedule", M, N, K, group, sms)[0]
+
+
+def fp8_ckpt_wgrad_schedule(M, N, K, flags, sms) -> dict:
+    """Host-only: how fp8_ckpt_wgrad divides the problem over `sms` SMs."""
+    return _product_schedule("fp8_ckpt_wgrad_schedule", M, N, K, int(flags), sms)[0]
 
 
 def w4_device_status(stream=None) -> int:

@@ -649,6 +649,21 @@ w4_status fp8_ckpt_wgrad(const void *dY_bf16, const uint8_t *X_e4m3, const uint8
                          cudaStream_t stream);
 
 /*
+ * w4a16_gated_schedule, w4a16_gated_bwd_schedule, w4a16_dgrad_schedule, fp8_ckpt_wgrad_schedule --
+ *   host-only queries (no GPU call): how these products are divided over `sms` SMs (1 .. 4096), by the
+ *   same planner the launches use. out[8] receives: CTAs that share a tile (1 or 2), units (tiles
+ *   times parts of the reduction), parts, columns of a tile (tokens; for dW, columns of dY), stages of 64 of
+ *   the whole reduction, stages that one accumulator sums at most, CTAs launched, workspace bytes of
+ *   counters and partial sums. All zero for w4a16_gated at M <= 16, which divides nothing.
+ *   w4a16_gated_bwd_schedule: out[16], the product of the gradients and then that of dX.
+ *   Errors: NULL / SHAPE / GROUP / ARG (flags).
+ */
+w4_status w4a16_gated_schedule(int64_t M, int64_t H, int64_t K, int group, int sms, int64_t *out);
+w4_status w4a16_gated_bwd_schedule(int64_t M, int64_t H, int64_t K, int group, int sms, int64_t *out);
+w4_status w4a16_dgrad_schedule(int64_t M, int64_t N, int64_t K, int group, int sms, int64_t *out);
+w4_status fp8_ckpt_wgrad_schedule(int64_t M, int64_t N, int64_t K, int flags, int sms, int64_t *out);
+
+/*
  * w4_device_status -- synchronizes `stream`, then reads and clears the device status word
  *   of the current device. *code_out receives W4_OK or the first W4_ERR_TIMEOUT /
  *   W4_ERR_DEVICE_CHECK recorded since the last call. Returns W4_ERR_CUDA if the

@@ -28,7 +28,7 @@ def far_weight(N, K, group, seed):
 
 # one and two rows of a large layer (bytes), few rows, one CTA a tile, and pairs
 @pytest.mark.parametrize("M,H,K,group", [(1, 8192, 4096, 128), (2, 4104, 8192, 32), (4, 200, 512, 64), (16, 136, 256, 256),
-                                         (40, 264, 512, 32), (300, 520, 1088, 64)])
+                                         (40, 264, 512, 32), (300, 520, 1088, 64), (600, 2056, 640, 32)])
 def test_zero_points_of_any_size(M, H, K, group):
     wg, wu = far_weight(H, K, group, 1), far_weight(H, K, group, 2)
     x = R.rows(M, K, 3, DEV, std=0.01)
@@ -41,7 +41,7 @@ def test_zero_points_of_any_size(M, H, K, group):
     T.check_bwd(got, x, dh, wg, wu, group, "gelu_tanh")
 
 
-@pytest.mark.parametrize("M,N,K,group", [(3, 72, 128, 32), (64, 1000, 512, 256), (300, 520, 1088, 64)])
+@pytest.mark.parametrize("M,N,K,group", [(3, 72, 128, 32), (64, 1000, 512, 256), (300, 520, 1088, 64), (300, 4096, 2112, 32)])
 def test_dgrad_zero_points_of_any_size(M, N, K, group):
     w, dy = far_weight(N, K, group, 5), R.rows(M, N, 6, DEV, std=0.01)
     dx = T.run_dgrad(dy, w, group, "asym")
