@@ -381,12 +381,22 @@ def _act(act) -> int:
     return int(act)
 
 
-def _buf(name, t, need, dev):
-    """Pointer of a contiguous tensor on CUDA device `dev` that must hold `need` bytes; None stays
-    None. The C entry points take bare pointers, so a tensor of the wrong size or of another
-    device is caught here."""
+_BF16 = (torch.bfloat16,)
+_U8 = (torch.uint8,)
+_HALF_BITS = (torch.float16, torch.int16, torch.uint16)  # w4_quantize's scales are fp16 bits in int16
+_I16 = (torch.int16,)
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
+_E8M0 = (torch.uint8, torch.float8_e8m0fnu)
+
+
+def _buf(name, t, need, dev, types=None):
+    """Pointer of a contiguous tensor of one of `types` on CUDA device `dev` that must hold `need`
+    bytes; None stays None. The C entry points take bare pointers, so a tensor of the wrong type or
+    size or of another device is caught here."""
     if t is None:
         return None
+    if types is not None and t.dtype not in types:
+        raise ValueError(f"{name} is {t.dtype}, not {' or '.join(str(v) for v in types)}")
     if t.get_device() != dev or dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor on the first argument's device")
     if not t.is_contiguous():
@@ -400,7 +410,8 @@ def _weight4(name, w, N, K, group, dev):
     """Pointers of a canonical weight (codes, scales, zeros or None) of W[N, K]."""
     # a group or size that the C entry point refuses asks for nothing here
     J = N * (K // group) * 2 if group in (32, 64, 128, 256) and N > 0 and K > 0 else 0
-    return (_buf(name, w[0], N * K // 2, dev), _buf(name, w[1], J, dev), _buf(name, w[2], J, dev))
+    return (_buf(f"{name} codes", w[0], N * K // 2, dev, _U8), _buf(f"{name} scales", w[1], J, dev, _HALF_BITS),
+            _buf(f"{name} zeros", w[2], J, dev, _I16))
 
 
 def _ws(workspace, dev):
@@ -425,8 +436,8 @@ def w4a16_gated(X, M, gate, up, H, K, group, mode, act, Y, workspace=None, strea
     (zeros None for symmetric weights); act: "silu" or "gelu_tanh"; workspace:
     alloc_gated_workspace(M, H, K, group). Runs on X's device."""
     d = X.get_device()
-    _call("w4a16_gated", d, stream, _buf("X", X, 2 * M * K, d), M, *_weight4("gate", gate, H, K, group, d),
-          *_weight4("up", up, H, K, group, d), H, K, group, _mode(mode), _act(act), _buf("Y", Y, 2 * M * H, d),
+    _call("w4a16_gated", d, stream, _buf("X", X, 2 * M * K, d, _BF16), M, *_weight4("gate", gate, H, K, group, d),
+          *_weight4("up", up, H, K, group, d), H, K, group, _mode(mode), _act(act), _buf("Y", Y, 2 * M * H, d, _BF16),
           *_ws(workspace, d))
 
 
@@ -440,11 +451,11 @@ def w4a16_gated_bwd(dH, M, gate, up, H, K, group, mode, act, dG, dU, dX, workspa
     checkpoint X8, x_scale (fp8_ckpt_save). dX may be None. workspace:
     alloc_gated_bwd_workspace(M, H, K, group, from_ckpt=X8 is not None)."""
     d = dH.get_device()
-    _call("w4a16_gated_bwd", d, stream, _buf("dH", dH, 2 * M * H, d), _buf("X", X, 2 * M * K, d),
-          _buf("X8", X8, M * K, d), _buf("x_scale", x_scale, M * (K // 32), d), M,
+    _call("w4a16_gated_bwd", d, stream, _buf("dH", dH, 2 * M * H, d, _BF16), _buf("X", X, 2 * M * K, d, _BF16),
+          _buf("X8", X8, M * K, d, _E4M3), _buf("x_scale", x_scale, M * (K // 32), d, _E8M0), M,
           *_weight4("gate", gate, H, K, group, d), *_weight4("up", up, H, K, group, d), H, K, group, _mode(mode),
-          _act(act), _buf("dG", dG, 2 * M * H, d), _buf("dU", dU, 2 * M * H, d), _buf("dX", dX, 2 * M * K, d),
-          *_ws(workspace, d))
+          _act(act), _buf("dG", dG, 2 * M * H, d, _BF16), _buf("dU", dU, 2 * M * H, d, _BF16),
+          _buf("dX", dX, 2 * M * K, d, _BF16), *_ws(workspace, d))
 
 
 def w4a16_dgrad_workspace_bytes(M, N, K, group) -> int:
@@ -455,22 +466,23 @@ def w4a16_dgrad(dY, M, weight, N, K, group, mode, dX, workspace=None, stream=Non
     """dX = dY W of a 4-bit linear layer; weight: (codes, scales, zeros) of W[N, K]; workspace:
     alloc_dgrad_workspace(M, N, K, group)."""
     d = dY.get_device()
-    _call("w4a16_dgrad", d, stream, _buf("dY", dY, 2 * M * N, d), M, *_weight4("weight", weight, N, K, group, d), N, K,
-          group, _mode(mode), _buf("dX", dX, 2 * M * K, d), *_ws(workspace, d))
+    _call("w4a16_dgrad", d, stream, _buf("dY", dY, 2 * M * N, d, _BF16), M,
+          *_weight4("weight", weight, N, K, group, d), N, K, group, _mode(mode),
+          _buf("dX", dX, 2 * M * K, d, _BF16), *_ws(workspace, d))
 
 
 def fp8_ckpt_save(X, M, K, X8, x_scale, stream=None):
     """The 8-bit checkpoint of X [M, K]: X8 uint8 (or float8_e4m3fn) [M, K], x_scale uint8 [M, K/32]."""
     d = X.get_device()
-    _call("fp8_ckpt_save", d, stream, _buf("X", X, 2 * M * K, d), M, K, _buf("X8", X8, M * K, d),
-          _buf("x_scale", x_scale, M * (K // 32), d))
+    _call("fp8_ckpt_save", d, stream, _buf("X", X, 2 * M * K, d, _BF16), M, K, _buf("X8", X8, M * K, d, _E4M3),
+          _buf("x_scale", x_scale, M * (K // 32), d, _E8M0))
 
 
 def fp8_ckpt_load(X8, x_scale, M, K, X, stream=None):
     """X [M, K] bf16 from its 8-bit checkpoint, exactly."""
     d = X8.get_device()
-    _call("fp8_ckpt_load", d, stream, _buf("X8", X8, M * K, d), _buf("x_scale", x_scale, M * (K // 32), d), M, K,
-          _buf("X", X, 2 * M * K, d))
+    _call("fp8_ckpt_load", d, stream, _buf("X8", X8, M * K, d, _E4M3),
+          _buf("x_scale", x_scale, M * (K // 32), d, _E8M0), M, K, _buf("X", X, 2 * M * K, d, _BF16))
 
 
 def fp8_ckpt_wgrad_workspace_bytes(M, N, K) -> int:
@@ -481,9 +493,10 @@ def fp8_ckpt_wgrad(dY, X8, x_scale, M, N, K, dW, flags=0, workspace=None, stream
     """dW [N, K] = dY^T X from the 8-bit checkpoint of X; bf16, or fp32 with W4_OUT_FP32 in flags;
     workspace: alloc_ckpt_wgrad_workspace(M, N, K)."""
     d, f = dY.get_device(), int(flags)
-    _call("fp8_ckpt_wgrad", d, stream, _buf("dY", dY, 2 * M * N, d), _buf("X8", X8, M * K, d),
-          _buf("x_scale", x_scale, M * (K // 32), d), M, N, K, _buf("dW", dW, (4 if f & W4_OUT_FP32 else 2) * N * K, d),
-          f, *_ws(workspace, d))
+    size, types = (4, (torch.float32,)) if f & W4_OUT_FP32 else (2, _BF16)
+    _call("fp8_ckpt_wgrad", d, stream, _buf("dY", dY, 2 * M * N, d, _BF16), _buf("X8", X8, M * K, d, _E4M3),
+          _buf("x_scale", x_scale, M * (K // 32), d, _E8M0), M, N, K, _buf("dW", dW, size * N * K, d, types), f,
+          *_ws(workspace, d))
 
 
 def _product_schedule(name, *args, products=1):
