@@ -107,3 +107,19 @@ def test_gated_bwd_infinities_and_nan(M, H, K, ckpt):
             others = [i for i in range(H) if i != h]
             assert torch.equal(a[m, others], b[m, others]) and not bool(torch.isfinite(a[m, h]))
     assert bool(torch.isnan(got[0][5, 9])) and bool(torch.isnan(got[2][5]).all()) and not bool(torch.isfinite(got[2][6]).any())
+
+
+@pytest.mark.parametrize("M,H,K,power", [(2, 200, 256, 97), (9, 200, 256, 97), (1, 8192, 4096, 110), (20, 200, 256, 110)])
+def test_huge_activations(M, H, K, power):
+    """|G| of 2^90 and more: the product is infinite, of U's sign, or zero where the gate closes; no NaN."""
+    g = 64
+    wg, wu = T.weights(H, K, g, "asym", 9)
+    x = (R.rows(M, K, 1, DEV).double() * 2.0 ** power).to(R.BF16)
+    y = T.run_gated(x, wg, wu, g, "asym", "silu").double()
+    T.status_ok()
+    G, U = x.double() @ R.dequant(wg, g).t(), x.double() @ R.dequant(wu, g).t()
+    e = 2.0 ** -11 + 2.0 ** -12
+    sure = (G.abs() > e * T.magnitudes(x, wg, g)) & (U.abs() > e * T.magnitudes(x, wu, g))
+    assert float(sure.double().mean()) > 0.95
+    want = torch.where(G > 0, float("inf") * torch.sign(U), 0.0 * U)
+    assert torch.equal(y[sure], want[sure]) and not bool(torch.isnan(y).any())
