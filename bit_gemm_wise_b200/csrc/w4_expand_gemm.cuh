@@ -25,11 +25,11 @@
 //                by TMA, into a ring of their own.
 // Lanes are weights and columns are tokens: a small batch takes a small N and the MMAs shrink with
 // it, while the expansion is shared by all tokens of a tile. What bounds a stage is the shared memory's
-// data path: codes in and out, A in and out and B twice, 128 bytes a cycle, came to 1060 (FWD), 980
-// (DGRAD) and 900 (WGRAD) cycles of its 990, 900 and 840 at N = 256 (192), against 512 (384) of MMAs.
-// So where there are more than 128 columns, two CTAs make a pair: one MMA of both SMs (M = 256) on
-// 128 lanes of each, every SM holding half of B, which it writes and reads half as often (DGRAD 714
-// cycles a stage). The first CTA of a pair issues the MMAs; the second one passes on that its stages
+// data path: codes in and out, A in and out and B twice, 128 bytes a cycle, kept it busy for 101% (FWD),
+// 98% (DGRAD) and 94% (WGRAD) of a stage's 984, 903 and 836 cycles at N = 256 (192), of which the MMAs
+// take 512 (384). So where there are more than 128 columns, two CTAs make a pair: one MMA of both SMs
+// (M = 256) on 128 lanes of each, every SM holding half of B, which it writes and reads half as often
+// (803, 712 and, at N = 256, 766 cycles a stage). The first CTA of a pair issues the MMAs; the second one passes on that its stages
 // are full. Beyond that, instructions count: the codes' pairs (i, i + 4) of eight stay in that order, and
 // B's rows (FWD) or the results' lanes (DGRAD, WGRAD) are permuted instead; a thread's scale
 // addresses move by one addition. (Not kept: a table of FWD's scales made beforehand, side by side for a
@@ -56,11 +56,15 @@ constexpr int GROUPS = 4;                     // of expansion warps; stage i is 
 
 // How a CTA's warps are divided. Sixteen expansion warps and four for the results leave a thread 80
 // registers; where the results take long (two gradients and dH for each pair of accumulators; tiles of
-// few stages), eight and eight do better. Measured with the two ways in turn, one CTA a tile, us: prefill
-// 4096 x 15360 x 3840 822 and 853, dgrad 4096 x 4096 x 14336 407 and 429; the gradients of 2048 x 14336 x
-// 4096 with their dX 1126 and 1065, wgrad 2048 x 4096 x 4096 91 and 87. In pairs of CTAs, whose stages are
-// shorter, the gelu of prefill counts as long too (911 and 829), silu does not (4096 x 14336 x 4096 879 and
-// 858, but 512 x 4096 x 4096 in groups of 32 43.0 and 45.3).
+// few stages), eight and eight do better. Us with the two ways in turn, on one GPU:
+//                                              one CTA a tile         pairs
+//   gated 4096 x 15360 x 3840, silu            944 and 988      848 and 842
+//   the same, gelu                             971 and 964      891 and 830
+//   gated 512 x 4096 x 4096 in groups of 32   42.7 and 45.1    41.3 and 43.0
+//   dgrad 4096 x 4096 x 14336                  446 and 463      383 and 392
+//   gradients and dX of 2048 x 14336 x 4096   1128 and 1047    1108 and 869  (both products one way)
+//   wgrad 2048 x 4096 x 4096                  88.8 and 87.8    82.0 and 74.3
+// So the gradients and WGRAD take eight and eight, and gelu does in pairs, whose stages are shorter.
 template <bool LONG_RESULTS> struct Roles {
     static constexpr int EXPAND = LONG_RESULTS ? 8 : 16, OUT = LONG_RESULTS ? 8 : 4;
     static constexpr int WPG = EXPAND / GROUPS;     // expansion warps per group
@@ -407,7 +411,7 @@ template <bool PAIR> __device__ __forceinline__ Unit unit_of(const Args &a, uint
     } else {
         t.tn = r / (uint32_t)a.S;
         t.s = r - t.tn * (uint32_t)a.S;
-        // parts of a.part stages; the first a.more of them have one more
+        // parts of a.part_kb stages; the first a.part_more of them have one more
         t.b0 = (int)(t.s * (uint32_t)a.part_kb + (t.s < (uint32_t)a.part_more ? t.s : (uint32_t)a.part_more));
         t.b1 = t.b0 + a.part_kb + (t.s < (uint32_t)a.part_more ? 1 : 0);
     }
@@ -908,7 +912,7 @@ __global__ void __launch_bounds__((RolesOf<KIND, GRADS, GELU, PAIR>::THREADS), 1
 
     if (warp < R::W_B) {
         // ------------------------------------------------ results (lane 32 q4 + lane of the tile), 16
-        // columns at a time, in turn by the warps of a quarter: the two result warps; and, in the CTA's
+        // columns at a time, in turn by the warps of a quarter: the result warps; and, in the CTA's
         // last tile, which has nothing behind it to overlap with, the expansion warps too, whose work is
         // done. Where a unit is summed up in several accumulators, they do not.
         constexpr int RANKS = R::RANKS, HELPERS = R::HELPERS;
@@ -1048,7 +1052,7 @@ __global__ void __launch_bounds__((RolesOf<KIND, GRADS, GELU, PAIR>::THREADS), 1
 
 // The fp16 copy of bf16 rows that the products above multiply: row m divided by the power of two
 // that brings its largest finite value into [2^14, 2^15). A bf16 value within 2^-31 of the
-// largest is exact in it; what is smaller is off by 2^-40 of the largest at most. One or two
+// largest is exact in it; what is smaller is off by 2^-39 of the largest at most. One or two
 // tensors of the same rows (the two gradients, which one accumulator sums) share a power; the 8-bit
 // checkpoint is restored on the way. One block per row, which it reads twice (the second time from
 // L1 or L2); bound by the memory traffic of reading 2 (1) and writing 2 bytes a value.
@@ -1094,7 +1098,7 @@ template <bool CKPT> __device__ __forceinline__ void prep_read(const Prep &p, in
 
 template <bool CKPT> __global__ void __launch_bounds__(256) row_prep_kernel(const Prep p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // of the kernel before, where this one may start early
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // for the product before, where this one is launched behind it
     __shared__ float top[8];
     const int64_t chunks = p.K >> 3;
     for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
@@ -1221,11 +1225,12 @@ inline Plan make_plan(int kind, int64_t lanes, int64_t cols, int64_t red, int so
         grow(MIN_STAGES + 1, 2 * GROUPS);
         grow(MAX_STAGES, MAX_RAW);
         // One CTA or two (more than 128 columns: 77 x 5632 x 2048 takes 16.6 us in pairs, 16.0 without), and
-        // parts of the reduction: what has the least estimated time, in cycles as
-        // measured. A stage takes the shared memory's traffic (the codes, A and the scales, and two passes
-        // of B, which a pair divides) or its MMAs; a unit takes 7000 to start and end, 8500 in a pair; the last part of a
-        // tile reads two partial sums of 16 columns in 1300 cycles, five groups of columns at a time,
-        // after 1500 for the count.
+        // parts of the reduction: what has the least estimated time, in cycles. One estimate serves all
+        // products. A stage takes the shared memory's traffic (the codes, A and the scales, and two passes
+        // of B, which a pair divides) or its MMAs: 916 at 256 columns, measured 984 (FWD) and 903 (DGRAD);
+        // in a pair 673, measured 803, 712 and 766 (WGRAD). A unit takes 7000 to start and end, 8500 in a
+        // pair; the last part of a tile reads two partial sums of 16 columns in 1300 cycles, five groups of
+        // columns at a time, after 1500 for the count.
         const int64_t tiles = p.Tw * p.Tn, workers = pair ? sms / 2 : sms;
         const double mem = 430 + 1.9 * p.box, mma = 2.1 * p.NT, stage = mem > mma ? mem : mma;
         for (int S = 1; S <= 32 && (S == 1 || S * 4 <= p.KB); ++S) {
@@ -1278,18 +1283,15 @@ inline EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// 8-bit [rows, width], plain boxes or boxes of 128 bytes' width with the 128-byte swizzle; what lies
-// outside reads as zero
-inline bool make_raw_map(CUtensorMap *tm, const void *p, int64_t rows, int64_t width, int box_width, int box_rows,
-                         bool swizzle = false) {
+// 8-bit [rows, width], plain boxes; what lies outside reads as zero
+inline bool make_raw_map(CUtensorMap *tm, const void *p, int64_t rows, int64_t width, int box_width, int box_rows) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)width};
     const cuuint32_t box[2] = {(cuuint32_t)box_width, (cuuint32_t)box_rows}, es[2] = {1, 1};
     return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(p), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1317,8 +1319,9 @@ template <typename F> bool allow_smem(F *kernel, int bytes, std::atomic<uint64_t
     return true;
 }
 
-// Launch that may start while the kernel before it on the stream is finishing (programmatic
-// dependent launch).
+// Launch by programmatic dependent launch where `behind` is 1: the kernel starts, up to its
+// griddepcontrol.wait, once every CTA of the one before it on the stream has issued launch_dependents
+// (the preparation kernels do at once) or has exited (the products' CTAs).
 template <typename... P, typename... A>
 w4_status launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream, int behind,
                         int cluster, A &&...args) {
@@ -1339,9 +1342,10 @@ w4_status launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads, s
     return launch_status();
 }
 
-// behind: the kernel before it on the stream is this call's own, so it may start while that one is
-// finishing. Else whatever came before is complete when it starts, and with that the weights that the
-// product behind it reads before it has waited for this kernel.
+// behind: the kernel before it on the stream is this call's own product, so this one may be launched
+// early: its blocks start when the product's last CTA exits, which hides the launch and nothing else.
+// Otherwise whatever came before is complete when it starts, and with that the weights that the product
+// behind it reads before it has waited for this kernel.
 inline w4_status launch_prep(const Prep &p, bool behind, cudaStream_t stream) {
     const unsigned grid = (unsigned)(p.M < (1 << 20) ? p.M : (1 << 20));
     if (behind)

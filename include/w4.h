@@ -537,8 +537,9 @@ w4_status w4_nf4_gemv(const void *x_bf16, int64_t M, const uint8_t *codes, const
                       int64_t N, int64_t K, void *y, int flags, cudaStream_t stream);
 
 /*
- * w4a16_gated -- the gated feed-forward block over 4-bit weights in one kernel: both projections,
- *   the activation and the product. No [gate | up] tensor goes through memory.
+ * w4a16_gated -- the gated feed-forward block over 4-bit weights: both projections, the activation
+ *   and the product in one kernel. No [gate | up] tensor goes through memory. Where it takes a
+ *   workspace, a small kernel before that one copies X into the form that the product reads.
  *     G = X Wg^T,  U = X Wu^T,  Y[m, h] = act(G[m, h]) * U[m, h]
  *   W4_ACT_SILU: act(g) = g / (1 + exp(-g)); W4_ACT_GELU_TANH: act(g) = 0.5 g (1 + tanh(sqrt(2/pi)
  *   (g + 0.044715 g^3))). The weights are the CANONICAL ones that w4_quantize writes (no prepack),
@@ -557,11 +558,11 @@ w4_status w4_nf4_gemv(const void *x_bf16, int64_t M, const uint8_t *codes, const
  *                concurrently need separate workspaces. After a call whose kernel recorded an error
  *                in the device status, zero-fill it again.
  *   M <= 16: the weights enter as exact integers and group scales and zero points are applied in
- *   fp32 (about 1e-5 relative before the one rounding to bf16; an infinity in a row may make that
- *   row's outputs NaN). M > 16: tcgen05 MMAs on weights
- *   dequantized to fp16 with one rounding (relative 2^-11 per weight; |w| up to 65504) and fp32
- *   accumulation; X enters as fp16 after each row is divided by a power of two, exact for values
- *   within 2^-31 of the row's largest.
+ *   fp32 (about 1e-5 relative before the one rounding to bf16; an infinity in a row, or a value past
+ *   2^100, may make that row's outputs NaN). M > 16: tcgen05 MMAs on weights dequantized to fp16 with
+ *   one rounding (relative 2^-11 per weight; |w| up to 65504, so that a layer with a larger one is served
+ *   at M <= 16 only) and fp32 accumulation; X enters as fp16 after each row is divided by a power of
+ *   two, exact for values within 2^-31 of the row's largest.
  *   Outputs must not overlap inputs. Results are bit-identical run to run on a given GPU.
  *   M > 16: the tensor cores' fp32 sums truncate each term, by up to 2^-25 of the sum so far. One of them
  *   takes 2^15 terms at most: off by up to 1.2e-3 of its largest partial sum, 6e-4 where terms of one sign
@@ -586,7 +587,8 @@ w4_status w4a16_gated(const void *X_bf16, int64_t M, const uint8_t *codes_gate, 
  *   dG_bf16, dU_bf16  device, bf16 [M, H], outputs (rounded once; dX is formed from the rounded ones)
  *   dX_bf16      device, bf16 [M, K], output, or NULL where it is not wanted (a first layer)
  *   workspace    as w4a16_gated's, of w4a16_gated_bwd_workspace_bytes(M, H, K, group, from_ckpt) bytes
- *                (from_ckpt 1: X comes as the checkpoint). Always needed.
+ *                (from_ckpt 1: X comes as the checkpoint; both sources ask for the same at
+ *                present). Always needed.
  *   Weights, X and the gradients enter the products as w4a16_gated's at M > 16. Outputs must not
  *   overlap inputs or each other. H % 8 == 0; other limits and errors as w4a16_gated.
  */
