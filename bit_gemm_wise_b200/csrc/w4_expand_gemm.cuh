@@ -121,6 +121,7 @@ struct Args {
     const __nv_bfloat16 *dh;  // FWD: NULL, or [cols, rows]: write the gradients of both projections
     void *out;                // FWD: Y or dG [cols, rows]; DGRAD: dX [cols, K]; WGRAD: dW [cols, K]
     __nv_bfloat16 *out2;      // FWD with dh: dU
+    uint16_t *rest;           // FWD with dh: NULL, or [cols, rows]: rest_of dG, and of dU above it
     const float *row_pow;     // FWD, DGRAD: the power of two that each token's row was divided by
     float *part;              // partial sums [tile][part][column / 4][lane][4]; carry: of a CTA's tile, [CTA]
     uint32_t *cnt;            // arrival counters [tile][4], zero between calls
@@ -629,6 +630,18 @@ __device__ __forceinline__ void expand_store(uint32_t raw, uint32_t base, const 
 __host__ __device__ __forceinline__ constexpr int value_at8(int place) { return (place >> 1) | ((place & 1) << 2); }
 __host__ __device__ __forceinline__ constexpr int value_at4(int place) { return (place >> 1) | ((place & 1) << 1); }
 
+// What rounding v to the bf16 value b left of it, as a byte: of the 16 bits below b's last place (RN's
+// choice makes them signed) the upper eight, rounded. with_rest(b, byte) is v to 16 significant bits.
+__device__ __forceinline__ uint32_t rest_of(float v, __nv_bfloat16 b) {
+    const int r = (int)(__float_as_uint(v) - ((uint32_t)__bfloat16_as_ushort(b) << 16));
+    return (uint32_t)min((r + 128) >> 8, 127) & 0xFFu;
+}
+// of a pair's word of bf16 values and its word of rests: value e (0 or 1), byte t of its rests
+__device__ __forceinline__ float with_rest(uint32_t w, uint32_t rests, int e, int t) {
+    const uint32_t r = (uint32_t)((int)(rests << (24 - 8 * (2 * e + t))) >> 16) & 0xFFFFFF00u;
+    return __uint_as_float((e ? w & 0xFFFF0000u : w << 16) + r);
+}
+
 // dH at the tokens and the feature that this lane finishes of columns [c, c + 16), n of which exist
 // (see emit). Only loads: nothing waits for them before emit() uses them.
 struct Incoming {
@@ -670,14 +683,17 @@ __device__ __forceinline__ void emit(const Args &a, const float *row_pow, const 
             const float g = f * (up ? got : v[2 * i]), u = f * (up ? v[2 * i + 1] : got);
             const Act t = act_of(g, GELU);
             const float d = GRADS ? bf16_lo(dh.v[i]) : 0.0f;
-            const __nv_bfloat16 first = __float2bfloat16_rn(GRADS ? d * u * t.slope : t.value * u);
-            if (whole) {
+            const float v1 = GRADS ? d * u * t.slope : t.value * u, v2 = d * t.value;
+            const __nv_bfloat16 first = __float2bfloat16_rn(v1), second = __float2bfloat16_rn(v2);
+            const auto store = [&] {
                 o[i * step] = first;
-                if (GRADS) o2[i * step] = __float2bfloat16_rn(d * t.value);
-            } else if (2 * i < m) {
-                o[i * step] = first;
-                if (GRADS) o2[i * step] = __float2bfloat16_rn(d * t.value);
-            }
+                if (GRADS) o2[i * step] = second;
+                if (GRADS && a.rest) a.rest[at + i * step] = (uint16_t)(rest_of(v1, first) | rest_of(v2, second) << 8);
+            };
+            if (whole)
+                store();
+            else if (2 * i < m)
+                store();
         }
     } else {
         const int pl = KIND == DGRAD ? (lane & ~7) + value_at8(lane & 7) : (lane & ~3) + value_at4(lane & 3);
@@ -1053,17 +1069,19 @@ __global__ void __launch_bounds__((RolesOf<KIND, GRADS, GELU, PAIR>::THREADS), 1
 // The fp16 copy of bf16 rows that the products above multiply: row m divided by the power of two
 // that brings its largest finite value into [2^14, 2^15). A bf16 value within 2^-31 of the
 // largest is exact in it; what is smaller is off by 2^-39 of the largest at most. One or two
-// tensors of the same rows (the two gradients, which one accumulator sums) share a power; the 8-bit
+// tensors of the same rows (the two gradients, which one accumulator sums) share a power. The
+// gradients come with the rests of their rounding, so that dX is formed from them to fp16's 11 bits and
+// not bf16's 8 (its error against 64 bits is 0.0017 of it, its own rounding, and was 0.0024). The 8-bit
 // checkpoint is restored on the way. One block per row, which it reads twice (the second time from
 // L1 or L2); bound by the memory traffic of reading 2 (1) and writing 2 bytes a value.
 struct Prep {
-    const __nv_bfloat16 *x[2];    // [M, K] each; NULL for the checkpoint
+    const __nv_bfloat16 *x[2];    // [M, K]: the rows, or dG and dU
+    const uint16_t *rest;         // the gradients' [M, K]: byte t of each is x[t]'s rest
     const uint8_t *x8, *xs;       // checkpoint values [M, K] and scale bytes [M, K/32]
     __half *y[2];                 // [M, K] each
     float *row_pow;               // [M]
     int64_t M, K;
-    int tensors;
-    int pairs;                    // each eight columns in expand8's order (the reduction of FWD)
+    int pairs;                    // ROWS: each eight columns in expand8's order (the reduction of FWD)
 };
 
 // a non-finite value takes no part in the maximum
@@ -1072,44 +1090,54 @@ __device__ __forceinline__ float finite_abs(float v) {
     return f <= 3.4e38f ? f : 0.0f;
 }
 
-template <bool CKPT> __device__ __forceinline__ void prep_read(const Prep &p, int t, int64_t m, int64_t i, float (&v)[8]) {
-    if (CKPT) {
+enum Source { ROWS = 0, CHECKPOINT = 1, GRADIENTS = 2 };
+
+// Eight columns of a row: of x[0], of the checkpoint, or of both gradients (v[1]; `rests` those of their
+// rounding, or zeros).
+template <int SRC>
+__device__ __forceinline__ void prep_read(const Prep &p, int64_t m, int64_t i, const uint4 &rests, float (&v)[SRC == GRADIENTS ? 2 : 1][8]) {
+    if (SRC == CHECKPOINT) {
         const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p.x8 + m * p.K) + i);
         const uint32_t b = __ldg(p.xs + m * (p.K >> 5) + (i >> 2));
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             uint32_t o[2];
             expand4_any(j ? w.y : w.x, b, o[0], o[1]);
-            v[4 * j] = bf16_lo(o[0]);
-            v[4 * j + 2] = bf16_hi(o[0]);
-            v[4 * j + 1] = bf16_lo(o[1]);
-            v[4 * j + 3] = bf16_hi(o[1]);
+            v[0][4 * j] = bf16_lo(o[0]);
+            v[0][4 * j + 2] = bf16_hi(o[0]);
+            v[0][4 * j + 1] = bf16_lo(o[1]);
+            v[0][4 * j + 3] = bf16_hi(o[1]);
         }
     } else {
-        const uint4 w = __ldcg(reinterpret_cast<const uint4 *>((t ? p.x[1] : p.x[0]) + m * p.K) + i);
-        const uint32_t o[4] = {w.x, w.y, w.z, w.w};
+        const uint32_t l[4] = {rests.x, rests.y, rests.z, rests.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = bf16_lo(o[j]);
-            v[2 * j + 1] = bf16_hi(o[j]);
+        for (int t = 0; t < (SRC == GRADIENTS ? 2 : 1); ++t) {
+            const uint4 w = __ldcg(reinterpret_cast<const uint4 *>(p.x[t] + m * p.K) + i);
+            const uint32_t o[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[t][2 * j] = with_rest(o[j], l[j], 0, t);
+                v[t][2 * j + 1] = with_rest(o[j], l[j], 1, t);
+            }
         }
     }
 }
 
-template <bool CKPT> __global__ void __launch_bounds__(256) row_prep_kernel(const Prep p) {
+template <int SRC> __global__ void __launch_bounds__(256) row_prep_kernel(const Prep p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");  // for the product before, where this one is launched behind it
     __shared__ float top[8];
+    constexpr int TENSORS = SRC == GRADIENTS ? 2 : 1;
     const int64_t chunks = p.K >> 3;
+    const uint4 none = make_uint4(0, 0, 0, 0);
     for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
         float mx = 0.0f;
-        for (int t = 0; t < p.tensors; ++t)
-            for (int64_t i = threadIdx.x; i < chunks; i += 256) {
-                float v[8];
-                prep_read<CKPT>(p, t, m, i, v);
+        for (int64_t i = threadIdx.x; i < chunks; i += 256) {
+            float v[TENSORS][8];
+            prep_read<SRC>(p, m, i, none, v);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) mx = fmaxf(mx, finite_abs(v[j]));
-            }
+            for (int j = 0; j < 8 * TENSORS; ++j) mx = fmaxf(mx, finite_abs(v[j >> 3][j & 7]));
+        }
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
         __syncthreads();  // the previous row's readers of top
@@ -1120,19 +1148,22 @@ template <bool CKPT> __global__ void __launch_bounds__(256) row_prep_kernel(cons
         if (e < 15) e = mx == 0.0f ? 141 : 15;      // factors stay finite; a row of zeros has factor 1
         const float f = __uint_as_float((uint32_t)(268 - e) << 23);  // 2^(14 - (e - 127))
         if (threadIdx.x == 0) p.row_pow[m] = __uint_as_float((uint32_t)(e - 14) << 23);
-        for (int t = 0; t < p.tensors; ++t)
-            for (int64_t i = threadIdx.x; i < chunks; i += 256) {
-                float v[8];
-                prep_read<CKPT>(p, t, m, i, v);
+        for (int64_t i = threadIdx.x; i < chunks; i += 256) {
+            float v[TENSORS][8];
+            prep_read<SRC>(p, m, i, SRC == GRADIENTS ? __ldcg(reinterpret_cast<const uint4 *>(p.rest + m * p.K) + i) : none, v);
+#pragma unroll
+            for (int t = 0; t < TENSORS; ++t) {
                 uint32_t o[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float lo = p.pairs ? v[j] : v[2 * j], hi = p.pairs ? v[j + 4] : v[2 * j + 1];
+                    const bool pairs = SRC == CHECKPOINT || (SRC == ROWS && p.pairs);
+                    const float lo = pairs ? v[t][j] : v[t][2 * j], hi = pairs ? v[t][j + 4] : v[t][2 * j + 1];
                     const __half2 h = __floats2half2_rn(lo * f, hi * f);
                     o[j] = *reinterpret_cast<const uint32_t *>(&h);
                 }
-                reinterpret_cast<uint4 *>((t ? p.y[1] : p.y[0]) + m * p.K)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+                reinterpret_cast<uint4 *>(p.y[t] + m * p.K)[i] = make_uint4(o[0], o[1], o[2], o[3]);
             }
+        }
     }
 }
 
@@ -1342,19 +1373,17 @@ w4_status launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads, s
     return launch_status();
 }
 
-// behind: the kernel before it on the stream is this call's own product, so this one may be launched
-// early: its blocks start when the product's last CTA exits, which hides the launch and nothing else.
-// Otherwise whatever came before is complete when it starts, and with that the weights that the product
-// behind it reads before it has waited for this kernel.
-inline w4_status launch_prep(const Prep &p, bool behind, cudaStream_t stream) {
+// Rows or a checkpoint: whatever came before on the stream is complete when this kernel starts, and with
+// that the weights that the product behind it reads before it has waited for this kernel. Gradients come
+// from this call's own product, so their kernel is launched behind it: its blocks start when the
+// product's last CTA exits, which hides the launch and nothing else.
+inline w4_status launch_prep(const Prep &p, cudaStream_t stream) {
     const unsigned grid = (unsigned)(p.M < (1 << 20) ? p.M : (1 << 20));
-    if (behind)
-        return p.x8 ? launch_behind(row_prep_kernel<true>, grid, 256, 0, stream, 1, 1, p)
-                    : launch_behind(row_prep_kernel<false>, grid, 256, 0, stream, 1, 1, p);
+    if (p.rest) return launch_behind(row_prep_kernel<GRADIENTS>, grid, 256, 0, stream, 1, 1, p);
     if (p.x8)
-        row_prep_kernel<true><<<grid, 256, 0, stream>>>(p);
+        row_prep_kernel<CHECKPOINT><<<grid, 256, 0, stream>>>(p);
     else
-        row_prep_kernel<false><<<grid, 256, 0, stream>>>(p);
+        row_prep_kernel<ROWS><<<grid, 256, 0, stream>>>(p);
     return launch_status();
 }
 

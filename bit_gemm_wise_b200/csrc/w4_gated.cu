@@ -585,9 +585,8 @@ W4_API w4_status w4a16_gated(const void *X_bf16, int64_t M, const uint8_t *codes
     prep.row_pow = reinterpret_cast<float *>(ws + q.row_pow);
     prep.M = M;
     prep.K = K;
-    prep.tensors = 1;
     prep.pairs = 1;
-    st = xg::launch_prep(prep, false, stream);
+    st = xg::launch_prep(prep, stream);
     if (st != W4_OK) return st;
     xg::Args a = {};
     a.row_pow = prep.row_pow;
@@ -605,16 +604,19 @@ W4_API w4_status w4a16_gated(const void *X_bf16, int64_t M, const uint8_t *codes
 namespace {
 
 // Workspace of the backward pass: counters and partial sums of its two products, then the fp16 rows
-// that each multiplies (X, and after it dG and dU), each time in the same place.
+// that each multiplies (X, and after it dG and dU), each time in the same place, and the rests of dG
+// and dU.
 struct BwdLayout {
     xg::Plan grads, dx;
     xg::PrepPlace q;
+    size_t end;
 };
 BwdLayout bwd_layout(int64_t M, int64_t H, int64_t K, int sms) {
     BwdLayout l;
     l.grads = xg::make_plan(xg::FWD, H, M, K, 1, sms, true);
     l.dx = xg::make_plan(xg::DGRAD, K, M, H, 2, sms);
     l.q = xg::place_prep(l.grads.bytes > l.dx.bytes ? l.grads.bytes : l.dx.bytes, M * (K > 2 * H ? K : 2 * H), M);
+    l.end = (l.q.end + (size_t)(M * H) * 2 + 255) / 256 * 256;
     return l;
 }
 
@@ -623,7 +625,7 @@ BwdLayout bwd_layout(int64_t M, int64_t H, int64_t K, int sms) {
 W4_API size_t w4a16_gated_bwd_workspace_bytes(int64_t M, int64_t H, int64_t K, int group, int from_ckpt) {
     if (!xg::shape_ok(M, H, K) || H % 8 != 0 || !valid_group(group) || K % group != 0) return 0;
     (void)from_ckpt;  // both sources become the same fp16 rows
-    return bwd_layout(M, H, K, num_sms()).q.end;
+    return bwd_layout(M, H, K, num_sms()).end;
 }
 
 W4_API w4_status w4a16_gated_bwd_schedule(int64_t M, int64_t H, int64_t K, int group, int sms, int64_t *out) {
@@ -656,7 +658,7 @@ W4_API w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const 
         if (p && !aligned16(p)) return W4_ERR_ALIGN;
     const int sms = num_sms();
     const BwdLayout l = bwd_layout(M, H, K, sms);
-    if (!workspace || workspace_bytes < l.q.end) return W4_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < l.end) return W4_ERR_WORKSPACE;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     xg::Prep prep = {};
     prep.x[0] = static_cast<const __nv_bfloat16 *>(X_bf16);
@@ -666,9 +668,8 @@ W4_API w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const 
     prep.row_pow = reinterpret_cast<float *>(ws + l.q.row_pow);
     prep.M = M;
     prep.K = K;
-    prep.tensors = 1;
     prep.pairs = 1;
-    st = xg::launch_prep(prep, false, stream);
+    st = xg::launch_prep(prep, stream);
     if (st != W4_OK) return st;
     xg::Maps tm;
     xg::Args a = {};
@@ -681,6 +682,7 @@ W4_API w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const 
     a.dh = static_cast<const __nv_bfloat16 *>(dH_bf16);
     a.out = dG_bf16;
     a.out2 = static_cast<__nv_bfloat16 *>(dU_bf16);
+    a.rest = dX_bf16 ? reinterpret_cast<uint16_t *>(ws + l.q.end) : nullptr;
     a.row_pow = prep.row_pow;
     if (!xg::make_map(&tm.b[0], prep.y[0], M, K, l.grads.box)) return W4_ERR_CUDA;
     tm.b[1] = tm.b[0];
@@ -689,18 +691,18 @@ W4_API w4_status w4a16_gated_bwd(const void *dH_bf16, const void *X_bf16, const 
     if (st != W4_OK || !dX_bf16) return st;
     prep.x[0] = static_cast<const __nv_bfloat16 *>(dG_bf16);
     prep.x[1] = static_cast<const __nv_bfloat16 *>(dU_bf16);
+    prep.rest = a.rest;
     prep.x8 = prep.xs = nullptr;
     prep.y[1] = prep.y[0] + M * H;
     prep.K = H;
-    prep.tensors = 2;
-    prep.pairs = 0;
-    st = xg::launch_prep(prep, true, stream);
+    st = xg::launch_prep(prep, stream);
     if (st != W4_OK) return st;
     if (!xg::make_map(&tm.b[0], prep.y[0], M, H, l.dx.box) || !xg::make_map(&tm.b[1], prep.y[1], M, H, l.dx.box))
         return W4_ERR_CUDA;
     a.dh = nullptr;
     a.out = dX_bf16;
     a.out2 = nullptr;
+    a.rest = nullptr;
     return xg::launch<xg::DGRAD, false, false>(l.dx, tm, a, workspace, sms, stream);
 }
 
@@ -741,8 +743,7 @@ W4_API w4_status w4a16_dgrad(const void *dY_bf16, int64_t M, const uint8_t *code
     prep.row_pow = reinterpret_cast<float *>(ws + q.row_pow);
     prep.M = M;
     prep.K = N;
-    prep.tensors = 1;
-    st = xg::launch_prep(prep, false, stream);
+    st = xg::launch_prep(prep, stream);
     if (st != W4_OK) return st;
     xg::Args a = {};
     a.row_pow = prep.row_pow;

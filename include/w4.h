@@ -584,7 +584,8 @@ w4_status w4a16_gated(const void *X_bf16, int64_t M, const uint8_t *codes_gate, 
  *   dH_bf16      device, bf16 [M, H], the gradient of w4a16_gated's output
  *   X_bf16       device, bf16 [M, K], the forward's input; or NULL with the 8-bit checkpoint of it:
  *   X_e4m3, X_scale   device, fp8_ckpt_save's outputs for X; both NULL when X_bf16 is given
- *   dG_bf16, dU_bf16  device, bf16 [M, H], outputs (rounded once; dX is formed from the rounded ones)
+ *   dG_bf16, dU_bf16  device, bf16 [M, H], outputs (rounded once; dX is formed from them before
+ *                that, to the 11 bits of the fp16 rows that its product takes)
  *   dX_bf16      device, bf16 [M, K], output, or NULL where it is not wanted (a first layer)
  *   workspace    as w4a16_gated's, of w4a16_gated_bwd_workspace_bytes(M, H, K, group, from_ckpt) bytes
  *                (from_ckpt 1: X comes as the checkpoint; both sources ask for the same at

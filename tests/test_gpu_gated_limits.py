@@ -97,14 +97,15 @@ def test_most_features(M):
         d, p, q = dh[:, sl].double(), dg[:, sl].double(), du[:, sl].double()
         T.check_bwd([dg[:, sl], du[:, sl], None], x, dh[:, sl], a, b, G, "silu")
         a, b = R.dequant(a, G), R.dequant(b, G)
-        # dX from the gradients as they were rounded
+        # Of the gradients as they are rounded, which dX is not formed from: their roundings are independent, so
+        # these sums of random signs differ by 2^-8 / sqrt(3) of them in the mean at most
         rx, mx = rx + p @ a + q @ b, mx + p.abs() @ a.abs() + q.abs() @ b.abs()
         rx2, mx2 = rx2 + d @ a, mx2 + d.abs() @ a.abs()
     e = 2.0 ** -11 + 2.0 ** -12
     T.near(dx, rx, e * mx + R.HALF * rx.abs(), 1.0)
     T.near(dx2, rx2, e * mx2 + R.HALF * rx2.abs(), 1.0)
     # sums of random signs: the weights' roundings are off by 2^-11 of the result in the mean at most
-    assert R.rel(dx, rx) <= R.HALF + 2.0 ** -11 and R.rel(dx2, rx2) <= R.HALF + 2.0 ** -11
+    assert R.rel(dx, rx) <= R.HALF * (1 + 3 ** -0.5) + 2.0 ** -11 and R.rel(dx2, rx2) <= R.HALF + 2.0 ** -11
 
 
 @pytest.mark.parametrize("M", [1, 2, 5, 17, 300])
