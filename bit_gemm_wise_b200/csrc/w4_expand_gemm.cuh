@@ -29,7 +29,7 @@
 // 98% (DGRAD) and 94% (WGRAD) of a stage's 984, 903 and 836 cycles at N = 256 (192), of which the MMAs
 // take 512 (384). So where there are more than 128 columns, two CTAs make a pair: one MMA of both SMs
 // (M = 256) on 128 lanes of each, every SM holding half of B, which it writes and reads half as often
-// (803, 712 and, at N = 256, 766 cycles a stage). The first CTA of a pair issues the MMAs; the second one passes on that its stages
+// (797, 727 and, at N = 256, 760 cycles a stage). The first CTA of a pair issues the MMAs; the second one passes on that its stages
 // are full. Beyond that, instructions count: the codes' pairs (i, i + 4) of eight stay in that order, and
 // B's rows (FWD) or the results' lanes (DGRAD, WGRAD) are permuted instead; a thread's scale
 // addresses move by one addition. (Not kept: a table of FWD's scales made beforehand, side by side for a
@@ -1219,9 +1219,8 @@ struct Plan {
 // it joins (2^-25 of the sum's power of two), and the sum after each step. So R terms in one
 // accumulator lose up to R * 1.25 * 2^-25 of its largest partial sum, half of that where it grows
 // steadily (2^20 terms of one sign: up to 2e-2, measured 5.5e-3). An accumulator therefore sums 2^15
-// terms at most (6e-4, a sixth of bf16's rounding, measured 1e-4), and for fp32 results 2048 (operands of
-// N(0, 1) against a 64-bit product: 4e-7 over 910 rows, 2e-6 over 2048 and 9e-6 over 8192). Longer
-// units are added up outside, in fp32: in the partial sums of a split reduction, in fp32 results
+// terms at most (6e-4, a sixth of bf16's rounding, measured 1e-4), and for fp32 results 2048 (random
+// signs against a 64-bit product: 3e-7 over 1000 rows, 6e-7 from 2048 to 8192). Longer units are added up outside, in fp32: in the partial sums of a split reduction, in fp32 results
 // themselves, else in one tile's worth of sums for each CTA.
 inline Plan make_plan(int kind, int64_t lanes, int64_t cols, int64_t red, int sources, int sms, bool grads = false,
                       bool fp32 = false) {
@@ -1266,7 +1265,7 @@ inline Plan make_plan(int kind, int64_t lanes, int64_t cols, int64_t red, int so
         // parts of the reduction: what has the least estimated time, in cycles. One estimate serves all
         // products. A stage takes the shared memory's traffic (the codes, A and the scales, and two passes
         // of B, which a pair divides) or its MMAs: 916 at 256 columns, measured 984 (FWD) and 903 (DGRAD);
-        // in a pair 673, measured 803, 712 and 766 (WGRAD). A unit takes 7000 to start and end, 8500 in a
+        // in a pair 673, measured 797, 727 and 760 (WGRAD). A unit takes 7000 to start and end, 8500 in a
         // pair; the last part of a tile reads two partial sums of 16 columns in 1300 cycles, five groups of
         // columns at a time, after 1500 for the count.
         const int64_t tiles = p.Tw * p.Tn, workers = pair ? sms / 2 : sms;
