@@ -45,7 +45,7 @@ W4_API const char *w4_status_str(int status) {
     }
 }
 
-W4_API int w4_version(void) { return 101; }
+W4_API int w4_version(void) { return 102; }
 
 W4_API w4_status w4_device_status(cudaStream_t stream, int *code_out) {
     if (!code_out) return W4_ERR_NULL;

@@ -1220,8 +1220,9 @@ struct Plan {
 // accumulator lose up to R * 1.25 * 2^-25 of its largest partial sum, half of that where it grows
 // steadily (2^20 terms of one sign: up to 2e-2, measured 5.5e-3). An accumulator therefore sums 2^15
 // terms at most (6e-4, a sixth of bf16's rounding, measured 1e-4), and for fp32 results 2048 (random
-// signs against a 64-bit product: 3e-7 over 1000 rows, 6e-7 from 2048 to 8192). Longer units are added up outside, in fp32: in the partial sums of a split reduction, in fp32 results
-// themselves, else in one tile's worth of sums for each CTA.
+// signs against a 64-bit product: 3e-7 over 1000 rows, 6e-7 from 2048 to 8192). Longer units are added
+// up outside, in fp32: in the partial sums of a split reduction, in fp32 results themselves, else in one
+// tile's worth of sums for each CTA.
 inline Plan make_plan(int kind, int64_t lanes, int64_t cols, int64_t red, int sources, int sms, bool grads = false,
                       bool fp32 = false) {
     const int most = (fp32 ? 2048 : 1 << 15) / BK;
