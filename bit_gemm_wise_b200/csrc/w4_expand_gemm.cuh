@@ -29,12 +29,12 @@
 // 98% (DGRAD) and 94% (WGRAD) of a stage's 984, 903 and 836 cycles at N = 256 (192), of which the MMAs
 // take 512 (384). So where there are more than 128 columns, two CTAs make a pair: one MMA of both SMs
 // (M = 256) on 128 lanes of each, every SM holding half of B, which it writes and reads half as often
-// (797, 727 and, at N = 256, 760 cycles a stage). The first CTA of a pair issues the MMAs; the second one passes on that its stages
-// are full. Beyond that, instructions count: the codes' pairs (i, i + 4) of eight stay in that order, and
-// B's rows (FWD) or the results' lanes (DGRAD, WGRAD) are permuted instead; a thread's scale
-// addresses move by one addition. (Not kept: a table of FWD's scales made beforehand, side by side for a
-// stage, which loads them in a tenth of the accesses: no faster, and small calls pay for it; tiles
-// ordered so that neighbours share their codes in L2: no faster.)
+// (797, 727 and, at N = 256, 760 cycles a stage). The first CTA of a pair issues the MMAs; the second one
+// passes on that its stages are full. Beyond that, instructions count: the codes' pairs (i, i + 4) of
+// eight stay in that order, and B's rows (FWD) or the results' lanes (DGRAD, WGRAD) are permuted instead;
+// a thread's scale addresses move by one addition. (Not kept: a table of FWD's scales made beforehand,
+// side by side for a stage, which loads them in a tenth of the accesses: no faster, and small calls pay
+// for it; tiles ordered so that neighbours share their codes in L2: no faster.)
 //
 // Where the tiles are too few for the SMs, the reduction is cut into S parts: each part's fp32 sums
 // go to the workspace and the last part to finish adds them in order, so results do not depend on
